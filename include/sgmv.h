@@ -82,7 +82,8 @@ enum {
     SGMV_ERR_RANK_MISMATCH = -4,     /* inputs.shape[1] != lora_b.shape[-1] */
     SGMV_ERR_SLICE_SIZE = -5,        /* slice_size != lora_b.shape[-2] */
     SGMV_ERR_LAYOUT_4D = -6,         /* 4-D lora_b whose dimension 1 is not 1 */
-    SGMV_ERR_OUT_NOT_CONTIGUOUS = -7,/* out is not contiguous row-major */
+    SGMV_ERR_OUT_NOT_CONTIGUOUS = -7,/* out is not contiguous row-major (large products: no unit column stride,
+                                        or rows that overlap) */
     SGMV_ERR_SLICE_RANGE = -8,       /* slice_offset < 0 or slice_offset + slice_size > out.shape[1] */
     SGMV_ERR_BATCHES = -9,           /* batches < 0, or a metadata tensor shorter than batches */
     SGMV_ERR_SHAPE = -10,            /* a negative extent, or max_seq_len < 0 */
@@ -91,8 +92,10 @@ enum {
     SGMV_ERR_VARIANT = -13,          /* the forced kernel variant cannot run this call */
     SGMV_ERR_NUM_SLICES = -14,       /* num_slices outside [1, SGMV_MAX_SLICES] */
     SGMV_ERR_SLICE_OVERLAP = -15,    /* two non-empty slices of one call share a column */
-    SGMV_ERR_OUT_WIDTH = -16,        /* sgmv_expand / sgmv_shrink: out.shape[1] != lora_b/lora_a.shape[-2] */
-    SGMV_ERR_WORKSPACE = -17,        /* sgmv_shrink: workspace not 16-byte aligned */
+    SGMV_ERR_OUT_WIDTH = -16,        /* sgmv_expand / sgmv_shrink / the large products: out.shape[1] is not the
+                                        weights' row count */
+    SGMV_ERR_WORKSPACE = -17,        /* workspace not 16-byte aligned (sgmv_shrink, sgmv_lora_linear), or too small
+                                        (sgmv_lora_linear) */
     SGMV_ERR_SCRATCH = -18,          /* reserved (no entry point returns it) */
     SGMV_ERR_CUDA = -20,             /* a CUDA runtime call failed */
     SGMV_ERR_LAUNCH = -21            /* a kernel launch failed */
@@ -304,6 +307,127 @@ SGMV_API int sgmv_shrink_plan(const sgmv_tensor* inputs, const sgmv_tensor* lora
 SGMV_API int bgmv_plan(const sgmv_tensor* inputs, const sgmv_tensor* lora_b, const sgmv_tensor* out,
               const sgmv_tensor* lora_idx, int64_t batches, int64_t slice_offset, int64_t slice_size,
               int add_inputs, int* variant);
+
+/*
+ * sgmv_lora_linear -- a shared projection with the low-rank adapters of many
+ * requests beside it, in one pass over out:
+ *
+ *     out[r, n] = sum_k x^[r, k] * W[n, k] + bias[n] + sum_j t[r, j] * B[a][n, j]
+ *     t[r, j]   = sum_k x^[r, k] * A[a][j, k]
+ *
+ * for EVERY row r < min(T_x, T_out); a is the adapter of the segment that holds
+ * row r, and rows of no segment, or of one whose adapter is outside
+ * [0, lora_num), get the projection and the bias alone.  t is kept in fp32 and
+ * not rounded; all sums are in fp32, and out is rounded once.  (Shrink, a
+ * library GEMM and expand in add mode give the same up to two more roundings.)
+ * out is overwritten; rows past min(T_x, T_out) keep their bits.  Segments must
+ * not overlap.
+ *
+ *   inputs    (T_x, K)          f16 | bf16 | f32, any strides
+ *   weight    (N, K)            f16 | bf16, any strides
+ *   bias      (N) or NULL       weight's dtype, any stride
+ *   lora_a    (lora_num, R, K) or (lora_num, 1, R, K)   weight's dtype, any strides
+ *   lora_b    (lora_num, N, R) or (lora_num, 1, N, R)   weight's dtype, any strides
+ *   out       (T_out, N)        f16 | bf16 | f32, unit column stride, any row
+ *             stride >= N (a column range of a wider tensor will do); must not
+ *             overlap any input
+ *   workspace DEVICE scratch, 16-byte aligned, owned by the caller and used only
+ *             by the work this call enqueues; nothing in it needs a value.  At
+ *             least the size that sgmv_lora_linear_plan reports (the rows'
+ *             adapters and t: about T * (R + 1) * 4 bytes), else
+ *             SGMV_ERR_WORKSPACE; with the preferred size the sums of t may be
+ *             split over more CTAs.  NULL will do for a call without adapters
+ *             (batches, lora_num or R zero).  Calls that run at the same time
+ *             need separate workspaces, and so do captured graphs that may.
+ *
+ * Statuses beside the common ones: SGMV_ERR_RANK_MISMATCH (K or R differ
+ * between tensors), SGMV_ERR_SLICE_SIZE (lora_b's N), SGMV_ERR_SHAPE (bias
+ * length, lora_a's and lora_b's lora_num), SGMV_ERR_OUT_WIDTH.
+ *
+ * The tensor-core path (SGMV_VARIANT_TC) needs inputs and weight in one half
+ * dtype, K contiguous in inputs, K or N contiguous in weight, and their rows on
+ * 16-byte boundaries; other calls run generic CUDA-core kernels.
+ */
+SGMV_API int sgmv_lora_linear(const sgmv_tensor* inputs, const sgmv_tensor* weight, const sgmv_tensor* bias,
+                     const sgmv_tensor* lora_a, const sgmv_tensor* lora_b, const sgmv_tensor* out,
+                     const sgmv_tensor* seq_start, const sgmv_tensor* seq_len, const sgmv_tensor* lora_idx,
+                     int64_t batches, int64_t max_seq_len, void* workspace, size_t workspace_bytes, void* stream);
+
+/* sgmv_lora_linear_plan -- validate as sgmv_lora_linear does (without a
+ * workspace) and report the variant a call would launch (0: nothing), the
+ * workspace bytes it needs and the bytes it would like.  Launches nothing. */
+SGMV_API int sgmv_lora_linear_plan(const sgmv_tensor* inputs, const sgmv_tensor* weight, const sgmv_tensor* bias,
+                          const sgmv_tensor* lora_a, const sgmv_tensor* lora_b, const sgmv_tensor* out,
+                          const sgmv_tensor* seq_start, const sgmv_tensor* seq_len, const sgmv_tensor* lora_idx,
+                          int64_t batches, int64_t max_seq_len, int* variant, size_t* workspace_bytes,
+                          size_t* preferred_workspace_bytes);
+
+/*
+ * sgmv_grouped_gemm -- matrix products grouped by expert with ragged sizes:
+ *
+ *     out[r, n] = (add_inputs ? out[r, n] : 0) + sum_k x^[r, k] * W[e][n, k]
+ *
+ * for the rows r of every segment, e = group_idx[b].  The formula, guards and
+ * metadata are sgmv_expand's with experts in the adapters' place; this entry
+ * point is made for full-size weights (any K on the tensor cores) and for
+ * both directions:
+ *
+ *   weights   (E, N, K) or (E, 1, N, K)   f16 | bf16, any strides.  Either K or N
+ *             may be the contiguous axis on the tensor-core path: the input
+ *             gradient dX = dY W of weights (E, O, I) is this product with
+ *             weights transposed to (E, I, O) as a view
+ *   inputs    (T_x, K)      f16 | bf16 | f32, any strides
+ *   out       (T_out, N)    f16 | bf16 | f32, unit column stride, any row stride
+ *             >= N; must not overlap any input.  Rows of no segment keep their bits
+ *
+ * Several segments may share an expert; segments must not overlap.  Sums are
+ * in fp32, one rounding.  Tensor-core path: as sgmv_lora_linear's, rows of
+ * inputs and weights (and the experts) on 16-byte boundaries, at most 4096
+ * segments.  max_seq_len is not used.
+ */
+SGMV_API int sgmv_grouped_gemm(const sgmv_tensor* inputs, const sgmv_tensor* weights, const sgmv_tensor* out,
+                      const sgmv_tensor* seq_start, const sgmv_tensor* seq_len, const sgmv_tensor* group_idx,
+                      int64_t batches, int64_t max_seq_len, int add_inputs, void* stream);
+
+/* sgmv_grouped_gemm_plan -- validate as sgmv_grouped_gemm does; *variant
+ * receives the variant a call would launch (0: nothing).  Launches nothing. */
+SGMV_API int sgmv_grouped_gemm_plan(const sgmv_tensor* inputs, const sgmv_tensor* weights, const sgmv_tensor* out,
+                           const sgmv_tensor* seq_start, const sgmv_tensor* seq_len, const sgmv_tensor* group_idx,
+                           int64_t batches, int64_t max_seq_len, int add_inputs, int* variant);
+
+/*
+ * sgmv_grouped_wgrad -- the weight gradient of the segmented products:
+ *
+ *     dW[e][n, k] = (add_inputs ? dW[e][n, k] : 0) + sum over b with group_idx[b] = e,
+ *                                                    rows r of segment b:  dY[r, n] * X[r, k]
+ *
+ * for EVERY e < E: without add_inputs an index that no row has gets zeros; with
+ * it, it keeps its bits.  Of sgmv_grouped_gemm it is the gradient by the
+ * weights; with X = t it is that of lora_b, with dY = dt that of lora_a.
+ *
+ *   grad_out      (T_y, N)     f16 | bf16 | f32, any strides
+ *   inputs        (T_x, K)     f16 | bf16 | f32, any strides
+ *   grad_weights  (E, N, K) or (E, 1, N, K)   f16 | bf16 | f32, unit stride along
+ *                 K, rows and indexes that do not overlap (else
+ *                 SGMV_ERR_OUT_NOT_CONTIGUOUS); must not overlap any input
+ *
+ * Rows at or beyond T_x or T_y are skipped, what they hold (NaN, infinities)
+ * never reaches dW.  Segments of one index add up in segment order; each sum is
+ * taken in fp32 (on the tensor cores the adder truncates, which over T rows
+ * leaves a relative error of about T * 1e-9) and rounded once.  Tensor-core path: grad_out
+ * and inputs in one half dtype, unit column strides, rows on 16-byte boundaries,
+ * dW's expert stride a multiple of its row stride.  max_seq_len is not used.
+ */
+SGMV_API int sgmv_grouped_wgrad(const sgmv_tensor* grad_out, const sgmv_tensor* inputs, const sgmv_tensor* grad_weights,
+                       const sgmv_tensor* seq_start, const sgmv_tensor* seq_len, const sgmv_tensor* group_idx,
+                       int64_t batches, int64_t max_seq_len, int add_inputs, void* stream);
+
+/* sgmv_grouped_wgrad_plan -- validate as sgmv_grouped_wgrad does; *variant
+ * receives the variant a call would launch (0: nothing).  Launches nothing. */
+SGMV_API int sgmv_grouped_wgrad_plan(const sgmv_tensor* grad_out, const sgmv_tensor* inputs,
+                            const sgmv_tensor* grad_weights, const sgmv_tensor* seq_start, const sgmv_tensor* seq_len,
+                            const sgmv_tensor* group_idx, int64_t batches, int64_t max_seq_len, int add_inputs,
+                            int* variant);
 
 /*
  * sgmv_validate_metadata -- check the VALUES of the metadata on the device and

@@ -23,6 +23,12 @@ output row is the slice), and ``bgmv_expand_slice`` its fixed-length
 counterpart with one token per row (both named in the page's Description).
 ``sgmv_shrink`` is the LoRA-A projection that produces the expand's input
 (I/O Contract, inputs).
+
+The large products beside them: ``sgmv_lora_linear`` is a whole shared
+projection with the adapters of many requests, ``sgmv_grouped_gemm`` multiplies
+the rows of every segment by its expert's full-size weights (or, with the
+weights seen transposed, computes the input gradient), and
+``sgmv_grouped_wgrad`` is the gradient by the weights.
 """
 import ctypes
 
@@ -31,7 +37,8 @@ import torch
 from . import _abi
 
 __all__ = ["sgmv_expand_slice", "sgmv_expand_multi_slice", "sgmv_expand", "bgmv_expand_slice", "sgmv_shrink",
-           "shrink_plan", "plan",
+           "shrink_plan", "plan", "sgmv_lora_linear", "lora_linear_plan", "sgmv_grouped_gemm", "grouped_gemm_plan",
+           "sgmv_grouped_wgrad", "grouped_wgrad_plan",
            "plan_multi_slice", "bgmv_plan", "validate_metadata", "set_variant", "device_error", "SgmvError",
            "VARIANT_AUTO", "VARIANT_SIMT", "VARIANT_TC", "VARIANT_DECODE", "VARIANT_TC_WIDE", "library_path"]
 
@@ -241,6 +248,99 @@ def plan(inputs, lora_b_weights, output_tensor, b_seq_start_loc, seq_len_tensor,
     if rc != 0:
         raise SgmvError(rc, "sgmv_plan")
     return v.value
+
+
+def _lora_args(inputs, weight, lora_a_weights, lora_b_weights, output_tensor, meta, bias):
+    d = _args(inputs, weight, output_tensor, *meta)
+    for t in (lora_a_weights, lora_b_weights) + (() if bias is None else (bias,)):
+        if not t.is_cuda or t.device != output_tensor.device:
+            raise ValueError("all tensors must be CUDA tensors on the same device")
+    x, w, out, s, l, idx = [ctypes.byref(v) for v in d]
+    return (x, w, None if bias is None else ctypes.byref(_desc(bias)), ctypes.byref(_desc(lora_a_weights)),
+            ctypes.byref(_desc(lora_b_weights)), out, s, l, idx)
+
+
+def sgmv_lora_linear(inputs, weight, lora_a_weights, lora_b_weights, output_tensor, b_seq_start_loc, seq_len_tensor,
+                     lora_indices_tensor, batches, max_seq_length, bias=None, workspace=None):
+    """``output_tensor[r] = inputs[r] @ weight.T + bias + (inputs[r] @ A.T) @ B.T`` with the adapter (A, B) of row r's
+    sequence; rows without one get the projection alone.  Every row is written.  ``workspace``: contiguous CUDA tensor
+    of scratch of at least ``lora_linear_plan``'s first size (None only without adapters)."""
+    d = _lora_args(inputs, weight, lora_a_weights, lora_b_weights, output_tensor,
+                   (b_seq_start_loc, seq_len_tensor, lora_indices_tensor), bias)
+    wp, wb = _ws(workspace)
+    if workspace is not None and workspace.device != output_tensor.device:
+        raise ValueError("all tensors must be CUDA tensors on the same device")
+    with torch.cuda.device(output_tensor.device):
+        rc = _lib.sgmv_lora_linear(*d, int(batches), int(max_seq_length), wp, wb, _stream_handle(output_tensor.device))
+    if rc != 0:
+        raise SgmvError(rc, "sgmv_lora_linear")
+    return output_tensor
+
+
+def lora_linear_plan(inputs, weight, lora_a_weights, lora_b_weights, output_tensor, b_seq_start_loc, seq_len_tensor,
+                     lora_indices_tensor, batches, max_seq_length, bias=None):
+    """(variant, workspace bytes needed, workspace bytes preferred) of a lora_linear call."""
+    d = _lora_args(inputs, weight, lora_a_weights, lora_b_weights, output_tensor,
+                   (b_seq_start_loc, seq_len_tensor, lora_indices_tensor), bias)
+    v, need, pref = ctypes.c_int(0), ctypes.c_size_t(0), ctypes.c_size_t(0)
+    with torch.cuda.device(output_tensor.device):
+        rc = _lib.sgmv_lora_linear_plan(*d, int(batches), int(max_seq_length), ctypes.byref(v), ctypes.byref(need),
+                                        ctypes.byref(pref))
+    if rc != 0:
+        raise SgmvError(rc, "sgmv_lora_linear_plan")
+    return v.value, need.value, pref.value
+
+
+def _grouped(name, a, b, c, meta, batches, max_seq_length, add_inputs):
+    d = _args(a, b, c, *meta)
+    with torch.cuda.device(c.device):
+        rc = getattr(_lib, name)(*[ctypes.byref(x) for x in d], int(batches), int(max_seq_length),
+                                 int(bool(add_inputs)), _stream_handle(c.device))
+    if rc != 0:
+        raise SgmvError(rc, name)
+    return c
+
+
+def _grouped_plan(name, a, b, c, meta, batches, max_seq_length, add_inputs):
+    d = _args(a, b, c, *meta)
+    v = ctypes.c_int(0)
+    with torch.cuda.device(c.device):
+        rc = getattr(_lib, name)(*[ctypes.byref(x) for x in d], int(batches), int(max_seq_length),
+                                 int(bool(add_inputs)), ctypes.byref(v))
+    if rc != 0:
+        raise SgmvError(rc, name)
+    return v.value
+
+
+def sgmv_grouped_gemm(inputs, weights, output_tensor, b_seq_start_loc, seq_len_tensor, group_indices_tensor, batches,
+                      max_seq_length, add_inputs=False):
+    """``output_tensor[r] = inputs[r] @ weights[e].T`` (added to the old values when ``add_inputs``) for the rows of
+    every segment with index e; other rows keep their bits.  ``weights`` is (E, N, K) with K or N contiguous: pass
+    ``w.transpose(1, 2)`` for the input gradient."""
+    return _grouped("sgmv_grouped_gemm", inputs, weights, output_tensor,
+                    (b_seq_start_loc, seq_len_tensor, group_indices_tensor), batches, max_seq_length, add_inputs)
+
+
+def grouped_gemm_plan(inputs, weights, output_tensor, b_seq_start_loc, seq_len_tensor, group_indices_tensor, batches,
+                      max_seq_length, add_inputs=False) -> int:
+    """Kernel variant a sgmv_grouped_gemm call with these arguments would launch (0 = none)."""
+    return _grouped_plan("sgmv_grouped_gemm_plan", inputs, weights, output_tensor,
+                         (b_seq_start_loc, seq_len_tensor, group_indices_tensor), batches, max_seq_length, add_inputs)
+
+
+def sgmv_grouped_wgrad(grad_output, inputs, grad_weights, b_seq_start_loc, seq_len_tensor, group_indices_tensor,
+                       batches, max_seq_length, add_inputs=False):
+    """``grad_weights[e] = grad_output[rows of e].T @ inputs[rows of e]`` (added to the old values when
+    ``add_inputs``) for every index e; an index without rows gets zeros (keeps its values when ``add_inputs``)."""
+    return _grouped("sgmv_grouped_wgrad", grad_output, inputs, grad_weights,
+                    (b_seq_start_loc, seq_len_tensor, group_indices_tensor), batches, max_seq_length, add_inputs)
+
+
+def grouped_wgrad_plan(grad_output, inputs, grad_weights, b_seq_start_loc, seq_len_tensor, group_indices_tensor,
+                       batches, max_seq_length, add_inputs=False) -> int:
+    """Kernel variant a sgmv_grouped_wgrad call with these arguments would launch (0 = none)."""
+    return _grouped_plan("sgmv_grouped_wgrad_plan", grad_output, inputs, grad_weights,
+                         (b_seq_start_loc, seq_len_tensor, group_indices_tensor), batches, max_seq_length, add_inputs)
 
 
 def validate_metadata(b_seq_start_loc, seq_len_tensor, lora_indices_tensor, batches, lora_num,

@@ -84,6 +84,16 @@ def load():
     lib.sgmv_shrink_plan.restype = i32
     lib.sgmv_shrink_plan.argtypes = [P, P, P, P, P, P, i64, i64, sz, ctypes.POINTER(i32), ctypes.POINTER(i32),
                                      ctypes.POINTER(sz)]
+    lib.sgmv_lora_linear.restype = i32
+    lib.sgmv_lora_linear.argtypes = [P, P, P, P, P, P, P, P, P, i64, i64, vp, sz, vp]
+    lib.sgmv_lora_linear_plan.restype = i32
+    lib.sgmv_lora_linear_plan.argtypes = [P, P, P, P, P, P, P, P, P, i64, i64, ctypes.POINTER(i32),
+                                          ctypes.POINTER(sz), ctypes.POINTER(sz)]
+    for name in ("sgmv_grouped_gemm", "sgmv_grouped_wgrad"):
+        fn, plan = getattr(lib, name), getattr(lib, name + "_plan")
+        fn.restype = plan.restype = i32
+        fn.argtypes = [P, P, P, P, P, P, i64, i64, i32, vp]
+        plan.argtypes = [P, P, P, P, P, P, i64, i64, i32, ctypes.POINTER(i32)]
     lib.sgmv_validate_metadata.restype = i32
     lib.sgmv_validate_metadata.argtypes = [P, P, P, i64, i64, i64, vp, vp]
     lib.sgmv_status_string.restype = ctypes.c_char_p

@@ -1,0 +1,678 @@
+// Large segmented products on the tensor cores: rows grouped by expert times
+// the expert's weights, and a shared projection with low-rank adapters.
+//
+//     out[r, n] = (add ? out[r, n] : 0) + sum_k x[r, k] * W[e][n, k]          (r in a segment with index e)
+//     out[r, n] = sum_k x[r, k] * W[n, k] + bias[n] + sum_j t[r, j] * B[a(r)][n, j]
+//
+// The product is computed turned round: the MMA's M axis are weight rows, its
+// N axis are tokens.  M is fixed by the hardware (128, or 256 for a CTA pair),
+// N is any multiple of 16 (32) up to 256, so a ragged segment costs only its
+// own rows rounded up to that, and a decode batch streams its weights through
+// the wide side of the MMA.  A segment of L rows is cut into ceil(L / tn)
+// token tiles of equal size (rounded up), not into full tiles and a rest.
+//
+// Roles (320 threads per CTA): warp 0 loads with TMA (x rows in boxes of 16 to
+// 128 rows, weights 128 rows, 64 columns of K per stage, 128-byte swizzle),
+// warp 1 issues the MMAs into one of two TMEM accumulators, warps 2-9 read the
+// other accumulator back (lane = weight row, column = token), finish the sums
+// and store; 32 lanes store 32 neighbouring columns of a row.
+// Rows of a load past the segment's end are other segments' rows or zeros:
+// they only reach accumulator columns that are not stored.
+//
+// Two forms, picked by a cost model on the host (choose_shape):
+//   pair   CTA pairs (cta_group::2), 256 weight rows x up to 256 tokens.  Each
+//          CTA loads its 128 weight rows and half of the tokens, so a stage
+//          brings 64 MMA columns per KB instead of 43: compute-bound shapes.
+//   single one CTA, 128 weight rows x up to 128 tokens; with few tiles, the
+//          CTAs of a cluster share one tile by cutting K, push their partial
+//          sums into each other's shared memory (every CTA owns a part of the
+//          tokens) and add them in rank order (deterministic): decode shapes.
+//
+// Every wait is bounded and reports a timeout through the device error word.
+#pragma once
+
+#include <cuda.h>
+
+#include "common.cuh"
+#include "plan_cache.cuh"
+#include "tc_ptx.cuh"
+
+namespace sgmv {
+namespace grp {
+
+using namespace sgmv::tc;
+
+constexpr int BK = 64;                  // K columns per stage: 128-byte rows
+constexpr int WROWS = 128;              // weight rows per CTA
+constexpr int W_TILE = WROWS * BK * 2;  // 16 KB
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int NUM_XMAPS = 4;            // x boxes of 16, 32, 64, 128 rows
+constexpr int MAX_SPLITS = 8;
+constexpr int BAND = 8;                 // token tiles walked together before the next weight tile
+constexpr int SEG_CAP = 4096;           // most segments a launch takes
+constexpr int SMEM_LIMIT = 232448 - 1024;
+
+struct Seg {
+    int32_t row0, rows, group;
+    int32_t ts;       // tokens per tile (the last tile of the segment may own fewer rows)
+    int32_t prefix;   // token tiles of earlier segments
+};
+
+struct Geo {
+    int32_t nblk, kblocks;
+    int32_t tn;           // most tokens per tile
+    int32_t splits;       // CTAs that share a tile by cutting K (single form)
+    int32_t stages, stage_bytes;
+    int32_t off_red, off_seg, off_bar;
+    int32_t acc_stride, tmem_cols;
+    int32_t w_mn;         // the weights' N axis is the contiguous one
+    int32_t dense_rows;   // >= 0: one segment of that many rows with group 0; -1: the call's segments
+    int32_t early;        // the preceding kernel is the adapters' shrink, which writes neither x nor weights
+    int32_t keep_w;       // weights are read by several token tiles: keep them in L2
+};
+
+struct XMaps {
+    CUtensorMap m[NUM_XMAPS];
+};
+
+// The low-rank part and the bias of a shared projection.
+struct Lora {
+    const float* t;              // (rows, R) fp32: x A^T
+    const int32_t* row_adapter;  // (rows): adapter, -1 for none
+    const void* b;               // (adapters, N, R), the weights' dtype
+    int64_t b_as, b_ns, b_ks;
+    int32_t R;
+    int32_t b_vec;               // rows of B can be read as 16-byte pieces
+    const void* bias;            // (N) in the weights' dtype, or null
+    int64_t bias_s;
+};
+
+struct Tile {
+    int32_t row0, rows, ts, n0, group;
+};
+
+__device__ __forceinline__ void decode_tile(const Seg* segs, int32_t nseg, const Geo& g, int32_t id, int32_t wtile,
+                                            Tile& t) {
+    const int32_t key = id / g.nblk;
+    int lo = 0, hi = nseg - 1;   // last segment whose prefix <= key (empty ones share their successor's)
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (segs[mid].prefix <= key) lo = mid;
+        else hi = mid - 1;
+    }
+    const Seg s = segs[lo];
+    const int32_t nt = (s.rows + s.ts - 1) / s.ts;
+    // bands of BAND token tiles; within a band the token tile is fastest, so the
+    // CTAs at work share few weight tiles and few x tiles
+    const int32_t local = id - s.prefix * g.nblk;
+    const int32_t band = local / (BAND * g.nblk);
+    const int32_t in_band = min(BAND, nt - band * BAND);
+    const int32_t r = local - band * BAND * g.nblk;
+    const int32_t tok = band * BAND + r % in_band;
+    t.n0 = (r / in_band) * wtile;
+    t.row0 = s.row0 + tok * s.ts;
+    t.rows = min(s.ts, s.rows - tok * s.ts);
+    t.ts = s.ts;
+    t.group = s.group;
+}
+
+// v[j] += sum_k t[row + j, k] * B[adapter of row + j][n, k] for j < valid, in
+// fp32, 16 ranks at a time: B's piece of the lane's column stays in registers
+// while neighbouring tokens share an adapter, t is one broadcast read per warp.
+template <int NT>
+__device__ __forceinline__ void add_lora(float (&v)[NT], int64_t row, int valid, int64_t n, bool n_ok, const Lora& lo,
+                                         bool bf16) {
+    for (int r0 = 0; r0 < lo.R; r0 += 16) {
+        int cur = -1;
+        float b[16];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            if (j >= valid) continue;
+            const int a = lo.row_adapter[row + j];
+            if (a < 0) continue;
+            if (a != cur) {
+                cur = a;
+                const int64_t base = (int64_t)a * lo.b_as + n * lo.b_ns;
+                if (!n_ok) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) b[k] = 0.f;
+                } else if (lo.b_vec && r0 + 16 <= lo.R) {
+                    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(lo.b) + base + r0);
+                    const uint4 u0 = __ldg(q), u1 = __ldg(q + 1);
+                    const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float2 f = unpack2(w[k], bf16);
+                        b[2 * k] = f.x;
+                        b[2 * k + 1] = f.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        b[k] = r0 + k < lo.R
+                                   ? half_bits_to_float(__ldg(static_cast<const uint16_t*>(lo.b) + base +
+                                                              (int64_t)(r0 + k) * lo.b_ks),
+                                                        bf16)
+                                   : 0.f;
+                }
+            }
+            const float* tp = lo.t + (row + j) * lo.R + r0;
+            float s0 = 0.f, s1 = 0.f;
+            if (lo.R % 16 == 0) {
+#pragma unroll
+                for (int k = 0; k < 16; k += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(tp + k);
+                    s0 = fmaf(f.x, b[k], s0);
+                    s1 = fmaf(f.y, b[k + 1], s1);
+                    s0 = fmaf(f.z, b[k + 2], s0);
+                    s1 = fmaf(f.w, b[k + 3], s1);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (r0 + k < lo.R) s0 = fmaf(tp[k], b[k], s0);
+            }
+            v[j] += s0 + s1;
+        }
+    }
+}
+
+// Adds the low-rank part, the bias or the old output, rounds once and stores
+// rows row .. row + valid - 1 of column n.
+template <int NT, bool LORA>
+__device__ __forceinline__ void finish(float (&v)[NT], int64_t row, int valid, int64_t n, bool n_ok, float bias,
+                                       const Problem& p, const Lora& lo, bool bf16) {
+    if (valid <= 0) return;
+    if (LORA) {
+        if (lo.R > 0) add_lora<NT>(v, row, valid, n, n_ok, lo, bf16);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) v[j] += bias;
+    }
+    if (!n_ok) return;
+    const int64_t base = row * p.H + p.off + n;
+    if (p.out_dt == SGMV_F32) {
+        float* o = static_cast<float*>(p.out) + base;
+        if (p.add) {
+            float old[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) old[j] = j < valid ? o[j * p.H] : 0.f;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) v[j] += old[j];
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            if (j < valid) o[j * p.H] = v[j];
+    } else {
+        const bool ob = p.out_dt == SGMV_BF16;
+        uint16_t* o = static_cast<uint16_t*>(p.out) + base;
+        if (p.add) {
+            uint16_t old[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) old[j] = j < valid ? o[j * p.H] : (uint16_t)0;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) v[j] += half_bits_to_float(old[j], ob);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            if (j < valid) o[j * p.H] = (uint16_t)float_to_half_bits(v[j], ob);
+    }
+}
+
+template <int CG, bool LORA>
+__global__ void __launch_bounds__(THREADS, 1)
+gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtensorMap wmap, const Problem p, const Geo g,
+            const Lora lo) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ int s_abort;
+    __shared__ uint32_t s_tmem_base;
+    __shared__ int32_t s_token_tiles;
+
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const uint32_t csize = CG == 2 ? 2u : (uint32_t)g.splits;
+    const uint32_t crank = csize > 1 ? cluster_rank() : 0u;
+    const int32_t cid = (int32_t)(blockIdx.x / csize), ncl = (int32_t)(gridDim.x / csize);
+    const uint32_t S = (uint32_t)g.stages;
+    Seg* segs = reinterpret_cast<Seg*>(smem + g.off_seg);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + g.off_bar);
+    uint64_t* empty = full + S;
+    uint64_t* acc_full = empty + S;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* red_full = acc_empty + 2;
+    uint64_t* red_free = red_full + 1;
+
+    if (tid == 0) {
+        s_abort = 0;
+        for (uint32_t i = 0; i < S; ++i) {
+            mbar_init(smem_u32(&full[i]), CG);   // each CTA of a pair announces its own bytes
+            mbar_init(smem_u32(&empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&acc_full[i]), 1);
+            mbar_init(smem_u32(&acc_empty[i]), CG * EPI_WARPS);
+        }
+        mbar_init(smem_u32(red_full), csize * EPI_WARPS);
+        mbar_init(smem_u32(red_free), csize * EPI_WARPS);
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        for (int k = 0; k < NUM_XMAPS; ++k) prefetch_tmap(&xmaps.m[k]);
+        prefetch_tmap(&wmap);
+    }
+    if (warp == 1) {
+        if (CG == 2) tmem_alloc_pair(smem_u32(&s_tmem_base), (uint32_t)g.tmem_cols);
+        else tmem_alloc(smem_u32(&s_tmem_base), (uint32_t)g.tmem_cols);
+    }
+
+    // Everything below may read memory written by the preceding kernel, unless
+    // that is the adapters' shrink: then only the epilogue waits for it.
+    if (!g.early) {
+        grid_dependency_wait();
+        grid_dependents_launch();
+    }
+
+    // Segment table (guards of sgmv.h applied), tile size and tiles of earlier segments.
+    const int32_t nseg = g.dense_rows >= 0 ? 1 : (int32_t)p.batches;
+    constexpr int32_t STEP = 16 * CG;
+    for (int32_t b = tid; b < nseg; b += THREADS) {
+        Segment s;
+        if (g.dense_rows >= 0) s = Segment{0, g.dense_rows, 0};
+        else s = load_segment(p, b);
+        const int32_t rows = (int32_t)s.rows;
+        const int32_t nt = (rows + g.tn - 1) / g.tn;
+        const int32_t ts = nt > 0 ? ((rows + nt - 1) / nt + STEP - 1) / STEP * STEP : STEP;
+        segs[b] = Seg{(int32_t)s.row0, rows, (int32_t)s.adapter, ts, 0};
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int32_t run = 0;
+        for (int32_t base = 0; base < nseg; base += 32) {
+            const int32_t b = base + lane;
+            const int32_t nt = b < nseg ? (segs[b].rows + segs[b].ts - 1) / segs[b].ts : 0;
+            int32_t v = nt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t t = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += t;
+            }
+            if (b < nseg) segs[b].prefix = run + v - nt;
+            run += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) s_token_tiles = run;
+    }
+    tc_fence_before();
+    if (csize > 1) cluster_sync();   // the barriers of the other CTAs are ready too
+    __syncthreads();
+    tc_fence_after();
+
+    const uint32_t tmem_base = s_tmem_base;
+    const int32_t total = s_token_tiles * g.nblk;
+    volatile int* abort_flag = &s_abort;
+    const bool bf16 = p.w_dt == SGMV_BF16;
+    constexpr int32_t WT = WROWS * CG;
+    const int32_t kb0 = CG == 2 ? 0 : (int32_t)((int64_t)g.kblocks * crank / csize);
+    const int32_t kb1 = CG == 2 ? g.kblocks : (int32_t)((int64_t)g.kblocks * (crank + 1) / csize);
+    Tile t;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            const uint64_t pol_x = policy_evict_normal();
+            const uint64_t pol_w = g.keep_w ? policy_evict_normal() : policy_evict_first();
+            uint32_t q = 0;
+            bool ok = true;
+            for (int32_t id = cid; ok && id < total; id += ncl) {
+                decode_tile(segs, nseg, g, id, WT, t);
+                const int32_t hs = t.ts / CG;   // token rows of this CTA
+                const int lvl = hs <= 16 ? 0 : hs <= 32 ? 1 : hs <= 64 ? 2 : 3;
+                const uint32_t bytes = W_TILE + (16u << lvl) * 128u;
+                const int32_t xr = t.row0 + (CG == 2 ? (int32_t)crank * hs : 0);
+                const int32_t n0 = t.n0 + (CG == 2 ? (int32_t)crank * WROWS : 0);
+                for (int32_t kb = kb0; kb < kb1; ++kb, ++q) {
+                    const uint32_t s = q % S;
+                    if (!mbar_wait(smem_u32(&empty[s]), ((q / S) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_PRODUCER)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t ws = smem_u32(smem + s * g.stage_bytes), xs = ws + W_TILE;
+                    if (CG == 2) {
+                        const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
+                        mbar_expect_tx_cluster(bar, bytes);
+                        if (g.w_mn) {
+                            tma_load_3d_pair(ws, &wmap, n0, kb * BK, t.group, bar, pol_w);
+                            tma_load_3d_pair(ws + W_TILE / 2, &wmap, n0 + 64, kb * BK, t.group, bar, pol_w);
+                        } else {
+                            tma_load_3d_pair(ws, &wmap, kb * BK, n0, t.group, bar, pol_w);
+                        }
+                        tma_load_2d_pair(xs, &xmaps.m[lvl], kb * BK, xr, bar, pol_x);
+                    } else {
+                        const uint32_t bar = smem_u32(&full[s]);
+                        mbar_expect_tx(bar, bytes);
+                        if (g.w_mn) {
+                            tma_load_3d(ws, &wmap, n0, kb * BK, t.group, bar, pol_w);
+                            tma_load_3d(ws + W_TILE / 2, &wmap, n0 + 64, kb * BK, t.group, bar, pol_w);
+                        } else {
+                            tma_load_3d(ws, &wmap, kb * BK, n0, t.group, bar, pol_w);
+                        }
+                        tma_load_2d(xs, &xmaps.m[lvl], kb * BK, xr, bar, pol_x);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA (the pair's first CTA)
+        if (CG == 1 || crank == 0) {
+            uint32_t q = 0, n = 0;
+            bool ok = true;
+            // K step of 16 inside a stage: 32 bytes along a K-major row, 16 rows of an N-major tile
+            const uint64_t w_step = (uint64_t)((g.w_mn ? 16 * 128 : 32) >> 4);
+            for (int32_t id = cid; ok && id < total; id += ncl, ++n) {
+                decode_tile(segs, nseg, g, id, WT, t);
+                const uint32_t acc = n & 1;
+                const uint32_t idesc = instr_desc_mn(bf16, WT, t.ts) | (g.w_mn ? IDESC_A_MN : 0u);
+                const uint32_t d = tmem_base + acc * (uint32_t)g.acc_stride;
+                if (!warp_wait(smem_u32(&acc_empty[acc]), ((n >> 1) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_MMA)) break;
+                tc_fence_after();
+                for (int32_t kb = kb0; kb < kb1; ++kb, ++q) {
+                    const uint32_t s = q % S;
+                    if (!warp_wait(smem_u32(&full[s]), (q / S) & 1, abort_flag, DEVERR_TIMEOUT_MMA)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t ws = smem_u32(smem + s * g.stage_bytes);
+                        const uint64_t ad = smem_desc(ws, g.w_mn ? W_TILE / 2 : 16, 1024, 2);
+                        const uint64_t bd = smem_desc(ws + W_TILE, 16, 1024, 2);
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk) {
+                            if (CG == 2)
+                                tc_mma_pair(d, ad + kk * w_step, bd + kk * 2, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+                            else
+                                tc_mma(d, ad + kk * w_step, bd + kk * 2, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+                        }
+                        if (CG == 2) tc_commit_pair(smem_u32(&empty[s]));
+                        else tc_commit(smem_u32(&empty[s]));
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (lane == 0) {
+                    if (CG == 2) tc_commit_pair(smem_u32(&acc_full[acc]));
+                    else tc_commit(smem_u32(&acc_full[acc]));
+                }
+                __syncwarp();
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        if (g.early) {
+            grid_dependency_wait();   // t and the rows' adapters; nothing was written before
+            grid_dependents_launch();
+        }
+        const int quad = warp % 4, half = (warp - 2) / 4;
+        const int nl = quad * 32 + lane;
+        uint32_t n = 0;
+        for (int32_t id = cid; id < total; id += ncl, ++n) {
+            decode_tile(segs, nseg, g, id, WT, t);
+            const uint32_t acc = n & 1;
+            const int64_t col = t.n0 + (CG == 2 ? (int32_t)crank * WROWS : 0) + nl;
+            const bool n_ok = col < p.N;
+            float bias = 0.f;
+            if (LORA && lo.bias && n_ok)
+                bias = half_bits_to_float(static_cast<const uint16_t*>(lo.bias)[col * lo.bias_s], bf16);
+            if (!warp_wait(smem_u32(&acc_full[acc]), (n >> 1) & 1, abort_flag, DEVERR_TIMEOUT_EPILOGUE)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + acc * (uint32_t)g.acc_stride + ((uint32_t)(quad * 32) << 16);
+            if (CG == 2 || csize == 1) {
+                for (int c = half * 32; c < t.ts; c += 64) {
+                    float v[32];
+                    tmem_ld32(taddr + (uint32_t)c, reinterpret_cast<uint32_t(&)[32]>(v));
+                    tmem_ld_wait();
+                    finish<32, LORA>(v, (int64_t)t.row0 + c, min(32, t.rows - c), col, n_ok, bias, p, lo, bf16);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 2) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[acc]), 0));
+                    else mbar_arrive(smem_u32(&acc_empty[acc]));
+                }
+            } else {
+                // partial sums go to the CTA that owns the token: red[source][token][weight row]
+                const int tw = (t.ts + (int)csize - 1) / (int)csize;
+                const uint32_t red = smem_u32(smem + g.off_red);
+                if (!warp_wait_cluster(smem_u32(red_free), (n & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_EPILOGUE)) break;
+                for (int c = half * 32; c < t.ts; c += 64) {
+                    float v[32];
+                    tmem_ld32(taddr + (uint32_t)c, reinterpret_cast<uint32_t(&)[32]>(v));
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int tok = c + j;
+                        if (tok < t.rows) {
+                            const int owner = tok / tw;
+                            st_cluster_f32(map_to_rank(red + ((((int)crank * tw + tok - owner * tw) * WROWS + nl) << 2),
+                                                       (uint32_t)owner),
+                                           v[j]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                fence_cluster();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&acc_empty[acc]));
+                if (lane < (int)csize) mbar_arrive_cluster(map_to_rank(smem_u32(red_full), (uint32_t)lane));
+                if (!warp_wait_cluster(smem_u32(red_full), n & 1, abort_flag, DEVERR_TIMEOUT_EPILOGUE)) break;
+                const int t0 = (int)crank * tw, cnt = min(tw, t.rows - t0);
+                const float* rp = reinterpret_cast<const float*>(smem + g.off_red) + nl;
+                for (int j0 = half * 8; j0 < cnt; j0 += 16) {
+                    float v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+                    for (int src = 0; src < (int)csize; ++src)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (j0 + j < cnt) v[j] += rp[(src * tw + j0 + j) * WROWS];
+                    finish<8, LORA>(v, (int64_t)t.row0 + t0 + j0, min(8, cnt - j0), col, n_ok, bias, p, lo, bf16);
+                }
+                __syncwarp();
+                if (lane < (int)csize) mbar_arrive_cluster(map_to_rank(smem_u32(red_free), (uint32_t)lane));
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (csize > 1) cluster_sync();   // no CTA leaves while another may still signal it
+    tc_fence_after();
+    if (warp == 1) {
+        if (CG == 2) tmem_dealloc_pair(tmem_base, (uint32_t)g.tmem_cols);
+        else tmem_dealloc(tmem_base, (uint32_t)g.tmem_cols);
+    }
+}
+
+// ====================================================================== host side
+
+struct Plan {
+    Geo geo;
+    XMaps xm;
+    CUtensorMap wm;
+    int cg;
+    int smem_bytes;
+    int grid;
+};
+
+// The tensor-core kernels take x and weights of one half dtype whose rows
+// (along K, or along N for the weights) are contiguous and start on 16-byte
+// boundaries.
+inline bool supports(const Problem& p) {
+    if (p.x_dt != p.w_dt || p.K < 1 || p.N < 1) return false;
+    if (p.x_cs != 1 || (p.x_rs * 2) % 16 || p.x_rs < p.K || (reinterpret_cast<uintptr_t>(p.x) & 15)) return false;
+    if (reinterpret_cast<uintptr_t>(p.w) & 15) return false;
+    const bool k_major = p.w_ks == 1 && (p.w_ns * 2) % 16 == 0 && p.w_ns >= p.K;
+    const bool n_major = p.w_ns == 1 && (p.w_ks * 2) % 16 == 0 && p.w_ks >= p.N;
+    if (!k_major && !n_major) return false;
+    const int64_t span = k_major ? p.N * p.w_ns : p.K * p.w_ks;
+    if (p.lora_num > 1 && ((p.w_as * 2) % 16 || p.w_as + (k_major ? p.w_ns - p.K : p.w_ks - p.N) < span)) return false;
+    const int64_t lim = int64_t(1) << 31;
+    if (p.K >= lim || p.N >= lim || p.x_rows >= lim || p.out_rows >= lim || p.lora_num >= lim) return false;
+    if (p.x_rs >= (int64_t(1) << 38) || p.w_ns >= (int64_t(1) << 38) || p.w_ks >= (int64_t(1) << 38) ||
+        p.w_as >= (int64_t(1) << 38))
+        return false;
+    // tile numbers are 32-bit
+    const int64_t rows = p.x_rows < p.out_rows ? p.x_rows : p.out_rows;
+    if ((rows / 16 + p.batches + 1) * ((p.N + WROWS - 1) / WROWS) >= lim) return false;
+    return p.batches <= SEG_CAP;
+}
+
+struct Shape {
+    int cg, tn, splits;
+};
+
+// The form with the least estimated time.  Cycles of one stage of a CTA: the
+// MMA's (2 per token column of 128 weight rows and 64 of K, 4096 products a
+// cycle) or the loads' (64 bytes a cycle from L2), whichever is longer; a tile
+// adds a fixed cost, a shared one the exchange of the partial sums.  Segments
+// are taken as equally long, since their lengths are on the device.
+inline Shape choose_shape(const Problem& p, bool dense, int sm_count, int forced_cg) {
+    const int64_t rows = p.x_rows < p.out_rows ? p.x_rows : p.out_rows;
+    const int64_t segs = dense ? 1 : (p.batches < rows ? p.batches : rows);
+    const int64_t mean = segs > 0 ? (rows + segs - 1) / segs : 1;
+    const int64_t kblocks = (p.K + BK - 1) / BK;
+    Shape best{1, 32, 1};
+    double best_cost = -1;
+    const int tns[2][3] = {{32, 64, 128}, {64, 128, 256}};
+    for (int cg = 1; cg <= 2; ++cg) {
+        if (forced_cg && cg != forced_cg) continue;
+        for (int ti = 0; ti < 3; ++ti) {
+            const int tn = tns[cg - 1][ti];
+            const int64_t nt = (mean + tn - 1) / tn;
+            const int64_t ts = ((mean + nt - 1) / nt + 16 * cg - 1) / (16 * cg) * (16 * cg);
+            const int64_t tiles = segs * nt * ((p.N + WROWS * cg - 1) / (WROWS * cg));
+            for (int sp = 1; sp <= (cg == 1 ? MAX_SPLITS : 1); sp *= 2) {
+                if (sp > 1 && kblocks < 4 * sp) break;
+                const int64_t workers = sm_count / (cg * sp) - (sp >= 4 ? 4 : 0);   // GPCs that a cluster does not fill
+                const int64_t waves = (tiles + workers - 1) / workers;
+                const double load = (W_TILE + (double)ts / cg * 128) / 64.0;
+                const double mma = 2.0 * ts;
+                const double stage = (load > mma ? load : mma) > 160.0 ? (load > mma ? load : mma) : 160.0;
+                const double cost = waves * ((double)((kblocks + sp - 1) / sp) * stage + 600.0) + (sp > 1 ? 1500.0 : 0.0) + 16.0 * ts;
+                if (best_cost < 0 || cost < best_cost * 0.97) {
+                    best_cost = cost;
+                    best = Shape{cg, tn, sp};
+                }
+            }
+        }
+    }
+    return best;
+}
+
+inline bool make_plan(const Problem& p, bool dense, bool early, int sm_count, int forced_cg, EncodeTiledFn enc, Plan* out) {
+    if (!supports(p) || !enc) return false;
+    const Shape sh = choose_shape(p, dense, sm_count, forced_cg);
+    Geo& g = out->geo;
+    const int64_t rows = p.x_rows < p.out_rows ? p.x_rows : p.out_rows;
+    out->cg = sh.cg;
+    g.tn = sh.tn;
+    g.splits = sh.splits;
+    g.nblk = (int32_t)((p.N + WROWS * sh.cg - 1) / (WROWS * sh.cg));
+    g.kblocks = (int32_t)((p.K + BK - 1) / BK);
+    g.w_mn = !(p.w_ks == 1 && (p.w_ns * 2) % 16 == 0 && p.w_ns >= p.K);
+    g.dense_rows = dense ? (int32_t)rows : -1;
+    g.early = early ? 1 : 0;
+    const int64_t segs = dense ? 1 : p.batches;
+    g.keep_w = rows > (int64_t)sh.tn * segs ? 1 : 0;
+    g.acc_stride = sh.tn < 32 ? 32 : sh.tn;
+    g.tmem_cols = 32;
+    while (g.tmem_cols < 2 * g.acc_stride) g.tmem_cols *= 2;
+    g.stage_bytes = W_TILE + (sh.tn / sh.cg) * 128;
+    const int red = sh.splits > 1 ? sh.splits * ((sh.tn + sh.splits - 1) / sh.splits) * WROWS * 4 : 0;
+    for (g.stages = 12; g.stages >= 2; --g.stages) {
+        g.off_red = g.stages * g.stage_bytes;
+        g.off_seg = g.off_red + red;
+        g.off_bar = (g.off_seg + (int)segs * (int)sizeof(Seg) + 15) & ~15;
+        out->smem_bytes = g.off_bar + 8 * (2 * g.stages + 6) + 1024;
+        if (out->smem_bytes <= SMEM_LIMIT) break;
+    }
+    if (g.stages < 2) return false;
+
+    const cuuint32_t ones[3] = {1, 1, 1};
+    for (int k = 0; k < NUM_XMAPS; ++k) {
+        const cuuint64_t dims[2] = {(cuuint64_t)p.K, (cuuint64_t)p.x_rows};
+        const cuuint64_t strides[1] = {(cuuint64_t)(p.x_rs * 2)};
+        const cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)(16 << k)};
+        if (enc(&out->xm.m[k], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(p.x), dims, strides, box, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    }
+    const int64_t in = g.w_mn ? p.N : p.K, mid = g.w_mn ? p.K : p.N, pitch = g.w_mn ? p.w_ks : p.w_ns;
+    const cuuint64_t dims[3] = {(cuuint64_t)in, (cuuint64_t)mid, (cuuint64_t)p.lora_num};
+    cuuint64_t e_stride = (cuuint64_t)(p.w_as * 2);
+    if (p.lora_num == 1) e_stride = (cuuint64_t)((mid * pitch * 2 + 15) / 16 * 16);
+    const cuuint64_t strides[2] = {(cuuint64_t)(pitch * 2), e_stride};
+    const cuuint32_t box[3] = {64, (cuuint32_t)(g.w_mn ? BK : WROWS), 1};
+    if (enc(&out->wm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(p.w), dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    // most tiles the call can have: every segment may end in a partial one
+    const int64_t most_segs = segs < rows ? segs : rows;
+    const int64_t tiles = (rows / sh.tn + most_segs + 1) * g.nblk;
+    const int csize = sh.cg == 2 ? 2 : sh.splits;
+    int64_t clusters = sm_count / csize;
+    if (tiles < clusters) clusters = tiles;
+    out->grid = (int)(clusters < 1 ? 1 : clusters) * csize;
+    return true;
+}
+
+struct PlanKey {
+    Problem p;
+    int32_t device, sm_count, dense, early, forced_cg, pad;
+};
+
+inline bool cached_plan(const Problem& p, bool dense, bool early, int sm_count, int forced_cg, EncodeTiledFn enc, Plan* out) {
+    static PlanCache<PlanKey, Plan> cache;
+    PlanKey key;
+    std::memset(&key, 0, sizeof(key));
+    std::memcpy(&key.p, &p, sizeof(Problem));
+    key.sm_count = sm_count;
+    key.dense = dense;
+    key.early = early;
+    key.forced_cg = forced_cg;
+    if (cudaGetDevice(&key.device) != cudaSuccess) return false;
+    return cache.get(key, out, [&](Plan* pl) { return make_plan(p, dense, early, sm_count, forced_cg, enc, pl); });
+}
+
+template <int CG, bool LORA>
+int launch_kernel(const Plan& pl, const Problem& p, const Lora& lo, cudaStream_t stream) {
+    auto kern = gemm_kernel<CG, LORA>;
+    static std::atomic<uint64_t> configured{0};
+    if (!set_smem_limit_once(kern, SMEM_LIMIT, configured)) return SGMV_ERR_CUDA;
+    const int csize = CG == 2 ? 2 : pl.geo.splits;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)csize;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)pl.grid);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = (size_t)pl.smem_bytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = csize > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, pl.xm, pl.wm, p, pl.geo, lo) == cudaSuccess ? SGMV_OK : SGMV_ERR_LAUNCH;
+}
+
+template <bool LORA>
+int launch(const Plan& pl, const Problem& p, const Lora& lo, cudaStream_t stream) {
+    return pl.cg == 2 ? launch_kernel<2, LORA>(pl, p, lo, stream) : launch_kernel<1, LORA>(pl, p, lo, stream);
+}
+
+}  // namespace grp
+}  // namespace sgmv

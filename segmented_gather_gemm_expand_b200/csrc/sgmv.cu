@@ -28,6 +28,9 @@ __device__ void raise_device_error(int32_t bits) { atomicOr(&g_device_error, bit
 
 #include "tc_kernel.cuh"
 #include "shrink.cuh"
+#include "grouped.cuh"
+#include "wgrad.cuh"
+#include "lora.cuh"
 
 static_assert(SGMV_MAX_SLICES == sgmv::tc::MAX_SLICES, "one fused launch takes every slice of a call");
 
@@ -446,7 +449,416 @@ float* static_scratch(int* rc) {
 
 }  // namespace
 
+// ---------------------------------------------------------------- large products
+
+namespace {
+
+// Rows up to which a shared projection's low-rank input is computed row by row
+// (an adapter per row) instead of in 128-row blocks of one adapter.
+constexpr int64_t kRowShrinkRows = 256;
+
+int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// out with unit column stride and rows that do not overlap.
+bool rows_ok(const sgmv_tensor* out) {
+    return (out->shape[1] <= 1 || out->stride[1] == 1) && (out->shape[0] <= 1 || out->stride[0] >= out->shape[1]);
+}
+
+int validate_meta(const sgmv_tensor* s, const sgmv_tensor* l, const sgmv_tensor* idx, int64_t batches,
+                  int64_t max_seq_len) {
+    int rc;
+    if (batches < 0) return SGMV_ERR_BATCHES;
+    if (max_seq_len < 0) return SGMV_ERR_SHAPE;
+    if ((rc = check_meta(s, batches))) return rc;
+    if ((rc = check_meta(l, batches))) return rc;
+    return check_meta(idx, batches);
+}
+
+void fill_meta(Problem& p, const sgmv_tensor* s, const sgmv_tensor* l, const sgmv_tensor* idx, int64_t batches) {
+    p.start = meta_of(s);
+    p.len = meta_of(l);
+    p.idx = meta_of(idx);
+    p.batches = batches;
+}
+
+void fill_x(Problem& p, const sgmv_tensor* x) {
+    p.x = x->data;
+    p.x_dt = x->dtype;
+    p.x_rows = x->shape[0];
+    p.K = x->shape[1];
+    p.x_rs = x->stride[0];
+    p.x_cs = x->stride[1];
+}
+
+void fill_out(Problem& p, const sgmv_tensor* out) {
+    p.out = out->data;
+    p.out_dt = out->dtype;
+    p.out_rows = out->shape[0];
+    p.H = out->shape[0] > 1 ? out->stride[0] : out->shape[1];
+}
+
+// The CTA form a forced variant fixes for the large products (0: the cost model chooses).
+int forced_cg(int forced) { return forced == SGMV_VARIANT_TC_WIDE ? 2 : 0; }
+
+// Variant of a large product whose tensor-core form can (tc_ok) run the call.
+int large_variant(bool tc_ok, int forced) {
+    if (forced == SGMV_VARIANT_DECODE) return SGMV_ERR_VARIANT;
+    if (forced == SGMV_VARIANT_SIMT) return SGMV_VARIANT_SIMT;
+    if (forced != SGMV_VARIANT_AUTO) return tc_ok ? (int)SGMV_VARIANT_TC : (int)SGMV_ERR_VARIANT;
+    return tc_ok ? SGMV_VARIANT_TC : SGMV_VARIANT_SIMT;
+}
+
+int validate_grouped(const sgmv_tensor* x, const sgmv_tensor* w, const sgmv_tensor* out, const sgmv_tensor* s,
+                     const sgmv_tensor* l, const sgmv_tensor* idx, int64_t batches, int64_t max_seq_len, int add,
+                     Call* call) {
+    std::memset(call, 0, sizeof(Call));
+    int rc;
+    if ((rc = check_basic(x)) || (rc = check_basic(w)) || (rc = check_basic(out))) return rc;
+    if ((rc = validate_meta(s, l, idx, batches, max_seq_len))) return rc;
+    if (x->ndim != 2 || out->ndim != 2 || (w->ndim != 3 && w->ndim != 4)) return SGMV_ERR_NDIM;
+    if (!is_float_dtype(x->dtype) || !is_half_dtype(w->dtype) || !is_float_dtype(out->dtype)) return SGMV_ERR_DTYPE;
+    const int wd = w->ndim;
+    if (wd == 4 && w->shape[1] != 1) return SGMV_ERR_LAYOUT_4D;
+    if (w->shape[wd - 1] != x->shape[1]) return SGMV_ERR_RANK_MISMATCH;
+    if (w->shape[wd - 2] != out->shape[1]) return SGMV_ERR_OUT_WIDTH;
+    if (!rows_ok(out)) return SGMV_ERR_OUT_NOT_CONTIGUOUS;
+    Problem& p = call->p;
+    fill_x(p, x);
+    fill_out(p, out);
+    fill_meta(p, s, l, idx, batches);
+    p.w = w->data;
+    p.w_dt = w->dtype;
+    p.lora_num = w->shape[0];
+    p.w_as = w->stride[0];
+    p.w_ns = w->stride[wd - 2];
+    p.w_ks = w->stride[wd - 1];
+    p.N = w->shape[wd - 2];
+    p.add = add ? 1 : 0;
+    call->max_seq_len = max_seq_len;
+    call->empty = batches == 0 || p.N == 0 || p.out_rows == 0 || p.x_rows == 0 || p.lora_num == 0;
+    return SGMV_OK;
+}
+
+int choose_grouped(const Call& c, const DeviceInfo& dev, int forced, grp::Plan* pl) {
+    const bool tc_ok = forced != SGMV_VARIANT_SIMT && dev.cc_major == 10 &&
+                       grp::cached_plan(c.p, false, false, dev.sm_count, forced_cg(forced), tc::encode_fn(), pl);
+    return large_variant(tc_ok, forced);
+}
+
+struct WgradCall {
+    Problem p;
+    int64_t y_cs, out_gs, out_cs;
+    bool empty;
+};
+
+int validate_wgrad(const sgmv_tensor* dy, const sgmv_tensor* x, const sgmv_tensor* dw, const sgmv_tensor* s,
+                   const sgmv_tensor* l, const sgmv_tensor* idx, int64_t batches, int64_t max_seq_len, int add,
+                   WgradCall* call) {
+    std::memset(call, 0, sizeof(WgradCall));
+    int rc;
+    if ((rc = check_basic(dy)) || (rc = check_basic(x)) || (rc = check_basic(dw))) return rc;
+    if ((rc = validate_meta(s, l, idx, batches, max_seq_len))) return rc;
+    if (dy->ndim != 2 || x->ndim != 2 || (dw->ndim != 3 && dw->ndim != 4)) return SGMV_ERR_NDIM;
+    if (!is_float_dtype(dy->dtype) || !is_float_dtype(x->dtype) || !is_float_dtype(dw->dtype)) return SGMV_ERR_DTYPE;
+    const int wd = dw->ndim;
+    if (wd == 4 && dw->shape[1] != 1) return SGMV_ERR_LAYOUT_4D;
+    if (dw->shape[wd - 1] != x->shape[1]) return SGMV_ERR_RANK_MISMATCH;
+    if (dw->shape[wd - 2] != dy->shape[1]) return SGMV_ERR_SLICE_SIZE;
+    const int64_t E = dw->shape[0], N = dw->shape[wd - 2], K = dw->shape[wd - 1];
+    const int64_t ns = dw->stride[wd - 2], gs = dw->stride[0];
+    // unit stride along K, rows and indexes that do not overlap
+    if ((K > 1 && dw->stride[wd - 1] != 1) || (N > 1 && ns < K) || (E > 1 && gs < (N - 1) * (N > 1 ? ns : 0) + K))
+        return SGMV_ERR_OUT_NOT_CONTIGUOUS;
+    Problem& p = call->p;
+    fill_x(p, x);
+    p.N = K;                       // dW's columns are X's
+    p.K = N;
+    p.w = dy->data;
+    p.w_dt = dy->dtype;
+    p.w_ns = dy->stride[0];
+    p.lora_num = E;
+    p.out = dw->data;
+    p.out_dt = dw->dtype;
+    p.out_rows = dy->shape[0];     // rows past the end of X or dY are skipped
+    p.H = N > 1 ? ns : K;
+    fill_meta(p, s, l, idx, batches);
+    p.add = add ? 1 : 0;
+    call->y_cs = dy->stride[1];
+    call->out_gs = E > 1 ? gs : 0;
+    call->out_cs = 1;
+    const bool no_rows = batches == 0 || p.x_rows == 0 || p.out_rows == 0;
+    call->empty = E == 0 || N == 0 || K == 0 || (no_rows && add);
+    if (no_rows) p.batches = 0;
+    return SGMV_OK;
+}
+
+int choose_wgrad(const WgradCall& c, const DeviceInfo& dev, int forced, wgr::Plan* pl) {
+    const bool tc_ok =
+        forced != SGMV_VARIANT_SIMT && dev.cc_major == 10 && c.p.batches > 0 &&
+        wgr::cached_plan(c.p, c.y_cs, c.out_gs, c.out_cs, dev.sm_count, tc::encode_fn(), pl);
+    return large_variant(tc_ok, forced);
+}
+
+// A shared projection with adapters: `base` is x W^T over all rows, `shrink`
+// t = x A^T over the segments.
+struct LoraCall {
+    Problem base, shrink;
+    grp::Lora lo;
+    int64_t rows;
+    bool low_rank;            // there is a low-rank part to compute
+    bool empty;
+    int64_t off_t, off_part;  // workspace: row adapters, t, partial sums of t
+};
+
+int validate_lora(const sgmv_tensor* x, const sgmv_tensor* w, const sgmv_tensor* bias, const sgmv_tensor* a,
+                  const sgmv_tensor* b, const sgmv_tensor* out, const sgmv_tensor* s, const sgmv_tensor* l,
+                  const sgmv_tensor* idx, int64_t batches, int64_t max_seq_len, LoraCall* call) {
+    std::memset(call, 0, sizeof(LoraCall));
+    int rc;
+    if ((rc = check_basic(x)) || (rc = check_basic(w)) || (rc = check_basic(a)) || (rc = check_basic(b)) ||
+        (rc = check_basic(out)))
+        return rc;
+    if (bias && (rc = check_basic(bias))) return rc;
+    if ((rc = validate_meta(s, l, idx, batches, max_seq_len))) return rc;
+    if (x->ndim != 2 || w->ndim != 2 || out->ndim != 2 || (bias && bias->ndim != 1)) return SGMV_ERR_NDIM;
+    if ((a->ndim != 3 && a->ndim != 4) || (b->ndim != 3 && b->ndim != 4)) return SGMV_ERR_NDIM;
+    if (!is_float_dtype(x->dtype) || !is_half_dtype(w->dtype) || !is_float_dtype(out->dtype)) return SGMV_ERR_DTYPE;
+    if (a->dtype != w->dtype || b->dtype != w->dtype || (bias && bias->dtype != w->dtype)) return SGMV_ERR_DTYPE;
+    const int ad = a->ndim, bd = b->ndim;
+    if ((ad == 4 && a->shape[1] != 1) || (bd == 4 && b->shape[1] != 1)) return SGMV_ERR_LAYOUT_4D;
+    const int64_t K = x->shape[1], N = w->shape[0], R = a->shape[ad - 2];
+    if (w->shape[1] != K || a->shape[ad - 1] != K || b->shape[bd - 1] != R) return SGMV_ERR_RANK_MISMATCH;
+    if (b->shape[bd - 2] != N) return SGMV_ERR_SLICE_SIZE;
+    if (a->shape[0] != b->shape[0] || (bias && bias->shape[0] != N)) return SGMV_ERR_SHAPE;
+    if (out->shape[1] != N) return SGMV_ERR_OUT_WIDTH;
+    if (!rows_ok(out)) return SGMV_ERR_OUT_NOT_CONTIGUOUS;
+    if (R > (int64_t(1) << 20)) return SGMV_ERR_TOO_LARGE;
+    Problem& p = call->base;
+    fill_x(p, x);
+    fill_out(p, out);
+    p.w = w->data;
+    p.w_dt = w->dtype;
+    p.lora_num = 1;
+    p.w_ns = w->stride[0];
+    p.w_ks = w->stride[1];
+    p.N = N;
+    call->rows = p.x_rows < p.out_rows ? p.x_rows : p.out_rows;
+    if (call->rows >= (int64_t(1) << 31)) return SGMV_ERR_TOO_LARGE;
+    call->low_rank = batches > 0 && a->shape[0] > 0 && R > 0;
+    call->empty = N == 0 || call->rows == 0;
+    Problem& q = call->shrink;
+    fill_x(q, x);
+    fill_meta(q, s, l, idx, batches);
+    q.w = a->data;
+    q.w_dt = a->dtype;
+    q.lora_num = a->shape[0];
+    q.w_as = a->stride[0];
+    q.w_ns = a->stride[ad - 2];
+    q.w_ks = a->stride[ad - 1];
+    q.N = R;
+    q.H = R;
+    q.out_dt = SGMV_F32;
+    q.out_rows = call->rows;
+    grp::Lora& lo = call->lo;
+    lo.b = b->data;
+    lo.b_as = b->stride[0];
+    lo.b_ns = b->stride[bd - 2];
+    lo.b_ks = b->stride[bd - 1];
+    lo.R = call->low_rank ? (int32_t)R : 0;
+    lo.b_vec = lo.b_ks == 1 && (lo.b_ns * 2) % 16 == 0 && (b->shape[0] <= 1 || (lo.b_as * 2) % 16 == 0) &&
+               (reinterpret_cast<uintptr_t>(lo.b) & 15) == 0;
+    if (bias) {
+        lo.bias = bias->data;
+        lo.bias_s = bias->stride[0];
+    }
+    call->off_t = align256(call->rows * 4);
+    call->off_part = call->off_t + align256(call->rows * R * 4);
+    return SGMV_OK;
+}
+
+// How a validated, non-empty call runs.
+struct LoraPlan {
+    int variant;
+    grp::Plan base;
+    enum { NONE, BY_ROW, BLOCKS, PRODUCT } shrink;   // how t is computed
+    int splits;                                      // BLOCKS: parts of K
+    grp::Plan product;                               // PRODUCT: t as a grouped product
+};
+
+// Points the call at its workspace; ws_bytes bounds the partial sums of t.
+int choose_lora(LoraCall* c, const DeviceInfo& dev, int forced, char* ws, size_t ws_bytes, LoraPlan* pl) {
+    if (c->low_rank) {
+        c->lo.row_adapter = reinterpret_cast<int32_t*>(ws);
+        c->lo.t = reinterpret_cast<float*>(ws + c->off_t);
+        c->shrink.out = ws + c->off_t;
+    }
+    const bool tc = forced != SGMV_VARIANT_SIMT && dev.cc_major == 10;
+    const bool tc_ok = tc && grp::cached_plan(c->base, true, c->low_rank, dev.sm_count, forced_cg(forced),
+                                              tc::encode_fn(), &pl->base);
+    pl->variant = large_variant(tc_ok, forced);
+    if (pl->variant < 0) return pl->variant;
+    pl->shrink = c->low_rank ? LoraPlan::BY_ROW : LoraPlan::NONE;
+    pl->splits = 1;
+    if (c->low_rank && tc && c->rows > kRowShrinkRows) {
+        if (shr::supports(c->shrink) && c->shrink.batches <= shr::SEG_CAP) {
+            pl->shrink = LoraPlan::BLOCKS;
+            int sp = shr::preferred_splits(c->shrink, dev.sm_count);
+            const size_t room = ws_bytes > (size_t)c->off_part ? ws_bytes - (size_t)c->off_part : 0;
+            while (sp > 1 && (size_t)shr::workspace_bytes_for(c->shrink, sp) > room) sp /= 2;
+            pl->splits = sp;
+        } else if (grp::cached_plan(c->shrink, false, false, dev.sm_count, 0, tc::encode_fn(), &pl->product)) {
+            pl->shrink = LoraPlan::PRODUCT;
+        }
+    }
+    return SGMV_OK;
+}
+
+int run_lora(const LoraCall& c, const DeviceInfo& dev, const LoraPlan& pl, char* ws, cudaStream_t st) {
+    int rc = SGMV_OK;
+    int32_t* rows = reinterpret_cast<int32_t*>(ws);
+    float* t = reinterpret_cast<float*>(ws + c.off_t);
+    const Call shrink{c.shrink, 0, false};
+    switch (pl.shrink) {
+        case LoraPlan::BY_ROW:
+            if ((rc = lora::launch_row_shrink(c.shrink, t, rows, c.rows, st))) return rc;
+            break;
+        case LoraPlan::BLOCKS:
+            if ((rc = lora::launch_row_adapter(c.shrink, rows, c.rows, st))) return rc;
+            if ((rc = launch_shrink(shrink, dev, pl.splits, reinterpret_cast<float*>(ws + c.off_part), st))) return rc;
+            break;
+        case LoraPlan::PRODUCT:
+            if ((rc = lora::launch_row_adapter(c.shrink, rows, c.rows, st))) return rc;
+            if ((rc = grp::launch<false>(pl.product, c.shrink, grp::Lora{}, st))) return rc;
+            break;
+        default: break;
+    }
+    if (pl.variant == SGMV_VARIANT_TC) return grp::launch<true>(pl.base, c.base, c.lo, st);
+    return lora::launch_lora_simt(c.base, c.lo, c.rows, st);
+}
+
+}  // namespace
+
 extern "C" {
+
+int sgmv_grouped_gemm(const sgmv_tensor* inputs, const sgmv_tensor* weights, const sgmv_tensor* out,
+                      const sgmv_tensor* seq_start, const sgmv_tensor* seq_len, const sgmv_tensor* group_idx,
+                      int64_t batches, int64_t max_seq_len, int add_inputs, void* stream) {
+    Call c;
+    int rc = validate_grouped(inputs, weights, out, seq_start, seq_len, group_idx, batches, max_seq_len, add_inputs, &c);
+    if (rc) return rc;
+    if (c.empty) return SGMV_OK;
+    DeviceInfo dev;
+    if ((rc = device_info(&dev))) return rc;
+    grp::Plan pl;
+    const int v = choose_grouped(c, dev, g_forced_variant.load(), &pl);
+    if (v < 0) return v;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (v == SGMV_VARIANT_TC) return grp::launch<false>(pl, c.p, grp::Lora{}, st);
+    return launch_simt(c, dev, st);
+}
+
+int sgmv_grouped_gemm_plan(const sgmv_tensor* inputs, const sgmv_tensor* weights, const sgmv_tensor* out,
+                           const sgmv_tensor* seq_start, const sgmv_tensor* seq_len, const sgmv_tensor* group_idx,
+                           int64_t batches, int64_t max_seq_len, int add_inputs, int* variant) {
+    if (!variant) return SGMV_ERR_NULL_ARG;
+    *variant = 0;
+    Call c;
+    int rc = validate_grouped(inputs, weights, out, seq_start, seq_len, group_idx, batches, max_seq_len, add_inputs, &c);
+    if (rc) return rc;
+    if (c.empty) return SGMV_OK;
+    DeviceInfo dev;
+    if ((rc = device_info(&dev))) return rc;
+    grp::Plan pl;
+    const int v = choose_grouped(c, dev, g_forced_variant.load(), &pl);
+    if (v < 0) return v;
+    *variant = v;
+    return SGMV_OK;
+}
+
+int sgmv_grouped_wgrad(const sgmv_tensor* grad_out, const sgmv_tensor* inputs, const sgmv_tensor* grad_weights,
+                       const sgmv_tensor* seq_start, const sgmv_tensor* seq_len, const sgmv_tensor* group_idx,
+                       int64_t batches, int64_t max_seq_len, int add_inputs, void* stream) {
+    WgradCall c;
+    int rc = validate_wgrad(grad_out, inputs, grad_weights, seq_start, seq_len, group_idx, batches, max_seq_len,
+                            add_inputs, &c);
+    if (rc) return rc;
+    if (c.empty) return SGMV_OK;
+    DeviceInfo dev;
+    if ((rc = device_info(&dev))) return rc;
+    wgr::Plan pl;
+    const int v = choose_wgrad(c, dev, g_forced_variant.load(), &pl);
+    if (v < 0) return v;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (v == SGMV_VARIANT_TC) return wgr::launch(pl, c.p, st);
+    return wgr::launch_simt(c.p, c.y_cs, c.out_gs, c.out_cs, st);
+}
+
+int sgmv_grouped_wgrad_plan(const sgmv_tensor* grad_out, const sgmv_tensor* inputs, const sgmv_tensor* grad_weights,
+                            const sgmv_tensor* seq_start, const sgmv_tensor* seq_len, const sgmv_tensor* group_idx,
+                            int64_t batches, int64_t max_seq_len, int add_inputs, int* variant) {
+    if (!variant) return SGMV_ERR_NULL_ARG;
+    *variant = 0;
+    WgradCall c;
+    int rc = validate_wgrad(grad_out, inputs, grad_weights, seq_start, seq_len, group_idx, batches, max_seq_len,
+                            add_inputs, &c);
+    if (rc) return rc;
+    if (c.empty) return SGMV_OK;
+    DeviceInfo dev;
+    if ((rc = device_info(&dev))) return rc;
+    wgr::Plan pl;
+    const int v = choose_wgrad(c, dev, g_forced_variant.load(), &pl);
+    if (v < 0) return v;
+    *variant = v;
+    return SGMV_OK;
+}
+
+int sgmv_lora_linear(const sgmv_tensor* inputs, const sgmv_tensor* weight, const sgmv_tensor* bias,
+                     const sgmv_tensor* lora_a, const sgmv_tensor* lora_b, const sgmv_tensor* out,
+                     const sgmv_tensor* seq_start, const sgmv_tensor* seq_len, const sgmv_tensor* lora_idx,
+                     int64_t batches, int64_t max_seq_len, void* workspace, size_t workspace_bytes, void* stream) {
+    LoraCall c;
+    int rc = validate_lora(inputs, weight, bias, lora_a, lora_b, out, seq_start, seq_len, lora_idx, batches,
+                           max_seq_len, &c);
+    if (rc) return rc;
+    if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 15)) return SGMV_ERR_WORKSPACE;
+    if (c.empty) return SGMV_OK;
+    if (c.low_rank && (!workspace || workspace_bytes < (size_t)c.off_part)) return SGMV_ERR_WORKSPACE;
+    DeviceInfo dev;
+    if ((rc = device_info(&dev))) return rc;
+    LoraPlan pl;
+    char* ws = static_cast<char*>(workspace);
+    if ((rc = choose_lora(&c, dev, g_forced_variant.load(), ws, workspace_bytes, &pl))) return rc;
+    return run_lora(c, dev, pl, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int sgmv_lora_linear_plan(const sgmv_tensor* inputs, const sgmv_tensor* weight, const sgmv_tensor* bias,
+                          const sgmv_tensor* lora_a, const sgmv_tensor* lora_b, const sgmv_tensor* out,
+                          const sgmv_tensor* seq_start, const sgmv_tensor* seq_len, const sgmv_tensor* lora_idx,
+                          int64_t batches, int64_t max_seq_len, int* variant, size_t* workspace_bytes,
+                          size_t* preferred_workspace_bytes) {
+    if (!variant || !workspace_bytes || !preferred_workspace_bytes) return SGMV_ERR_NULL_ARG;
+    *variant = 0;
+    *workspace_bytes = 0;
+    *preferred_workspace_bytes = 0;
+    LoraCall c;
+    int rc = validate_lora(inputs, weight, bias, lora_a, lora_b, out, seq_start, seq_len, lora_idx, batches,
+                           max_seq_len, &c);
+    if (rc) return rc;
+    if (c.empty) return SGMV_OK;
+    DeviceInfo dev;
+    if ((rc = device_info(&dev))) return rc;
+    LoraPlan pl;
+    // an aligned stand-in for the workspace's address: only sizes matter here
+    if ((rc = choose_lora(&c, dev, g_forced_variant.load(), reinterpret_cast<char*>(uintptr_t(256)), ~size_t(0), &pl)))
+        return rc;
+    *variant = pl.variant;
+    if (c.low_rank) {
+        *workspace_bytes = (size_t)c.off_part;
+        *preferred_workspace_bytes =
+            (size_t)(c.off_part + (pl.shrink == LoraPlan::BLOCKS ? shr::workspace_bytes_for(c.shrink, pl.splits) : 0));
+    }
+    return SGMV_OK;
+}
 
 int sgmv_shrink_static_scratch(const sgmv_tensor* inputs, const sgmv_tensor* lora_a, const sgmv_tensor* out,
                                const sgmv_tensor* seq_start, const sgmv_tensor* seq_len,
@@ -683,7 +1095,7 @@ const char* sgmv_status_string(int code) {
         case SGMV_ERR_NUM_SLICES: return "num_slices outside [1, SGMV_MAX_SLICES]";
         case SGMV_ERR_SLICE_OVERLAP: return "two slices of a multi-slice call overlap";
         case SGMV_ERR_OUT_WIDTH: return "out.shape[1] != lora_b.shape[-2] (plain expand and shrink write whole rows)";
-        case SGMV_ERR_WORKSPACE: return "workspace is not 16-byte aligned";
+        case SGMV_ERR_WORKSPACE: return "workspace is not 16-byte aligned, or too small for a call that needs one";
         case SGMV_ERR_SCRATCH: return "reserved status (no entry point returns it)";
         case SGMV_ERR_CUDA: return "a CUDA runtime call failed";
         case SGMV_ERR_LAUNCH: return "kernel launch failed";
