@@ -245,7 +245,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
     if (tid == 0) {
         s_abort = 0;
         for (uint32_t i = 0; i < S; ++i) {
-            mbar_init(smem_u32(&full[i]), CG);   // each CTA of a pair announces its own bytes
+            mbar_init(smem_u32(&full[i]), 1);   // the first CTA of a pair announces the bytes of both
             mbar_init(smem_u32(&empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -337,8 +337,11 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                     }
                     const uint32_t ws = smem_u32(smem + s * g.stage_bytes), xs = ws + W_TILE;
                     if (CG == 2) {
+                        // both CTAs' loads count at the first one's barrier; it alone announces them: a remote
+                        // arrival with release semantics costs a memory barrier per stage (1640 cycles a stage
+                        // instead of 512).  The second CTA cannot run a phase ahead, since it waits for `empty`.
                         const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
-                        mbar_expect_tx_cluster(bar, bytes);
+                        if (crank == 0) mbar_expect_tx(smem_u32(&full[s]), 2 * bytes);
                         if (g.w_mn) {
                             tma_load_3d_pair(ws, &wmap, n0, kb * BK, t.group, bar, pol_w);
                             tma_load_3d_pair(ws + W_TILE / 2, &wmap, n0 + 64, kb * BK, t.group, bar, pol_w);

@@ -76,7 +76,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     if (tid == 0) {
         s_abort = 0;
         for (uint32_t i = 0; i < S; ++i) {
-            mbar_init(smem_u32(&full[i]), 2);
+            mbar_init(smem_u32(&full[i]), 2);   // two arrivals of the first CTA's producer, or one of each CTA's warp 10
             mbar_init(smem_u32(&empty[i]), 1);
             mbar_init(smem_u32(&part[i]), 1);
         }
@@ -185,7 +185,10 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
                             mbar_expect_tx(bar, bytes);
                         } else {
                             bar = map_to_rank(smem_u32(&full[s]), 0);
-                            mbar_expect_tx_cluster(bar, bytes);
+                            if (crank == 0) {
+                                mbar_expect_tx(smem_u32(&full[s]), 2 * bytes);
+                                mbar_arrive(smem_u32(&full[s]));
+                            }
                         }
                         for (int i = 0; i < 2; ++i)
                             tma_load_2d_pair(xs + i * HALF, &xmap, k0 + i * 64, sg.row0 + r, bar, pol);
