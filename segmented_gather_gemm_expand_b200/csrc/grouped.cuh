@@ -317,10 +317,10 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        if (lane == 0) {
+        if (elect_one()) {
             const uint64_t pol_x = policy_evict_normal();
             const uint64_t pol_w = g.keep_w ? policy_evict_normal() : policy_evict_first();
-            uint32_t q = 0;
+            uint32_t s = 0, phase = 1;
             bool ok = true;
             for (int32_t id = cid; ok && id < total; id += ncl) {
                 decode_tile(segs, nseg, g, id, WT, t);
@@ -329,9 +329,8 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                 const uint32_t bytes = W_TILE + (16u << lvl) * 128u;
                 const int32_t xr = t.row0 + (CG == 2 ? (int32_t)crank * hs : 0);
                 const int32_t n0 = t.n0 + (CG == 2 ? (int32_t)crank * WROWS : 0);
-                for (int32_t kb = kb0; kb < kb1; ++kb, ++q) {
-                    const uint32_t s = q % S;
-                    if (!mbar_wait(smem_u32(&empty[s]), ((q / S) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_PRODUCER)) {
+                for (int32_t kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(smem_u32(&empty[s]), phase, abort_flag, DEVERR_TIMEOUT_PRODUCER)) {
                         ok = false;
                         break;
                     }
@@ -360,55 +359,57 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                         }
                         tma_load_2d(xs, &xmaps.m[lvl], kb * BK, xr, bar, pol_x);
                     }
+                    if (++s == S) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA (the pair's first CTA)
-        if (CG == 1 || crank == 0) {
-            uint32_t q = 0, n = 0;
+        if ((CG == 1 || crank == 0) && elect_one()) {
+            uint32_t s = 0, phase = 0, n = 0;
             bool ok = true;
             // K step of 16 inside a stage: 32 bytes along a K-major row, 16 rows of an N-major tile
             const uint64_t w_step = (uint64_t)((g.w_mn ? 16 * 128 : 32) >> 4);
+            const uint64_t ad0 = smem_desc(smem_u32(smem), g.w_mn ? W_TILE / 2 : 16, 1024, 2);
+            const uint64_t bd0 = smem_desc(smem_u32(smem) + W_TILE, 16, 1024, 2);
+            const uint64_t stage_step = (uint64_t)(g.stage_bytes >> 4);
             for (int32_t id = cid; ok && id < total; id += ncl, ++n) {
                 decode_tile(segs, nseg, g, id, WT, t);
                 const uint32_t acc = n & 1;
                 const uint32_t idesc = instr_desc_mn(bf16, WT, t.ts) | (g.w_mn ? IDESC_A_MN : 0u);
                 const uint32_t d = tmem_base + acc * (uint32_t)g.acc_stride;
-                if (!warp_wait(smem_u32(&acc_empty[acc]), ((n >> 1) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_MMA)) break;
+                if (!mbar_wait(smem_u32(&acc_empty[acc]), ((n >> 1) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_MMA)) break;
                 tc_fence_after();
-                for (int32_t kb = kb0; kb < kb1; ++kb, ++q) {
-                    const uint32_t s = q % S;
-                    if (!warp_wait(smem_u32(&full[s]), (q / S) & 1, abort_flag, DEVERR_TIMEOUT_MMA)) {
+                for (int32_t kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(smem_u32(&full[s]), phase, abort_flag, DEVERR_TIMEOUT_MMA)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t ws = smem_u32(smem + s * g.stage_bytes);
-                        const uint64_t ad = smem_desc(ws, g.w_mn ? W_TILE / 2 : 16, 1024, 2);
-                        const uint64_t bd = smem_desc(ws + W_TILE, 16, 1024, 2);
+                    const uint64_t ad = ad0 + s * stage_step, bd = bd0 + s * stage_step;
 #pragma unroll
-                        for (int kk = 0; kk < BK / 16; ++kk) {
-                            if (CG == 2)
-                                tc_mma_pair(d, ad + kk * w_step, bd + kk * 2, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
-                            else
-                                tc_mma(d, ad + kk * w_step, bd + kk * 2, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
-                        }
-                        if (CG == 2) tc_commit_pair(smem_u32(&empty[s]));
-                        else tc_commit(smem_u32(&empty[s]));
+                    for (int kk = 0; kk < BK / 16; ++kk) {
+                        const uint32_t more = (kk > 0 || kb > kb0) ? 1u : 0u;
+                        if (CG == 2) tc_mma_pair(d, ad + kk * w_step, bd + kk * 2, idesc, more);
+                        else tc_mma(d, ad + kk * w_step, bd + kk * 2, idesc, more);
                     }
-                    __syncwarp();
+                    if (CG == 2) tc_commit_pair(smem_u32(&empty[s]));
+                    else tc_commit(smem_u32(&empty[s]));
+                    if (++s == S) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
                 if (!ok) break;
-                if (lane == 0) {
-                    if (CG == 2) tc_commit_pair(smem_u32(&acc_full[acc]));
-                    else tc_commit(smem_u32(&acc_full[acc]));
-                }
-                __syncwarp();
+                if (CG == 2) tc_commit_pair(smem_u32(&acc_full[acc]));
+                else tc_commit(smem_u32(&acc_full[acc]));
             }
         }
+        __syncwarp();
     } else {
         // ------------------------------------------------------------ epilogue
         if (g.early) {

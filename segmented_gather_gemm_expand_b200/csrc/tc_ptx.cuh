@@ -271,6 +271,19 @@ __device__ __forceinline__ void grid_dependents_launch() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// True in one lane of a converged warp.  A branch on it tells the compiler that
+// a single thread runs the body, so the operands of MMA and TMA instructions
+// stay in uniform registers (lane == 0 made it rebuild them for every one).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
+}
+
 // CTA pairs and clusters ------------------------------------------------------
 
 __device__ __forceinline__ uint32_t cluster_rank() {

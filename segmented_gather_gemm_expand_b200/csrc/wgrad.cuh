@@ -158,11 +158,11 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        if (lane == 0) {
+        if (elect_one()) {
             const uint64_t pol = policy_evict_normal();
             const int nybox = hs > 64 ? 2 : 1;
             const uint32_t bytes = (uint32_t)(2 + nybox) * HALF;
-            uint32_t q = 0;
+            uint32_t s = 0, phase = 1;
             bool ok = true;
             for (int32_t id = cid; ok && id < total; id += ncl) {
                 int32_t e, k0, n0;
@@ -171,9 +171,8 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
                 n0 += (int32_t)(crank * hs);
                 for (int32_t b = exps[e].first; ok && b >= 0; b = segs[b].next) {
                     const Seg sg = segs[b];
-                    for (int32_t r = 0; r < sg.rows; r += BT, ++q) {
-                        const uint32_t s = q % S;
-                        if (!mbar_wait(smem_u32(&empty[s]), ((q / S) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_PRODUCER)) {
+                    for (int32_t r = 0; r < sg.rows; r += BT) {
+                        if (!mbar_wait(smem_u32(&empty[s]), phase, abort_flag, DEVERR_TIMEOUT_PRODUCER)) {
                             ok = false;
                             break;
                         }
@@ -194,6 +193,10 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
                             tma_load_2d_pair(xs + i * HALF, &xmap, k0 + i * 64, sg.row0 + r, bar, pol);
                         for (int i = 0; i < nybox; ++i)
                             tma_load_2d_pair(ys + i * HALF, &ymap, n0 + i * 64, sg.row0 + r, bar, pol);
+                        if (++s == S) {
+                            s = 0;
+                            phase ^= 1;
+                        }
                     }
                 }
             }
@@ -201,47 +204,48 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA (the pair's first CTA)
-        if (crank == 0) {
+        if (crank == 0 && elect_one()) {
             const uint32_t idesc = instr_desc_mn(bf16, 256, g.ts) | IDESC_A_MN | IDESC_B_MN;
-            uint32_t q = 0, n = 0;
+            // 64-column boxes are HALF apart, 8-token groups 1024 bytes; a K step is 16 tokens
+            const uint64_t ad0 = smem_desc(smem_u32(smem), HALF, 1024, 2);
+            const uint64_t bd0 = smem_desc(smem_u32(smem) + 2 * HALF, HALF, 1024, 2);
+            uint32_t s = 0, phase = 0, n = 0;
             bool ok = true;
             for (int32_t id = cid; ok && id < total; id += ncl, ++n) {
                 int32_t e, k0, n0;
                 decode(id, e, k0, n0);
                 const uint32_t acc = n & 1;
                 const uint32_t d = tmem_base + acc * (uint32_t)g.acc_stride;
-                if (!warp_wait(smem_u32(&acc_empty[acc]), ((n >> 1) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_MMA)) break;
+                if (!mbar_wait(smem_u32(&acc_empty[acc]), ((n >> 1) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_MMA)) break;
                 tc_fence_after();
                 uint32_t more = 0;
                 for (int32_t b = exps[e].first; ok && b >= 0; b = segs[b].next) {
                     const int32_t rows = segs[b].rows;
-                    for (int32_t r = 0; r < rows; r += BT, ++q) {
-                        const uint32_t s = q % S;
-                        if (!warp_wait_cluster(smem_u32(&full[s]), (q / S) & 1, abort_flag, DEVERR_TIMEOUT_MMA)) {
+                    for (int32_t r = 0; r < rows; r += BT) {
+                        if (!mbar_wait(smem_u32(&full[s]), phase, abort_flag, DEVERR_TIMEOUT_MMA)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        if (lane == 0) {
-                            const uint32_t xs = smem_u32(smem + s * STAGE);
-                            // 64-column boxes are HALF apart, 8-token groups 1024 bytes; a K step is 16 tokens
-                            const uint64_t ad = smem_desc(xs, HALF, 1024, 2);
-                            const uint64_t bd = smem_desc(xs + 2 * HALF, HALF, 1024, 2);
-                            const int steps = min(BT / 16, (rows - r + 15) / 16);
-                            for (int kk = 0; kk < steps; ++kk) {
-                                tc_mma_pair(d, ad + kk * 128, bd + kk * 128, idesc, more);
-                                more = 1;
-                            }
-                            tc_commit_pair(smem_u32(&empty[s]));
+                        const uint64_t ad = ad0 + s * (uint64_t)(STAGE >> 4), bd = bd0 + s * (uint64_t)(STAGE >> 4);
+                        const int steps = (rows - r + 15) / 16;   // K steps that hold rows
+#pragma unroll
+                        for (int kk = 0; kk < BT / 16; ++kk) {
+                            if (kk < steps) tc_mma_pair(d, ad + kk * 128, bd + kk * 128, idesc, more);
+                            more = 1;
                         }
-                        __syncwarp();
+                        tc_commit_pair(smem_u32(&empty[s]));
+                        if (++s == S) {
+                            s = 0;
+                            phase ^= 1;
+                        }
                     }
                 }
                 if (!ok) break;
-                if (lane == 0) tc_commit_pair(smem_u32(&acc_full[acc]));
-                __syncwarp();
+                tc_commit_pair(smem_u32(&acc_full[acc]));
             }
         }
+        __syncwarp();
     } else if (warp == FIX_WARP) {
         // ------------------------------------------------------------ rows past a segment's end
         uint32_t q = 0, phase = 0;   // phase: one bit per stage (at most 32 stages)
