@@ -28,6 +28,17 @@
 //          sums into each other's shared memory (every CTA owns a part of the
 //          tokens) and add them in rank order (deterministic): decode shapes.
 //
+// The low-rank part of a shared projection comes in one of two ways (LoraMode):
+//   LORA_MMA   as further K steps of the same accumulator, for batches whose
+//          segments are long enough to share an MMA: for every run of rows with
+//          one adapter in a token tile, one stage per 32 ranks holds B[a]'s rows
+//          (TMA) and t's rows (warp 10), zero outside the run.  t is fp32 and
+//          enters as the sum of two half-precision parts (hi, and what is left
+//          of it, rounded), three where out is fp32: relative errors of 2^-16
+//          (2^-24) against out's own rounding of 2^-9 (2^-24).
+//   LORA_FMA   on the CUDA cores in the epilogue, in fp32: single tokens with an
+//          adapter each, or a B that TMA cannot read.
+//
 // Every wait is bounded and reports a timeout through the device error word.
 #pragma once
 
@@ -46,7 +57,9 @@ constexpr int BK = 64;                  // K columns per stage: 128-byte rows
 constexpr int WROWS = 128;              // weight rows per CTA
 constexpr int W_TILE = WROWS * BK * 2;  // 16 KB
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int LORA_WARP = 2 + EPI_WARPS;   // LORA_MMA only
+enum LoraMode { LORA_NONE = 0, LORA_FMA = 1, LORA_MMA = 2 };
+constexpr int threads_of(int lora) { return 64 + 32 * EPI_WARPS + (lora == LORA_MMA ? 32 : 0); }
 constexpr int NUM_XMAPS = 4;            // x boxes of 16, 32, 64, 128 rows
 constexpr int MAX_SPLITS = 8;
 constexpr int BAND = 8;                 // token tiles walked together before the next weight tile
@@ -76,13 +89,21 @@ struct XMaps {
     CUtensorMap m[NUM_XMAPS];
 };
 
+// A run of neighbouring rows of one token tile that share an adapter.
+struct Run {
+    int32_t adapter, begin, end;   // rows [begin, end)
+    int32_t count;                 // in the tile's first record: runs of the tile (may be 0)
+};
+
 // The low-rank part and the bias of a shared projection.
 struct Lora {
     const float* t;              // (rows, R) fp32: x A^T
-    const int32_t* row_adapter;  // (rows): adapter, -1 for none
+    const int32_t* row_adapter;  // LORA_FMA, (rows): adapter, -1 for none
+    const Run* runs;             // LORA_MMA, (rows): the runs of a tile from its first row's place on
     const void* b;               // (adapters, N, R), the weights' dtype
     int64_t b_as, b_ns, b_ks;
     int32_t R;
+    int32_t parts;               // LORA_MMA: half-precision parts of t (2 or 3)
     int32_t b_vec;               // rows of B can be read as 16-byte pieces
     const void* bias;            // (N) in the weights' dtype, or null
     int64_t bias_s;
@@ -180,12 +201,12 @@ __device__ __forceinline__ void add_lora(float (&v)[NT], int64_t row, int valid,
 
 // Adds the low-rank part, the bias or the old output, rounds once and stores
 // rows row .. row + valid - 1 of column n.
-template <int NT, bool LORA>
+template <int NT, int LORA>
 __device__ __forceinline__ void finish(float (&v)[NT], int64_t row, int valid, int64_t n, bool n_ok, float bias,
                                        const Problem& p, const Lora& lo, bool bf16) {
     if (valid <= 0) return;
-    if (LORA) {
-        if (lo.R > 0) add_lora<NT>(v, row, valid, n, n_ok, lo, bf16);
+    if (LORA == LORA_FMA && lo.R > 0) add_lora<NT>(v, row, valid, n, n_ok, lo, bf16);
+    if (LORA != LORA_NONE) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) v[j] += bias;
     }
@@ -219,10 +240,57 @@ __device__ __forceinline__ void finish(float (&v)[NT], int64_t row, int valid, i
     }
 }
 
-template <int CG, bool LORA>
-__global__ void __launch_bounds__(THREADS, 1)
-gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtensorMap wmap, const Problem p, const Geo g,
-            const Lora lo) {
+// The part of v that the parts before have not covered, rounded to the half
+// type: hi = rounded(v), then rounded(v - hi), ...  fp16 saturates (what is left
+// goes to the next part); an infinity or NaN stays in the first part alone.
+__device__ __forceinline__ uint32_t next_part(float& v, bool bf16) {
+    float h = v;
+    if (!bf16 && fabsf(v) > 65504.f && fabsf(v) <= 3.4e38f) h = copysignf(65504.f, v);
+    const uint32_t bits = float_to_half_bits(h, bf16);
+    const float back = half_bits_to_float(bits, bf16);
+    v = fabsf(back) <= 3.4e38f ? v - back : 0.f;
+    return bits;
+}
+
+// Rows [row0, row0 + rows) of t, ranks [r0, r0 + C), as a K-major tile with
+// 128-byte swizzle: `parts` groups of C columns (C = 32 for two parts, 16 for
+// three), zero outside the run and past the last rank.  One lane per row.
+__device__ __forceinline__ void write_t_tile(uint8_t* dst, int64_t row0, int rows, const Run& run, int r0, const Lora& lo,
+                                             int lane, bool bf16) {
+    const int C = lo.parts == 2 ? 32 : 16, ranks = min(C, lo.R - r0);
+    for (int i = lane; i < rows; i += 32) {
+        const int64_t row = row0 + i;
+        const bool in = row >= run.begin && row < run.end;
+        const float* src = lo.t + row * lo.R + r0;
+        for (int c = 0; c < (ranks + 15) / 16 * 16; c += 8) {
+            float v[8];
+            if (in && c + 8 <= ranks) {   // R is a multiple of 8: 16-byte reads
+                const float4 a = *reinterpret_cast<const float4*>(src + c), b = *reinterpret_cast<const float4*>(src + c + 4);
+                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = 0.f;
+            }
+            for (int part = 0; part < lo.parts; ++part) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t x = next_part(v[2 * k], bf16);
+                    w[k] = x | next_part(v[2 * k + 1], bf16) << 16;
+                }
+                const int chunk = (part * C + c) / 8;
+                *reinterpret_cast<uint4*>(dst + i * 128 + ((chunk ^ (i & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+}
+
+template <int CG, int LORA>
+__global__ void __launch_bounds__(threads_of(LORA), 1)
+gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtensorMap wmap,
+            const __grid_constant__ CUtensorMap bmap, const Problem p, const Geo g, const Lora lo) {
+    constexpr int THREADS = threads_of(LORA);
+    constexpr uint32_t T_ARRIVALS = LORA == LORA_MMA ? CG : 0;   // arrivals of the warps that write t
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ int s_abort;
@@ -241,12 +309,14 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* red_full = acc_empty + 2;
     uint64_t* red_free = red_full + 1;
+    uint64_t* t_go = red_free + 1;   // LORA_MMA: the stage is free for t (one phase per low-rank stage it serves)
 
     if (tid == 0) {
         s_abort = 0;
         for (uint32_t i = 0; i < S; ++i) {
-            mbar_init(smem_u32(&full[i]), 1);   // the first CTA of a pair announces the bytes of both
+            mbar_init(smem_u32(&full[i]), 1 + T_ARRIVALS);   // the first CTA of a pair announces the bytes of both
             mbar_init(smem_u32(&empty[i]), 1);
+            if (LORA == LORA_MMA) mbar_init(smem_u32(&t_go[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&acc_full[i]), 1);
@@ -259,6 +329,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
     if (warp == 0 && lane == 0) {
         for (int k = 0; k < NUM_XMAPS; ++k) prefetch_tmap(&xmaps.m[k]);
         prefetch_tmap(&wmap);
+        if (LORA == LORA_MMA) prefetch_tmap(&bmap);
     }
     if (warp == 1) {
         if (CG == 2) tmem_alloc_pair(smem_u32(&s_tmem_base), (uint32_t)g.tmem_cols);
@@ -313,6 +384,8 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
     constexpr int32_t WT = WROWS * CG;
     const int32_t kb0 = CG == 2 ? 0 : (int32_t)((int64_t)g.kblocks * crank / csize);
     const int32_t kb1 = CG == 2 ? g.kblocks : (int32_t)((int64_t)g.kblocks * (crank + 1) / csize);
+    const bool lora_here = CG == 2 || crank == 0;   // of CTAs that share a tile, the first adds the low-rank part
+    const int32_t t_ranks = lo.parts == 2 ? 32 : 16;
     Tile t;
 
     if (warp == 0) {
@@ -340,7 +413,10 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                         // arrival with release semantics costs a memory barrier per stage (1640 cycles a stage
                         // instead of 512).  The second CTA cannot run a phase ahead, since it waits for `empty`.
                         const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
-                        if (crank == 0) mbar_expect_tx(smem_u32(&full[s]), 2 * bytes);
+                        if (crank == 0) {
+                            mbar_expect_tx(smem_u32(&full[s]), 2 * bytes);
+                            if (T_ARRIVALS) mbar_arrive_n(smem_u32(&full[s]), T_ARRIVALS);
+                        }
                         if (g.w_mn) {
                             tma_load_3d_pair(ws, &wmap, n0, kb * BK, t.group, bar, pol_w);
                             tma_load_3d_pair(ws + W_TILE / 2, &wmap, n0 + 64, kb * BK, t.group, bar, pol_w);
@@ -351,6 +427,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                     } else {
                         const uint32_t bar = smem_u32(&full[s]);
                         mbar_expect_tx(bar, bytes);
+                        if (T_ARRIVALS) mbar_arrive_n(bar, T_ARRIVALS);
                         if (g.w_mn) {
                             tma_load_3d(ws, &wmap, n0, kb * BK, t.group, bar, pol_w);
                             tma_load_3d(ws + W_TILE / 2, &wmap, n0 + 64, kb * BK, t.group, bar, pol_w);
@@ -364,9 +441,67 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                         phase ^= 1;
                     }
                 }
+                if (LORA == LORA_MMA && ok && lora_here) {
+                    if (g.early) grid_dependency_wait();   // the runs
+                    const int32_t nruns = lo.runs[t.row0].count;
+                    for (int32_t r = 0; ok && r < nruns; ++r) {
+                        const int32_t a = lo.runs[t.row0 + r].adapter;
+                        for (int32_t r0 = 0; r0 < lo.R; r0 += t_ranks) {
+                            if (!mbar_wait(smem_u32(&empty[s]), phase, abort_flag, DEVERR_TIMEOUT_PRODUCER)) {
+                                ok = false;
+                                break;
+                            }
+                            // warp 10 cannot wait for `empty` itself: it skips the K stages, and a parity
+                            // tells neighbouring phases apart only
+                            mbar_arrive(smem_u32(&t_go[s]));
+                            const uint32_t ws = smem_u32(smem + s * g.stage_bytes);
+                            if (CG == 2) {
+                                if (crank == 0) mbar_expect_tx(smem_u32(&full[s]), 2 * W_TILE);
+                                tma_load_3d_pair(ws, &bmap, r0, n0, a, map_to_rank(smem_u32(&full[s]), 0), pol_x);
+                            } else {
+                                mbar_expect_tx(smem_u32(&full[s]), W_TILE);
+                                tma_load_3d(ws, &bmap, r0, n0, a, smem_u32(&full[s]), pol_x);
+                            }
+                            if (++s == S) {
+                                s = 0;
+                                phase ^= 1;
+                            }
+                        }
+                    }
+                }
             }
         }
         __syncwarp();
+    } else if (LORA == LORA_MMA && warp == LORA_WARP) {
+        // ------------------------------------------------------------ t into the low-rank stages
+        if (g.early) grid_dependency_wait();
+        uint32_t q = 0, phases = 0;   // phases: one bit per stage
+        bool ok = true;
+        for (int32_t id = cid; ok && lora_here && id < total; id += ncl) {
+            decode_tile(segs, nseg, g, id, WT, t);
+            q += (uint32_t)(kb1 - kb0);
+            const int32_t hs = t.ts / CG;
+            const int32_t row0 = t.row0 + (CG == 2 ? (int32_t)crank * hs : 0);
+            const int32_t nruns = lo.runs[t.row0].count;
+            for (int32_t r = 0; ok && r < nruns; ++r) {
+                const Run run = lo.runs[t.row0 + r];
+                for (int32_t r0 = 0; r0 < lo.R; r0 += t_ranks, ++q) {
+                    const uint32_t s = q % S;
+                    if (!warp_wait(smem_u32(&t_go[s]), (phases >> s) & 1, abort_flag, DEVERR_TIMEOUT_CONVERT)) {
+                        ok = false;
+                        break;
+                    }
+                    phases ^= 1u << s;
+                    write_t_tile(smem + s * g.stage_bytes + W_TILE, row0, hs, run, r0, lo, lane, bf16);
+                    asm volatile("fence.proxy.async;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (CG == 2) mbar_arrive_cluster(map_to_rank(smem_u32(&full[s]), 0));
+                        else mbar_arrive(smem_u32(&full[s]));
+                    }
+                }
+            }
+        }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA (the pair's first CTA)
         if ((CG == 1 || crank == 0) && elect_one()) {
@@ -404,6 +539,35 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                         phase ^= 1;
                     }
                 }
+                if (LORA == LORA_MMA && ok && lora_here) {
+                    if (g.early) grid_dependency_wait();
+                    const int32_t nruns = lo.runs[t.row0].count;
+                    const uint32_t idesc_t = instr_desc_mn(bf16, WT, t.ts);
+                    const uint64_t bk0 = smem_desc(smem_u32(smem), 16, 1024, 2);   // B's rows are K-major
+                    for (int32_t r = 0; ok && r < nruns; ++r) {
+                        for (int32_t r0 = 0; r0 < lo.R; r0 += t_ranks) {
+                            if (!mbar_wait(smem_u32(&full[s]), phase, abort_flag, DEVERR_TIMEOUT_MMA)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const uint64_t ad = bk0 + s * stage_step, bd = bd0 + s * stage_step;
+                            const int steps = (min(t_ranks, lo.R - r0) + 15) / 16;
+                            for (int part = 0; part < lo.parts; ++part)
+                                for (int kk = 0; kk < steps; ++kk) {
+                                    const uint64_t td = bd + (uint64_t)((part * t_ranks) / 8 + kk * 2);
+                                    if (CG == 2) tc_mma_pair(d, ad + kk * 2, td, idesc_t, 1u);
+                                    else tc_mma(d, ad + kk * 2, td, idesc_t, 1u);
+                                }
+                            if (CG == 2) tc_commit_pair(smem_u32(&empty[s]));
+                            else tc_commit(smem_u32(&empty[s]));
+                            if (++s == S) {
+                                s = 0;
+                                phase ^= 1;
+                            }
+                        }
+                    }
+                }
                 if (!ok) break;
                 if (CG == 2) tc_commit_pair(smem_u32(&acc_full[acc]));
                 else tc_commit(smem_u32(&acc_full[acc]));
@@ -425,7 +589,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
             const int64_t col = t.n0 + (CG == 2 ? (int32_t)crank * WROWS : 0) + nl;
             const bool n_ok = col < p.N;
             float bias = 0.f;
-            if (LORA && lo.bias && n_ok)
+            if (LORA != LORA_NONE && lo.bias && n_ok)
                 bias = half_bits_to_float(static_cast<const uint16_t*>(lo.bias)[col * lo.bias_s], bf16);
             if (!warp_wait(smem_u32(&acc_full[acc]), (n >> 1) & 1, abort_flag, DEVERR_TIMEOUT_EPILOGUE)) break;
             tc_fence_after();
@@ -597,7 +761,7 @@ inline bool make_plan(const Problem& p, bool dense, bool early, int sm_count, in
         g.off_red = g.stages * g.stage_bytes;
         g.off_seg = g.off_red + red;
         g.off_bar = (g.off_seg + (int)segs * (int)sizeof(Seg) + 15) & ~15;
-        out->smem_bytes = g.off_bar + 8 * (2 * g.stages + 6) + 1024;
+        out->smem_bytes = g.off_bar + 8 * (3 * g.stages + 6) + 1024;
         if (out->smem_bytes <= SMEM_LIMIT) break;
     }
     if (g.stages < 2) return false;
@@ -650,8 +814,8 @@ inline bool cached_plan(const Problem& p, bool dense, bool early, int sm_count, 
     return cache.get(key, out, [&](Plan* pl) { return make_plan(p, dense, early, sm_count, forced_cg, enc, pl); });
 }
 
-template <int CG, bool LORA>
-int launch_kernel(const Plan& pl, const Problem& p, const Lora& lo, cudaStream_t stream) {
+template <int CG, int LORA>
+int launch_kernel(const Plan& pl, const CUtensorMap& bm, const Problem& p, const Lora& lo, cudaStream_t stream) {
     auto kern = gemm_kernel<CG, LORA>;
     static std::atomic<uint64_t> configured{0};
     if (!set_smem_limit_once(kern, SMEM_LIMIT, configured)) return SGMV_ERR_CUDA;
@@ -665,17 +829,37 @@ int launch_kernel(const Plan& pl, const Problem& p, const Lora& lo, cudaStream_t
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)pl.grid);
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(threads_of(LORA));
     cfg.dynamicSmemBytes = (size_t)pl.smem_bytes;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = csize > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, pl.xm, pl.wm, p, pl.geo, lo) == cudaSuccess ? SGMV_OK : SGMV_ERR_LAUNCH;
+    return cudaLaunchKernelEx(&cfg, kern, pl.xm, pl.wm, bm, p, pl.geo, lo) == cudaSuccess ? SGMV_OK : SGMV_ERR_LAUNCH;
 }
 
-template <bool LORA>
-int launch(const Plan& pl, const Problem& p, const Lora& lo, cudaStream_t stream) {
-    return pl.cg == 2 ? launch_kernel<2, LORA>(pl, p, lo, stream) : launch_kernel<1, LORA>(pl, p, lo, stream);
+template <int LORA>
+int launch(const Plan& pl, const CUtensorMap& bm, const Problem& p, const Lora& lo, cudaStream_t stream) {
+    return pl.cg == 2 ? launch_kernel<2, LORA>(pl, bm, p, lo, stream) : launch_kernel<1, LORA>(pl, bm, p, lo, stream);
+}
+
+// Rows of the token tiles that the kernel cuts `rows` dense rows into.
+inline int32_t dense_tile_rows(const Geo& g, int cg) {
+    const int32_t rows = g.dense_rows, nt = (rows + g.tn - 1) / g.tn, step = 16 * cg;
+    return nt > 0 ? ((rows + nt - 1) / nt + step - 1) / step * step : step;
+}
+
+// Tensor map of lora_b (adapters, N, R) for LORA_MMA; false where TMA cannot read it.
+inline bool encode_b(const Lora& lo, int64_t N, int64_t adapters, EncodeTiledFn enc, CUtensorMap* out) {
+    if (!enc || !lo.b_vec || lo.R % 8 || lo.b_ns < lo.R || adapters >= (int64_t(1) << 31)) return false;
+    if (lo.b_ns >= (int64_t(1) << 38) || lo.b_as >= (int64_t(1) << 38)) return false;
+    if (adapters > 1 && lo.b_as < (N - 1) * lo.b_ns + lo.R) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)lo.R, (cuuint64_t)N, (cuuint64_t)adapters};
+    const cuuint64_t strides[2] = {(cuuint64_t)(lo.b_ns * 2),
+                                   (cuuint64_t)(adapters > 1 ? lo.b_as * 2 : (N * lo.b_ns * 2 + 15) / 16 * 16)};
+    const cuuint32_t box[3] = {64, WROWS, 1}, ones[3] = {1, 1, 1};
+    return enc(out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(lo.b), dims, strides, box, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace grp

@@ -22,24 +22,52 @@ __device__ __forceinline__ int32_t block_adapter(const Problem& p, int64_t row, 
     return *s_adapter;
 }
 
-// row_adapter[r] for every row: one thread per row scans the segments, which
-// the block stages in shared memory a few at a time.
+// The adapter of every row, and for the tensor-core form the runs of rows that
+// share one in each token tile of tile_rows (at most 256) rows.  One block per
+// tile, one thread per row: it scans the segments, which the block stages in
+// shared memory 256 at a time; a run starts where the adapter changes.
 constexpr int ROWS_THREADS = 256;
-__global__ void __launch_bounds__(ROWS_THREADS) row_adapter_kernel(Problem p, int32_t* row_adapter, int64_t rows) {
+__global__ void __launch_bounds__(ROWS_THREADS)
+row_runs_kernel(Problem p, int32_t* row_adapter, grp::Run* runs, int32_t tile_rows, int64_t rows) {
     __shared__ Segment s_seg[ROWS_THREADS];
+    __shared__ int32_t s_a[ROWS_THREADS + 1];
+    __shared__ int32_t s_warp[ROWS_THREADS / 32];
     tc::grid_dependency_wait();
     tc::grid_dependents_launch();
-    const int64_t row = (int64_t)blockIdx.x * ROWS_THREADS + threadIdx.x;
+    const int tid = threadIdx.x;
+    const int64_t row0 = (int64_t)blockIdx.x * tile_rows, row = row0 + tid;
+    const bool mine = tid < tile_rows && row < rows;
     int32_t a = -1;
     for (int64_t base = 0; base < p.batches; base += ROWS_THREADS) {
         __syncthreads();
-        if (base + threadIdx.x < p.batches) s_seg[threadIdx.x] = load_segment(p, base + threadIdx.x);
+        if (base + tid < p.batches) s_seg[tid] = load_segment(p, base + tid);
         __syncthreads();
         const int n = (int)min((int64_t)ROWS_THREADS, p.batches - base);
         for (int i = 0; i < n; ++i)
             if (row >= s_seg[i].row0 && row < s_seg[i].row0 + s_seg[i].rows) a = (int32_t)s_seg[i].adapter;
     }
-    if (row < rows) row_adapter[row] = a;
+    if (!mine) a = -1;
+    if (mine) row_adapter[row] = a;
+    if (!runs) return;
+    s_a[tid + 1] = a;
+    if (tid == 0) s_a[0] = -1;
+    __syncthreads();
+    const bool begins = a >= 0 && s_a[tid] != a;
+    const unsigned mask = __ballot_sync(0xffffffffu, begins);
+    if (tid % 32 == 0) s_warp[tid / 32] = __popc(mask);
+    __syncthreads();
+    int32_t at = __popc(mask & ((1u << (tid % 32)) - 1)), total = 0;
+    for (int w = 0; w < ROWS_THREADS / 32; ++w) {
+        if (w < tid / 32) at += s_warp[w];
+        total += s_warp[w];
+    }
+    if (begins) {
+        int32_t end = tid + 1;
+        while (end < ROWS_THREADS && s_a[end + 1] == a) ++end;
+        grp::Run r{a, (int32_t)row, (int32_t)(row0 + end), total};
+        runs[row0 + at] = r;
+    }
+    if (tid == 0 && total == 0) runs[row0] = grp::Run{-1, 0, 0, 0};
 }
 
 // t[row, j] = sum_k x^[row, k] * A[a][j, k] in fp32 for four ranks per block;
@@ -191,10 +219,12 @@ int launch_dependent(void (*kern)(KArgs...), dim3 grid, int threads, cudaStream_
     return cudaLaunchKernelEx(&cfg, kern, KArgs(args)...) == cudaSuccess ? SGMV_OK : SGMV_ERR_LAUNCH;
 }
 
-inline int launch_row_adapter(const Problem& p, int32_t* row_adapter, int64_t rows, cudaStream_t stream) {
-    const int64_t blocks = (rows + ROWS_THREADS - 1) / ROWS_THREADS;
-    if (blocks > 0x7fffffff) return SGMV_ERR_TOO_LARGE;
-    return launch_dependent(row_adapter_kernel, dim3((unsigned)blocks), ROWS_THREADS, stream, p, row_adapter, rows);
+// runs: null where only the rows' adapters are wanted.
+inline int launch_row_runs(const Problem& p, int32_t* row_adapter, grp::Run* runs, int32_t tile_rows, int64_t rows,
+                           cudaStream_t stream) {
+    const int64_t blocks = (rows + tile_rows - 1) / tile_rows;
+    return launch_dependent(row_runs_kernel, dim3((unsigned)blocks), ROWS_THREADS, stream, p, row_adapter, runs, tile_rows,
+                            rows);
 }
 
 inline int launch_row_shrink(const Problem& p, float* t, int32_t* row_adapter, int64_t rows, cudaStream_t stream) {

@@ -456,6 +456,8 @@ namespace {
 // Rows up to which a shared projection's low-rank input is computed row by row
 // (an adapter per row) instead of in 128-row blocks of one adapter.
 constexpr int64_t kRowShrinkRows = 256;
+// Rows per segment from which the low-rank part runs on the tensor cores.
+constexpr int64_t kMmaRunRows = 16;
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
@@ -607,7 +609,7 @@ struct LoraCall {
     int64_t rows;
     bool low_rank;            // there is a low-rank part to compute
     bool empty;
-    int64_t off_t, off_part;  // workspace: row adapters, t, partial sums of t
+    int64_t off_runs, off_t, off_part;  // workspace: row adapters, runs, t, partial sums of t
 };
 
 int validate_lora(const sgmv_tensor* x, const sgmv_tensor* w, const sgmv_tensor* bias, const sgmv_tensor* a,
@@ -671,7 +673,8 @@ int validate_lora(const sgmv_tensor* x, const sgmv_tensor* w, const sgmv_tensor*
         lo.bias = bias->data;
         lo.bias_s = bias->stride[0];
     }
-    call->off_t = align256(call->rows * 4);
+    call->off_runs = align256(call->rows * 4);
+    call->off_t = call->off_runs + align256(call->rows * (int64_t)sizeof(grp::Run));
     call->off_part = call->off_t + align256(call->rows * R * 4);
     return SGMV_OK;
 }
@@ -680,6 +683,8 @@ int validate_lora(const sgmv_tensor* x, const sgmv_tensor* w, const sgmv_tensor*
 struct LoraPlan {
     int variant;
     grp::Plan base;
+    bool mma;                                        // the low-rank part as K steps (LORA_MMA)
+    CUtensorMap bm;
     enum { NONE, BY_ROW, BLOCKS, PRODUCT } shrink;   // how t is computed
     int splits;                                      // BLOCKS: parts of K
     grp::Plan product;                               // PRODUCT: t as a grouped product
@@ -697,6 +702,13 @@ int choose_lora(LoraCall* c, const DeviceInfo& dev, int forced, char* ws, size_t
                                               tc::encode_fn(), &pl->base);
     pl->variant = large_variant(tc_ok, forced);
     if (pl->variant < 0) return pl->variant;
+    // K steps pay from a few rows per segment on: a run costs an MMA over its whole token tile
+    pl->mma = tc_ok && c->low_rank && c->rows >= kMmaRunRows * c->shrink.batches &&
+              grp::encode_b(c->lo, c->base.N, c->shrink.lora_num, tc::encode_fn(), &pl->bm);
+    if (pl->mma) {
+        c->lo.runs = reinterpret_cast<const grp::Run*>(ws + c->off_runs);
+        c->lo.parts = c->base.out_dt == SGMV_F32 ? 3 : 2;
+    }
     pl->shrink = c->low_rank ? LoraPlan::BY_ROW : LoraPlan::NONE;
     pl->splits = 1;
     if (c->low_rank && tc && c->rows > kRowShrinkRows) {
@@ -718,21 +730,26 @@ int run_lora(const LoraCall& c, const DeviceInfo& dev, const LoraPlan& pl, char*
     int32_t* rows = reinterpret_cast<int32_t*>(ws);
     float* t = reinterpret_cast<float*>(ws + c.off_t);
     const Call shrink{c.shrink, 0, false};
+    // row_shrink_kernel finds the rows' adapters by itself
+    if (pl.shrink != LoraPlan::NONE && (pl.mma || pl.shrink != LoraPlan::BY_ROW)) {
+        grp::Run* runs = pl.mma ? reinterpret_cast<grp::Run*>(ws + c.off_runs) : nullptr;
+        const int32_t tile = pl.mma ? grp::dense_tile_rows(pl.base.geo, pl.base.cg) : lora::ROWS_THREADS;
+        if ((rc = lora::launch_row_runs(c.shrink, rows, runs, tile, c.rows, st))) return rc;
+    }
     switch (pl.shrink) {
-        case LoraPlan::BY_ROW:
-            if ((rc = lora::launch_row_shrink(c.shrink, t, rows, c.rows, st))) return rc;
-            break;
+        case LoraPlan::BY_ROW: rc = lora::launch_row_shrink(c.shrink, t, rows, c.rows, st); break;
         case LoraPlan::BLOCKS:
-            if ((rc = lora::launch_row_adapter(c.shrink, rows, c.rows, st))) return rc;
-            if ((rc = launch_shrink(shrink, dev, pl.splits, reinterpret_cast<float*>(ws + c.off_part), st))) return rc;
+            rc = launch_shrink(shrink, dev, pl.splits, reinterpret_cast<float*>(ws + c.off_part), st);
             break;
         case LoraPlan::PRODUCT:
-            if ((rc = lora::launch_row_adapter(c.shrink, rows, c.rows, st))) return rc;
-            if ((rc = grp::launch<false>(pl.product, c.shrink, grp::Lora{}, st))) return rc;
+            rc = grp::launch<grp::LORA_NONE>(pl.product, CUtensorMap{}, c.shrink, grp::Lora{}, st);
             break;
         default: break;
     }
-    if (pl.variant == SGMV_VARIANT_TC) return grp::launch<true>(pl.base, c.base, c.lo, st);
+    if (rc) return rc;
+    if (pl.variant == SGMV_VARIANT_TC)
+        return pl.mma ? grp::launch<grp::LORA_MMA>(pl.base, pl.bm, c.base, c.lo, st)
+                      : grp::launch<grp::LORA_FMA>(pl.base, CUtensorMap{}, c.base, c.lo, st);
     return lora::launch_lora_simt(c.base, c.lo, c.rows, st);
 }
 
@@ -753,7 +770,7 @@ int sgmv_grouped_gemm(const sgmv_tensor* inputs, const sgmv_tensor* weights, con
     const int v = choose_grouped(c, dev, g_forced_variant.load(), &pl);
     if (v < 0) return v;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (v == SGMV_VARIANT_TC) return grp::launch<false>(pl, c.p, grp::Lora{}, st);
+    if (v == SGMV_VARIANT_TC) return grp::launch<grp::LORA_NONE>(pl, CUtensorMap{}, c.p, grp::Lora{}, st);
     return launch_simt(c, dev, st);
 }
 

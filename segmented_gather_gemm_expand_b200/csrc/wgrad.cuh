@@ -296,7 +296,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
                     if (!any)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0.f;
-                    grp::finish<32, false>(v, (int64_t)e * g.rows_per_group + n0 + c, min(32, valid - c), col, col < p.N,
+                    grp::finish<32, grp::LORA_NONE>(v, (int64_t)e * g.rows_per_group + n0 + c, min(32, valid - c), col, col < p.N,
                                            0.f, p, none, bf16);
                 }
             }
