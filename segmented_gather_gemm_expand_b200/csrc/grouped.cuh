@@ -62,6 +62,7 @@ enum LoraMode { LORA_NONE = 0, LORA_FMA = 1, LORA_MMA = 2 };
 constexpr int threads_of(int lora) { return 64 + 32 * EPI_WARPS + (lora == LORA_MMA ? 32 : 0); }
 constexpr int NUM_XMAPS = 4;            // x boxes of 16, 32, 64, 128 rows
 constexpr int MAX_SPLITS = 8;
+constexpr int STAGE_ROWS = 32 * 64;     // epilogue: a warp's 32 x 32 halves
 constexpr int BAND = 8;                 // token tiles walked together before the next weight tile
 constexpr int SEG_CAP = 4096;           // most segments a launch takes
 constexpr int SMEM_LIMIT = 232448 - 1024;
@@ -77,7 +78,8 @@ struct Geo {
     int32_t tn;           // most tokens per tile
     int32_t splits;       // CTAs that share a tile by cutting K (single form)
     int32_t stages, stage_bytes;
-    int32_t off_red, off_seg, off_bar;
+    int32_t off_out, off_red, off_seg, off_bar;
+    int32_t out_vec;      // half output in 16-byte pieces
     int32_t acc_stride, tmem_cols;
     int32_t w_mn;         // the weights' N axis is the contiguous one
     int32_t dense_rows;   // >= 0: one segment of that many rows with group 0; -1: the call's segments
@@ -200,19 +202,27 @@ __device__ __forceinline__ void add_lora(float (&v)[NT], int64_t row, int valid,
 }
 
 // Adds the low-rank part, the bias or the old output, rounds once and stores
-// rows row .. row + valid - 1 of column n.
+// rows row .. row + valid - 1 of column n (= the warp's first column + lane).
+//
+// fp32 output: a warp's store is a row's 32 columns, 128 bytes.  Half output:
+// that would be 32 stores of 64 bytes for 32 rows, and a tile of 256 x 256
+// spent 8500 cycles on them; so the warp turns its 32 x 32 piece round in
+// shared memory (`stage`, 64 bytes per row) and stores 8 rows at a time, 16
+// bytes per lane.  That needs 16-byte aligned output rows (p.off, the warp's
+// first column, is a multiple of 32) and 32 columns inside the matrix; other
+// warps store element by element.
 template <int NT, int LORA>
 __device__ __forceinline__ void finish(float (&v)[NT], int64_t row, int valid, int64_t n, bool n_ok, float bias,
-                                       const Problem& p, const Lora& lo, bool bf16) {
+                                       const Problem& p, const Lora& lo, bool bf16, uint16_t* stage, bool out_vec) {
     if (valid <= 0) return;
     if (LORA == LORA_FMA && lo.R > 0) add_lora<NT>(v, row, valid, n, n_ok, lo, bf16);
     if (LORA != LORA_NONE) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) v[j] += bias;
     }
-    if (!n_ok) return;
-    const int64_t base = row * p.H + p.off + n;
+    const int64_t base = row * p.H + n;
     if (p.out_dt == SGMV_F32) {
+        if (!n_ok) return;
         float* o = static_cast<float*>(p.out) + base;
         if (p.add) {
             float old[NT];
@@ -224,20 +234,45 @@ __device__ __forceinline__ void finish(float (&v)[NT], int64_t row, int valid, i
 #pragma unroll
         for (int j = 0; j < NT; ++j)
             if (j < valid) o[j * p.H] = v[j];
-    } else {
-        const bool ob = p.out_dt == SGMV_BF16;
-        uint16_t* o = static_cast<uint16_t*>(p.out) + base;
+        return;
+    }
+    const bool ob = p.out_dt == SGMV_BF16;
+    const int lane = threadIdx.x % 32;
+    if (out_vec && n - lane + 32 <= p.N) {
+        const int r = lane / 4, c = (lane % 4) * 8;
+        uint16_t* o = static_cast<uint16_t*>(p.out) + (base - lane + r * p.H + c);
+        uint4* s = reinterpret_cast<uint4*>(stage + r * 32 + c);
         if (p.add) {
-            uint16_t old[NT];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) old[j] = j < valid ? o[j * p.H] : (uint16_t)0;
+            for (int j = 0; j < NT; j += 8)
+                if (j + r < valid) s[j * 4] = *reinterpret_cast<const uint4*>(o + j * p.H);
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < NT; ++j) v[j] += half_bits_to_float(old[j], ob);
+            for (int j = 0; j < NT; ++j)
+                if (j < valid) v[j] += half_bits_to_float(stage[j * 32 + lane], ob);
+            __syncwarp();
         }
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-            if (j < valid) o[j * p.H] = (uint16_t)float_to_half_bits(v[j], ob);
+        for (int j = 0; j < NT; ++j) stage[j * 32 + lane] = (uint16_t)float_to_half_bits(v[j], ob);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < NT; j += 8)
+            if (j + r < valid) *reinterpret_cast<uint4*>(o + j * p.H) = s[j * 4];
+        __syncwarp();
+        return;
     }
+    if (!n_ok) return;
+    uint16_t* o = static_cast<uint16_t*>(p.out) + base;
+    if (p.add) {
+        uint16_t old[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) old[j] = j < valid ? o[j * p.H] : (uint16_t)0;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) v[j] += half_bits_to_float(old[j], ob);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+        if (j < valid) o[j * p.H] = (uint16_t)float_to_half_bits(v[j], ob);
 }
 
 // The part of v that the parts before have not covered, rounded to the half
@@ -582,6 +617,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
         }
         const int quad = warp % 4, half = (warp - 2) / 4;
         const int nl = quad * 32 + lane;
+        uint16_t* stage = reinterpret_cast<uint16_t*>(smem + g.off_out + (warp - 2) * STAGE_ROWS);
         uint32_t n = 0;
         for (int32_t id = cid; id < total; id += ncl, ++n) {
             decode_tile(segs, nseg, g, id, WT, t);
@@ -599,7 +635,8 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                     float v[32];
                     tmem_ld32(taddr + (uint32_t)c, reinterpret_cast<uint32_t(&)[32]>(v));
                     tmem_ld_wait();
-                    finish<32, LORA>(v, (int64_t)t.row0 + c, min(32, t.rows - c), col, n_ok, bias, p, lo, bf16);
+                    finish<32, LORA>(v, (int64_t)t.row0 + c, min(32, t.rows - c), col, n_ok, bias, p, lo, bf16,
+                                     stage, g.out_vec);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -643,7 +680,8 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             if (j0 + j < cnt) v[j] += rp[(src * tw + j0 + j) * WROWS];
-                    finish<8, LORA>(v, (int64_t)t.row0 + t0 + j0, min(8, cnt - j0), col, n_ok, bias, p, lo, bf16);
+                    finish<8, LORA>(v, (int64_t)t.row0 + t0 + j0, min(8, cnt - j0), col, n_ok, bias, p, lo, bf16,
+                                    stage, g.out_vec);
                 }
                 __syncwarp();
                 if (lane < (int)csize) mbar_arrive_cluster(map_to_rank(smem_u32(red_free), (uint32_t)lane));
@@ -693,6 +731,11 @@ inline bool supports(const Problem& p) {
     const int64_t rows = p.x_rows < p.out_rows ? p.x_rows : p.out_rows;
     if ((rows / 16 + p.batches + 1) * ((p.N + WROWS - 1) / WROWS) >= lim) return false;
     return p.batches <= SEG_CAP;
+}
+
+// Half output rows can be written as 16-byte pieces.
+inline bool out_vec_ok(const Problem& p) {
+    return p.out_dt != SGMV_F32 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.H % 8 == 0;
 }
 
 struct Shape {
@@ -750,6 +793,7 @@ inline bool make_plan(const Problem& p, bool dense, bool early, int sm_count, in
     g.w_mn = !(p.w_ks == 1 && (p.w_ns * 2) % 16 == 0 && p.w_ns >= p.K);
     g.dense_rows = dense ? (int32_t)rows : -1;
     g.early = early ? 1 : 0;
+    g.out_vec = out_vec_ok(p);
     const int64_t segs = dense ? 1 : p.batches;
     g.keep_w = rows > (int64_t)sh.tn * segs ? 1 : 0;
     g.acc_stride = sh.tn < 32 ? 32 : sh.tn;
@@ -758,7 +802,8 @@ inline bool make_plan(const Problem& p, bool dense, bool early, int sm_count, in
     g.stage_bytes = W_TILE + (sh.tn / sh.cg) * 128;
     const int red = sh.splits > 1 ? sh.splits * ((sh.tn + sh.splits - 1) / sh.splits) * WROWS * 4 : 0;
     for (g.stages = 12; g.stages >= 2; --g.stages) {
-        g.off_red = g.stages * g.stage_bytes;
+        g.off_out = g.stages * g.stage_bytes;
+        g.off_red = g.off_out + EPI_WARPS * STAGE_ROWS;
         g.off_seg = g.off_red + red;
         g.off_bar = (g.off_seg + (int)segs * (int)sizeof(Seg) + 15) & ~15;
         out->smem_bytes = g.off_bar + 8 * (3 * g.stages + 6) + 1024;

@@ -38,7 +38,8 @@ constexpr int SMEM_LIMIT = grp::SMEM_LIMIT;
 struct Geo {
     int32_t kblk, nblk, ts;     // tiles along K and N; columns of dY per tile (multiple of 32)
     int32_t stages;
-    int32_t off_seg, off_exp, off_bar;
+    int32_t off_out, off_seg, off_exp, off_bar;
+    int32_t out_vec;            // half dW in 16-byte pieces
     int32_t acc_stride, tmem_cols;
     int64_t rows_per_group;     // rows of dW between two indexes
 };
@@ -277,6 +278,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
         // ------------------------------------------------------------ epilogue
         const int quad = warp % 4, half = (warp - 2) / 4;
         const grp::Lora none = {};
+        uint16_t* stage = reinterpret_cast<uint16_t*>(smem + g.off_out + (warp - 2) * grp::STAGE_ROWS);
         uint32_t n = 0;
         for (int32_t id = cid; id < total; id += ncl, ++n) {
             int32_t e, k0, n0;
@@ -297,7 +299,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0.f;
                     grp::finish<32, grp::LORA_NONE>(v, (int64_t)e * g.rows_per_group + n0 + c, min(32, valid - c), col, col < p.N,
-                                           0.f, p, none, bf16);
+                                           0.f, p, none, bf16, stage, g.out_vec);
                 }
             }
             tc_fence_before();
@@ -377,11 +379,13 @@ inline bool make_plan(const Problem& p, int64_t y_cs, int64_t out_gs, int64_t ou
     g.ts = (int32_t)(((p.K + nt - 1) / nt + 31) / 32 * 32);
     g.nblk = (int32_t)((p.K + g.ts - 1) / g.ts);
     g.rows_per_group = p.lora_num > 1 ? out_gs / p.H : 0;
+    g.out_vec = grp::out_vec_ok(p);
     g.acc_stride = g.ts;
     g.tmem_cols = 32;
     while (g.tmem_cols < 2 * g.acc_stride) g.tmem_cols *= 2;
     for (g.stages = 7; g.stages >= 2; --g.stages) {
-        g.off_seg = g.stages * STAGE;
+        g.off_out = g.stages * STAGE;
+        g.off_seg = g.off_out + EPI_WARPS * grp::STAGE_ROWS;
         g.off_exp = g.off_seg + (int)p.batches * (int)sizeof(Seg);
         g.off_bar = (g.off_exp + (int)p.lora_num * (int)sizeof(Exp) + 15) & ~15;
         out->smem_bytes = g.off_bar + 8 * (3 * g.stages + 4) + 1024;
