@@ -357,7 +357,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
             mbar_init(smem_u32(&acc_full[i]), 1);
             mbar_init(smem_u32(&acc_empty[i]), CG * EPI_WARPS);
         }
-        mbar_init(smem_u32(red_full), csize * EPI_WARPS);
+        mbar_init(smem_u32(red_full), 1);   // the expected bytes, then the stores' own counts
         mbar_init(smem_u32(red_free), csize * EPI_WARPS);
         fence_barrier_init();
     }
@@ -505,6 +505,14 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                     }
                 }
             }
+            // the commits of the other CTA's MMAs arrive here: none may be under way when this CTA ends
+            for (uint32_t i = 0; CG == 2 && ok && i < S; ++i) {
+                ok = mbar_wait(smem_u32(&empty[s]), phase, abort_flag, DEVERR_TIMEOUT_PRODUCER);
+                if (++s == S) {
+                    s = 0;
+                    phase ^= 1;
+                }
+            }
         }
         __syncwarp();
     } else if (LORA == LORA_MMA && warp == LORA_WARP) {
@@ -618,7 +626,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
         const int quad = warp % 4, half = (warp - 2) / 4;
         const int nl = quad * 32 + lane;
         uint16_t* stage = reinterpret_cast<uint16_t*>(smem + g.off_out + (warp - 2) * STAGE_ROWS);
-        uint32_t n = 0;
+        uint32_t n = 0, reds = 0;   // reds: exchanges in which this CTA owned tokens
         for (int32_t id = cid; id < total; id += ncl, ++n) {
             decode_tile(segs, nseg, g, id, WT, t);
             const uint32_t acc = n & 1;
@@ -640,51 +648,62 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    if (CG == 2) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[acc]), 0));
+                if (lane == 0 && id + 2 * ncl < total) {   // somebody waits for it
+                    if (CG == 2) mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[acc]), 0));
                     else mbar_arrive(smem_u32(&acc_empty[acc]));
                 }
             } else {
-                // partial sums go to the CTA that owns the token: red[source][token][weight row]
-                const int tw = (t.ts + (int)csize - 1) / (int)csize;
-                const uint32_t red = smem_u32(smem + g.off_red);
-                if (!warp_wait_cluster(smem_u32(red_free), (n & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_EPILOGUE)) break;
-                for (int c = half * 32; c < t.ts; c += 64) {
+                // Partial sums go to the CTA that owns the token, four tokens of a weight row
+                // (16 bytes) at a time: red[source][token / 4][weight row][token % 4].  The
+                // stores count themselves at the owner's barrier, so nobody fences.
+                const int tw = ((t.ts + (int)csize - 1) / (int)csize + 3) & ~3;
+                const uint32_t red = smem_u32(smem + g.off_red) + (crank * (tw / 4) * WROWS + nl) * 16;
+                const int t0 = (int)crank * tw, cnt = min(tw, t.rows - t0);
+                if (cnt > 0 && warp == 2 && lane == 0)
+                    mbar_expect_tx(smem_u32(red_full), csize * (uint32_t)((cnt + 3) / 4) * WROWS * 16u);
+                if (n > 0 && !warp_wait_cluster(smem_u32(red_free), (n & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_EPILOGUE))
+                    break;
+                for (int c = half * 32; c < t.rows; c += 64) {
                     float v[32];
                     tmem_ld32(taddr + (uint32_t)c, reinterpret_cast<uint32_t(&)[32]>(v));
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
+                    for (int j = 0; j < 32; j += 4) {
                         const int tok = c + j;
                         if (tok < t.rows) {
-                            const int owner = tok / tw;
-                            st_cluster_f32(map_to_rank(red + ((((int)crank * tw + tok - owner * tw) * WROWS + nl) << 2),
-                                                       (uint32_t)owner),
-                                           v[j]);
+                            const uint32_t owner = (uint32_t)(tok / tw);
+                            st_async_v4(map_to_rank(red + ((tok - (int)owner * tw) / 4) * (WROWS * 16), owner),
+                                        map_to_rank(smem_u32(red_full), owner), v[j], v[j + 1], v[j + 2], v[j + 3]);
                         }
                     }
                 }
                 tc_fence_before();
-                fence_cluster();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&acc_empty[acc]));
-                if (lane < (int)csize) mbar_arrive_cluster(map_to_rank(smem_u32(red_full), (uint32_t)lane));
-                if (!warp_wait_cluster(smem_u32(red_full), n & 1, abort_flag, DEVERR_TIMEOUT_EPILOGUE)) break;
-                const int t0 = (int)crank * tw, cnt = min(tw, t.rows - t0);
-                const float* rp = reinterpret_cast<const float*>(smem + g.off_red) + nl;
-                for (int j0 = half * 8; j0 < cnt; j0 += 16) {
-                    float v[8];
+                if (cnt > 0) {
+                    if (!warp_wait_cluster(smem_u32(red_full), reds & 1, abort_flag, DEVERR_TIMEOUT_EPILOGUE)) break;
+                    ++reds;
+                    const float4* rp = reinterpret_cast<const float4*>(smem + g.off_red) + nl;
+                    for (int j0 = half * 8; j0 < cnt; j0 += 16) {
+                        float v[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = 0.f;
-                    for (int src = 0; src < (int)csize; ++src)
+                        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+                        for (int src = 0; src < (int)csize; ++src)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (j0 + j < cnt) v[j] += rp[(src * tw + j0 + j) * WROWS];
-                    finish<8, LORA>(v, (int64_t)t.row0 + t0 + j0, min(8, cnt - j0), col, n_ok, bias, p, lo, bf16,
-                                    stage, g.out_vec);
+                            for (int j = 0; j < 8; j += 4)
+                                if (j0 + j < cnt) {
+                                    const float4 f = rp[(src * (tw / 4) + (j0 + j) / 4) * WROWS];
+                                    v[j] += f.x;
+                                    v[j + 1] += f.y;
+                                    v[j + 2] += f.z;
+                                    v[j + 3] += f.w;
+                                }
+                        finish<8, LORA>(v, (int64_t)t.row0 + t0 + j0, min(8, cnt - j0), col, n_ok, bias, p, lo, bf16,
+                                        stage, g.out_vec);
+                    }
                 }
                 __syncwarp();
-                if (lane < (int)csize) mbar_arrive_cluster(map_to_rank(smem_u32(red_free), (uint32_t)lane));
+                if (lane < (int)csize && id + ncl < total) mbar_arrive_remote(map_to_rank(smem_u32(red_free), (uint32_t)lane));
             }
         }
     }
@@ -800,7 +819,7 @@ inline bool make_plan(const Problem& p, bool dense, bool early, int sm_count, in
     g.tmem_cols = 32;
     while (g.tmem_cols < 2 * g.acc_stride) g.tmem_cols *= 2;
     g.stage_bytes = W_TILE + (sh.tn / sh.cg) * 128;
-    const int red = sh.splits > 1 ? sh.splits * ((sh.tn + sh.splits - 1) / sh.splits) * WROWS * 4 : 0;
+    const int red = sh.splits > 1 ? sh.splits * (((sh.tn + sh.splits - 1) / sh.splits + 3) & ~3) * WROWS * 4 : 0;
     for (g.stages = 12; g.stages >= 2; --g.stages) {
         g.off_out = g.stages * g.stage_bytes;
         g.off_red = g.off_out + EPI_WARPS * STAGE_ROWS;

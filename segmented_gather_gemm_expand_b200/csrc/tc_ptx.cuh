@@ -303,15 +303,24 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
     return r;
 }
 
-// Barrier over every thread of the cluster; orders shared-memory accesses.
+// Barrier over every thread of the cluster.  Relaxed: it orders no memory (the
+// mbarriers' initialisation has a fence of its own), it only says that every
+// CTA of the cluster has come this far; the ordering form would wait for the
+// output stores.  Before the last one, a role must have waited for everything
+// that other CTAs still signal to its CTA.
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
-
 // Arrivals on a barrier of any CTA of the cluster (address from map_to_rank).
+// The plain form orders what the CTA's own threads see, which is enough to hand
+// back a buffer that was only read; the release form also orders this thread's
+// writes for the cluster, and waits until its global stores are performed.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -342,8 +351,13 @@ __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity,
     return __all_sync(0xffffffffu, ok);
 }
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Stores 16 bytes into the shared memory of a CTA of the cluster and counts
+// them at that CTA's mbarrier; nothing else orders or waits for them.
+__device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t bar, float a, float b, float c, float d) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(
+                     addr),
+                 "r"(bar), "f"(a), "f"(b), "f"(c), "f"(d)
+                 : "memory");
 }
 
 // TMA loads into this CTA whose bytes are counted by a barrier that may be in

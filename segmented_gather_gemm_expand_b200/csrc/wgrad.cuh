@@ -201,6 +201,14 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
                     }
                 }
             }
+            // the commits of the other CTA's MMAs arrive here: none may be under way when this CTA ends
+            for (uint32_t i = 0; ok && i < S; ++i) {
+                ok = mbar_wait(smem_u32(&empty[s]), phase, abort_flag, DEVERR_TIMEOUT_PRODUCER);
+                if (++s == S) {
+                    s = 0;
+                    phase ^= 1;
+                }
+            }
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -304,7 +312,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[acc]), 0));
+            if (lane == 0 && id + 2 * ncl < total) mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[acc]), 0));
         }
     }
 
