@@ -36,13 +36,16 @@
 //          enters as the sum of two half-precision parts (hi, and what is left
 //          of it, rounded), three where out is fp32: relative errors of 2^-16
 //          (2^-24) against out's own rounding of 2^-9 (2^-24).
-//   LORA_FMA   on the CUDA cores in the epilogue, in fp32: single tokens with an
-//          adapter each, or a B that TMA cannot read.
+//   LORA_FMA   on the CUDA cores in fp32, by the epilogue's warps while the K loop
+//          runs (they keep it in shared memory until the sums are there): single
+//          tokens with an adapter each, or a B that TMA cannot read.
 //
 // Every wait is bounded and reports a timeout through the device error word.
 #pragma once
 
 #include <cuda.h>
+
+#include <mutex>
 
 #include "common.cuh"
 #include "plan_cache.cuh"
@@ -78,7 +81,7 @@ struct Geo {
     int32_t tn;           // most tokens per tile
     int32_t splits;       // CTAs that share a tile by cutting K (single form)
     int32_t stages, stage_bytes;
-    int32_t off_out, off_red, off_seg, off_bar;
+    int32_t off_out, off_delta, off_red, off_seg, off_bar;
     int32_t out_vec;      // half output in 16-byte pieces
     int32_t acc_stride, tmem_cols;
     int32_t w_mn;         // the weights' N axis is the contiguous one
@@ -140,86 +143,74 @@ __device__ __forceinline__ void decode_tile(const Seg* segs, int32_t nseg, const
     t.group = s.group;
 }
 
-// v[j] += sum_k t[row + j, k] * B[adapter of row + j][n, k] for j < valid, in
-// fp32, 16 ranks at a time: B's piece of the lane's column stays in registers
-// while neighbouring tokens share an adapter, t is one broadcast read per warp.
-template <int NT>
-__device__ __forceinline__ void add_lora(float (&v)[NT], int64_t row, int valid, int64_t n, bool n_ok, const Lora& lo,
-                                         bool bf16) {
-    for (int r0 = 0; r0 < lo.R; r0 += 16) {
-        int cur = -1;
-        float b[16];
+// d[j] = sum_k t[row + j, k] * B[adapter of row + j][n, k] for j < valid, in
+// fp32, 16 ranks at a time.  The B pieces of all eight tokens are requested
+// before the first is used: decode batches have an adapter per token, and one
+// after the other their latencies add up (48 tokens: 51 us against 26).
+__device__ __forceinline__ void lora_delta(float (&d)[8], int64_t row, int valid, int64_t n, bool n_ok, const Lora& lo,
+                                           bool bf16) {
+    int a[8];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            if (j >= valid) continue;
-            const int a = lo.row_adapter[row + j];
-            if (a < 0) continue;
-            if (a != cur) {
-                cur = a;
-                const int64_t base = (int64_t)a * lo.b_as + n * lo.b_ns;
-                if (!n_ok) {
+    for (int j = 0; j < 8; ++j) {
+        d[j] = 0.f;
+        a[j] = j < valid ? lo.row_adapter[row + j] : -1;
+    }
+    const uint16_t* b = static_cast<const uint16_t*>(lo.b) + n * lo.b_ns;
+    const float* t = lo.t + row * lo.R;
+    int r0 = 0;
+    if (lo.b_vec && lo.R % 4 == 0) {
+        for (; r0 + 16 <= lo.R; r0 += 16) {
+            uint4 u[8][2];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) b[k] = 0.f;
-                } else if (lo.b_vec && r0 + 16 <= lo.R) {
-                    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(lo.b) + base + r0);
-                    const uint4 u0 = __ldg(q), u1 = __ldg(q + 1);
-                    const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+            for (int j = 0; j < 8; ++j) {
+                const bool on = a[j] >= 0 && n_ok;
+                const uint4* q = reinterpret_cast<const uint4*>(b + (int64_t)a[j] * lo.b_as + r0);
+                u[j][0] = on ? __ldg(q) : make_uint4(0, 0, 0, 0);
+                u[j][1] = on ? __ldg(q + 1) : make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float2 f = unpack2(w[k], bf16);
-                        b[2 * k] = f.x;
-                        b[2 * k + 1] = f.y;
+            for (int j = 0; j < 8; ++j) {
+                if (a[j] < 0) continue;
+                const float4* tp = reinterpret_cast<const float4*>(t + j * lo.R + r0);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t w[4] = {u[j][h].x, u[j][h].y, u[j][h].z, u[j][h].w};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float4 f = tp[h * 2 + k];
+                        const float2 b0 = unpack2(w[2 * k], bf16), b1 = unpack2(w[2 * k + 1], bf16);
+                        d[j] = fmaf(f.x, b0.x, d[j]);
+                        d[j] = fmaf(f.y, b0.y, d[j]);
+                        d[j] = fmaf(f.z, b1.x, d[j]);
+                        d[j] = fmaf(f.w, b1.y, d[j]);
                     }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        b[k] = r0 + k < lo.R
-                                   ? half_bits_to_float(__ldg(static_cast<const uint16_t*>(lo.b) + base +
-                                                              (int64_t)(r0 + k) * lo.b_ks),
-                                                        bf16)
-                                   : 0.f;
                 }
             }
-            const float* tp = lo.t + (row + j) * lo.R + r0;
-            float s0 = 0.f, s1 = 0.f;
-            if (lo.R % 16 == 0) {
-#pragma unroll
-                for (int k = 0; k < 16; k += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(tp + k);
-                    s0 = fmaf(f.x, b[k], s0);
-                    s1 = fmaf(f.y, b[k + 1], s1);
-                    s0 = fmaf(f.z, b[k + 2], s0);
-                    s1 = fmaf(f.w, b[k + 3], s1);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (r0 + k < lo.R) s0 = fmaf(tp[k], b[k], s0);
-            }
-            v[j] += s0 + s1;
         }
     }
+    for (; r0 < lo.R; ++r0)   // the last ranks, and B in any other layout
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (a[j] >= 0 && n_ok)
+                d[j] = fmaf(t[j * lo.R + r0],
+                            half_bits_to_float(__ldg(b + (int64_t)a[j] * lo.b_as + r0 * lo.b_ks), bf16), d[j]);
 }
 
-// Adds the low-rank part, the bias or the old output, rounds once and stores
-// rows row .. row + valid - 1 of column n (= the warp's first column + lane).
+// Adds the old output (add mode), rounds once and stores rows row .. row +
+// valid - 1 of column n (= the warp's first column + lane).
 //
 // fp32 output: a warp's store is a row's 32 columns, 128 bytes.  Half output:
-// that would be 32 stores of 64 bytes for 32 rows, and a tile of 256 x 256
-// spent 8500 cycles on them; so the warp turns its 32 x 32 piece round in
-// shared memory (`stage`, 64 bytes per row) and stores 8 rows at a time, 16
-// bytes per lane.  That needs 16-byte aligned output rows (p.off, the warp's
-// first column, is a multiple of 32) and 32 columns inside the matrix; other
-// warps store element by element.
-template <int NT, int LORA>
-__device__ __forceinline__ void finish(float (&v)[NT], int64_t row, int valid, int64_t n, bool n_ok, float bias,
-                                       const Problem& p, const Lora& lo, bool bf16, uint16_t* stage, bool out_vec) {
+// that would be NT stores of 64 bytes for NT rows, and a tile of 256 x 256
+// spent 8500 cycles on them; so the warp turns its piece round in shared memory
+// (`stage`) and stores 8 rows at a time, 16 bytes per lane: 32 tokens as pairs
+// (one packed conversion and one 4-byte store per pair and column, split again
+// after the read), 8 tokens as halves.  That needs 16-byte aligned output rows
+// and 32 columns inside the matrix; other warps store element by element.
+template <int NT>
+__device__ __forceinline__ void put(float (&v)[NT], int64_t row, int valid, int64_t n, const Problem& p, uint32_t* stage,
+                                    bool out_vec) {
     if (valid <= 0) return;
-    if (LORA == LORA_FMA && lo.R > 0) add_lora<NT>(v, row, valid, n, n_ok, lo, bf16);
-    if (LORA != LORA_NONE) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j) v[j] += bias;
-    }
+    const bool n_ok = n < p.N;
     const int64_t base = row * p.H + n;
     if (p.out_dt == SGMV_F32) {
         if (!n_ok) return;
@@ -240,24 +231,46 @@ __device__ __forceinline__ void finish(float (&v)[NT], int64_t row, int valid, i
     const int lane = threadIdx.x % 32;
     if (out_vec && n - lane + 32 <= p.N) {
         const int r = lane / 4, c = (lane % 4) * 8;
-        uint16_t* o = static_cast<uint16_t*>(p.out) + (base - lane + r * p.H + c);
-        uint4* s = reinterpret_cast<uint4*>(stage + r * 32 + c);
+        uint16_t* o = static_cast<uint16_t*>(p.out) + (base - lane + c);
+        uint16_t* halves = reinterpret_cast<uint16_t*>(stage);   // [token][32 columns]
         if (p.add) {
 #pragma unroll
             for (int j = 0; j < NT; j += 8)
-                if (j + r < valid) s[j * 4] = *reinterpret_cast<const uint4*>(o + j * p.H);
+                if (j + r < valid)
+                    *reinterpret_cast<uint4*>(halves + (j + r) * 32 + c) = *reinterpret_cast<const uint4*>(o + (j + r) * p.H);
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                if (j < valid) v[j] += half_bits_to_float(stage[j * 32 + lane], ob);
+                if (j < valid) v[j] += half_bits_to_float(halves[j * 32 + lane], ob);
             __syncwarp();
         }
+        if (NT == 32) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) stage[j * 32 + lane] = (uint16_t)float_to_half_bits(v[j], ob);
-        __syncwarp();
+            for (int j = 0; j < NT; j += 2) stage[j * 16 + lane] = pack2(v[j], v[j + 1], ob);   // [pair][32 columns]
+            __syncwarp();
 #pragma unroll
-        for (int j = 0; j < NT; j += 8)
-            if (j + r < valid) *reinterpret_cast<uint4*>(o + j * p.H) = s[j * 4];
+            for (int j = 0; j < NT; j += 16) {
+                const uint4 x = *reinterpret_cast<const uint4*>(stage + (j / 2 + r) * 32 + c);
+                const uint4 y = *reinterpret_cast<const uint4*>(stage + (j / 2 + r) * 32 + c + 4);
+                const int at = j + 2 * r;
+                if (at < valid)
+                    *reinterpret_cast<uint4*>(o + at * p.H) =
+                        make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.z, x.w, 0x5410),
+                                   __byte_perm(y.x, y.y, 0x5410), __byte_perm(y.z, y.w, 0x5410));
+                if (at + 1 < valid)
+                    *reinterpret_cast<uint4*>(o + (at + 1) * p.H) =
+                        make_uint4(__byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x7632),
+                                   __byte_perm(y.x, y.y, 0x7632), __byte_perm(y.z, y.w, 0x7632));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) halves[j * 32 + lane] = (uint16_t)float_to_half_bits(v[j], ob);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < NT; j += 8)
+                if (j + r < valid)
+                    *reinterpret_cast<uint4*>(o + (j + r) * p.H) = *reinterpret_cast<const uint4*>(halves + (j + r) * 32 + c);
+        }
         __syncwarp();
         return;
     }
@@ -275,6 +288,38 @@ __device__ __forceinline__ void finish(float (&v)[NT], int64_t row, int valid, i
         if (j < valid) o[j * p.H] = (uint16_t)float_to_half_bits(v[j], ob);
 }
 
+// A warp's share of a tile in TMEM: columns (tokens) c0, c0 + 64, ... in pieces
+// of 32, the next piece under way while one is stored.  `drained` runs once
+// the last piece is in registers; delta (or null): what to add per token, in
+// the lane's column of a [token][128] array.
+template <class Drained>
+__device__ __forceinline__ void drain(uint32_t taddr, int c0, int ts, int64_t row0, int rows, int64_t n, float bias,
+                                      const float* delta, const Problem& p, uint32_t* stage, bool out_vec,
+                                      Drained&& drained) {
+    uint32_t next[32];
+    float v[32];
+    if (c0 >= ts) {
+        drained();
+        return;
+    }
+    tmem_ld32(taddr + (uint32_t)c0, next);
+    for (int c = c0;; c += 64) {
+        tmem_ld_wait(next);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(next[j]) + bias;
+        const bool more = c + 64 < ts;
+        if (more) tmem_ld32(taddr + (uint32_t)c + 64, next);
+        else drained();
+        if (delta) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (c + j < rows) v[j] += delta[(c + j) * WROWS];
+        }
+        put<32>(v, row0 + c, min(32, rows - c), n, p, stage, out_vec);
+        if (!more) break;
+    }
+}
+
 // The part of v that the parts before have not covered, rounded to the half
 // type: hi = rounded(v), then rounded(v - hi), ...  fp16 saturates (what is left
 // goes to the next part); an infinity or NaN stays in the first part alone.
@@ -287,34 +332,40 @@ __device__ __forceinline__ uint32_t next_part(float& v, bool bf16) {
     return bits;
 }
 
-// Rows [row0, row0 + rows) of t, ranks [r0, r0 + C), as a K-major tile with
-// 128-byte swizzle: `parts` groups of C columns (C = 32 for two parts, 16 for
-// three), zero outside the run and past the last rank.  One lane per row.
-__device__ __forceinline__ void write_t_tile(uint8_t* dst, int64_t row0, int rows, const Run& run, int r0, const Lora& lo,
-                                             int lane, bool bf16) {
-    const int C = lo.parts == 2 ? 32 : 16, ranks = min(C, lo.R - r0);
-    for (int i = lane; i < rows; i += 32) {
-        const int64_t row = row0 + i;
-        const bool in = row >= run.begin && row < run.end;
-        const float* src = lo.t + row * lo.R + r0;
-        for (int c = 0; c < (ranks + 15) / 16 * 16; c += 8) {
-            float v[8];
-            if (in && c + 8 <= ranks) {   // R is a multiple of 8: 16-byte reads
-                const float4 a = *reinterpret_cast<const float4*>(src + c), b = *reinterpret_cast<const float4*>(src + c + 4);
-                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-            } else {
+// A low-rank stage's t: rows row0 .. row0 + 127 of t, ranks [r0, r0 + C), as a
+// K-major tile with 128-byte swizzle: `parts` groups of C columns (C = 32 for
+// two parts, 16 for three), zero outside the run and past the last rank.  A
+// lane holds four rows of 16 ranks, all requested at once.
+struct TRows {
+    float4 q[4][4];
+};
+
+__device__ __forceinline__ void load_t(TRows& x, int64_t row0, int rows, const Run& run, int r, const Lora& lo, int lane) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = 0.f;
-            }
-            for (int part = 0; part < lo.parts; ++part) {
-                uint32_t w[4];
+    for (int i = 0; i < 4; ++i) {
+        const int64_t row = row0 + lane + 32 * i;
+        const bool in = lane + 32 * i < rows && row >= run.begin && row < run.end;
+        const float4* src = reinterpret_cast<const float4*>(lo.t + row * lo.R + r);   // R, r: multiples of 8
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t x = next_part(v[2 * k], bf16);
-                    w[k] = x | next_part(v[2 * k + 1], bf16) << 16;
-                }
-                const int chunk = (part * C + c) / 8;
-                *reinterpret_cast<uint4*>(dst + i * 128 + ((chunk ^ (i & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int k = 0; k < 4; ++k) x.q[i][k] = in && r + 4 * k < lo.R ? src[k] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+}
+
+__device__ __forceinline__ void store_t(uint8_t* dst, TRows& x, int rows, int c, int parts, int lane, bool bf16) {
+    const int C = parts == 2 ? 32 : 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = lane + 32 * i;
+        if (row >= rows) continue;
+        for (int part = 0; part < parts; ++part) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float4 &a = x.q[i][2 * h], &b = x.q[i][2 * h + 1];
+                uint32_t w[8] = {next_part(a.x, bf16), next_part(a.y, bf16), next_part(a.z, bf16), next_part(a.w, bf16),
+                                 next_part(b.x, bf16), next_part(b.y, bf16), next_part(b.z, bf16), next_part(b.w, bf16)};
+                const int chunk = (part * C + c) / 8 + h;
+                *reinterpret_cast<uint4*>(dst + row * 128 + ((chunk ^ (row & 7)) << 4)) =
+                    make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
             }
         }
     }
@@ -530,12 +581,20 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                 const Run run = lo.runs[t.row0 + r];
                 for (int32_t r0 = 0; r0 < lo.R; r0 += t_ranks, ++q) {
                     const uint32_t s = q % S;
+                    const int ranks = min(t_ranks, lo.R - r0);
+                    TRows x;
+                    load_t(x, row0, hs, run, r0, lo, lane);
                     if (!warp_wait(smem_u32(&t_go[s]), (phases >> s) & 1, abort_flag, DEVERR_TIMEOUT_CONVERT)) {
                         ok = false;
                         break;
                     }
                     phases ^= 1u << s;
-                    write_t_tile(smem + s * g.stage_bytes + W_TILE, row0, hs, run, r0, lo, lane, bf16);
+                    uint8_t* dst = smem + s * g.stage_bytes + W_TILE;
+                    store_t(dst, x, hs, 0, lo.parts, lane, bf16);
+                    if (ranks > 16) {
+                        load_t(x, row0, hs, run, r0 + 16, lo, lane);
+                        store_t(dst, x, hs, 16, lo.parts, lane, bf16);
+                    }
                     asm volatile("fence.proxy.async;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) {
@@ -625,7 +684,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
         }
         const int quad = warp % 4, half = (warp - 2) / 4;
         const int nl = quad * 32 + lane;
-        uint16_t* stage = reinterpret_cast<uint16_t*>(smem + g.off_out + (warp - 2) * STAGE_ROWS);
+        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + g.off_out + (warp - 2) * STAGE_ROWS);
         uint32_t n = 0, reds = 0;   // reds: exchanges in which this CTA owned tokens
         for (int32_t id = cid; id < total; id += ncl, ++n) {
             decode_tile(segs, nseg, g, id, WT, t);
@@ -633,32 +692,39 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
             const int64_t col = t.n0 + (CG == 2 ? (int32_t)crank * WROWS : 0) + nl;
             const bool n_ok = col < p.N;
             float bias = 0.f;
-            if (LORA != LORA_NONE && lo.bias && n_ok)
-                bias = half_bits_to_float(static_cast<const uint16_t*>(lo.bias)[col * lo.bias_s], bf16);
+            if (lo.bias && n_ok) bias = half_bits_to_float(static_cast<const uint16_t*>(lo.bias)[col * lo.bias_s], bf16);
+            const int tw = csize > 1 && CG == 1 ? ((t.ts + (int)csize - 1) / (int)csize + 3) & ~3 : t.ts;
+            const int t0 = CG == 1 ? (int)crank * tw : 0, cnt = min(tw, t.rows - t0);   // tokens this CTA finishes
+            float* delta = reinterpret_cast<float*>(smem + g.off_delta) + nl;           // [token][weight row]
+            if (LORA == LORA_FMA) {
+                // while the K loop runs: the low-rank part of the tokens that this warp will store
+                for (int j0 = csize > 1 ? half * 8 : half * 32; j0 < cnt;) {
+                    float d[8];
+                    lora_delta(d, (int64_t)t.row0 + t0 + j0, cnt - j0, col, n_ok, lo, bf16);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j0 + j < tw) delta[(j0 + j) * WROWS] = d[j];
+                    j0 += csize > 1 ? 16 : (j0 & 31) == 24 ? 40 : 8;
+                }
+            }
             if (!warp_wait(smem_u32(&acc_full[acc]), (n >> 1) & 1, abort_flag, DEVERR_TIMEOUT_EPILOGUE)) break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + acc * (uint32_t)g.acc_stride + ((uint32_t)(quad * 32) << 16);
             if (CG == 2 || csize == 1) {
-                for (int c = half * 32; c < t.ts; c += 64) {
-                    float v[32];
-                    tmem_ld32(taddr + (uint32_t)c, reinterpret_cast<uint32_t(&)[32]>(v));
-                    tmem_ld_wait();
-                    finish<32, LORA>(v, (int64_t)t.row0 + c, min(32, t.rows - c), col, n_ok, bias, p, lo, bf16,
-                                     stage, g.out_vec);
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0 && id + 2 * ncl < total) {   // somebody waits for it
-                    if (CG == 2) mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[acc]), 0));
-                    else mbar_arrive(smem_u32(&acc_empty[acc]));
-                }
+                drain(taddr, half * 32, t.ts, t.row0, t.rows, col, bias, LORA == LORA_FMA ? delta : nullptr, p, stage,
+                      g.out_vec, [&] {
+                          tc_fence_before();
+                          __syncwarp();
+                          if (lane == 0 && id + 2 * ncl < total) {   // somebody waits for it
+                              if (CG == 2) mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[acc]), 0));
+                              else mbar_arrive(smem_u32(&acc_empty[acc]));
+                          }
+                      });
             } else {
                 // Partial sums go to the CTA that owns the token, four tokens of a weight row
                 // (16 bytes) at a time: red[source][token / 4][weight row][token % 4].  The
                 // stores count themselves at the owner's barrier, so nobody fences.
-                const int tw = ((t.ts + (int)csize - 1) / (int)csize + 3) & ~3;
                 const uint32_t red = smem_u32(smem + g.off_red) + (crank * (tw / 4) * WROWS + nl) * 16;
-                const int t0 = (int)crank * tw, cnt = min(tw, t.rows - t0);
                 if (cnt > 0 && warp == 2 && lane == 0)
                     mbar_expect_tx(smem_u32(red_full), csize * (uint32_t)((cnt + 3) / 4) * WROWS * 16u);
                 if (n > 0 && !warp_wait_cluster(smem_u32(red_free), (n & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_EPILOGUE))
@@ -687,7 +753,8 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                     for (int j0 = half * 8; j0 < cnt; j0 += 16) {
                         float v[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+                        for (int j = 0; j < 8; ++j)
+                            v[j] = LORA == LORA_FMA ? bias + delta[min(j0 + j, tw - 1) * WROWS] : bias;
                         for (int src = 0; src < (int)csize; ++src)
 #pragma unroll
                             for (int j = 0; j < 8; j += 4)
@@ -698,8 +765,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                                     v[j + 2] += f.z;
                                     v[j + 3] += f.w;
                                 }
-                        finish<8, LORA>(v, (int64_t)t.row0 + t0 + j0, min(8, cnt - j0), col, n_ok, bias, p, lo, bf16,
-                                        stage, g.out_vec);
+                        put<8>(v, (int64_t)t.row0 + t0 + j0, min(8, cnt - j0), col, p, stage, g.out_vec);
                     }
                 }
                 __syncwarp();
@@ -761,34 +827,52 @@ struct Shape {
     int cg, tn, splits;
 };
 
-// The form with the least estimated time.  Cycles of one stage of a CTA: the
-// MMA's (2 per token column of 128 weight rows and 64 of K, 4096 products a
-// cycle) or the loads' (64 bytes a cycle from L2), whichever is longer; a tile
-// adds a fixed cost, a shared one the exchange of the partial sums.  Segments
-// are taken as equally long, since their lengths are on the device.
-inline Shape choose_shape(const Problem& p, bool dense, int sm_count, int forced_cg) {
+// What a plan is made for, besides the problem.
+struct Want {
+    bool dense;      // one segment of all rows
+    bool early;
+    int lora;        // LoraMode
+    int R;
+    int sm_count;
+    int clusters[4]; // clusters of 1, 2, 4, 8 CTAs that fit on the device at a time
+    int forced_cg;   // 0: the cost model chooses
+};
+
+// The form with the least estimated time, in SM cycles.  A CTA's stage takes as
+// long as its MMAs (2 cycles per token column for 128 weight rows and 64 of K)
+// or its loads (64 bytes a cycle from L2); a tile adds a fixed cost, a shared
+// one the exchange of the partial sums, LORA_FMA its reads of B and its
+// arithmetic.  The whole takes at least as long as memory needs for the weights
+// (3500 bytes a cycle).  Segments are taken as equally long, since their
+// lengths are on the device.
+inline Shape choose_shape(const Problem& p, const Want& w) {
     const int64_t rows = p.x_rows < p.out_rows ? p.x_rows : p.out_rows;
-    const int64_t segs = dense ? 1 : (p.batches < rows ? p.batches : rows);
+    const int64_t segs = w.dense ? 1 : (p.batches < rows ? p.batches : rows);
     const int64_t mean = segs > 0 ? (rows + segs - 1) / segs : 1;
     const int64_t kblocks = (p.K + BK - 1) / BK;
+    const double experts = w.dense ? 1 : (double)(segs < p.lora_num ? segs : p.lora_num);
+    const double memory = experts * (double)p.N * p.K * 2.0 / 3500.0;
     Shape best{1, 32, 1};
     double best_cost = -1;
     const int tns[2][3] = {{32, 64, 128}, {64, 128, 256}};
     for (int cg = 1; cg <= 2; ++cg) {
-        if (forced_cg && cg != forced_cg) continue;
+        if (w.lora == LORA_FMA ? cg == 2 : w.forced_cg && cg != w.forced_cg) continue;
         for (int ti = 0; ti < 3; ++ti) {
             const int tn = tns[cg - 1][ti];
             const int64_t nt = (mean + tn - 1) / tn;
             const int64_t ts = ((mean + nt - 1) / nt + 16 * cg - 1) / (16 * cg) * (16 * cg);
             const int64_t tiles = segs * nt * ((p.N + WROWS * cg - 1) / (WROWS * cg));
-            for (int sp = 1; sp <= (cg == 1 ? MAX_SPLITS : 1); sp *= 2) {
+            for (int lg = 0, sp = 1; sp <= (cg == 1 ? MAX_SPLITS : 1); sp *= 2, ++lg) {
                 if (sp > 1 && kblocks < 4 * sp) break;
-                const int64_t workers = sm_count / (cg * sp) - (sp >= 4 ? 4 : 0);   // GPCs that a cluster does not fill
+                const int64_t workers = w.clusters[cg == 2 ? 1 : lg] > 0 ? w.clusters[cg == 2 ? 1 : lg] : 1;
                 const int64_t waves = (tiles + workers - 1) / workers;
                 const double load = (W_TILE + (double)ts / cg * 128) / 64.0;
                 const double mma = 2.0 * ts;
-                const double stage = (load > mma ? load : mma) > 160.0 ? (load > mma ? load : mma) : 160.0;
-                const double cost = waves * ((double)((kblocks + sp - 1) / sp) * stage + 600.0) + (sp > 1 ? 1500.0 : 0.0) + 16.0 * ts;
+                const double own = (double)((ts + sp - 1) / sp);   // tokens a CTA finishes
+                const double fma = w.lora == LORA_FMA ? own * w.R * (256.0 / 50.0 + 2.0) : 0.0;
+                const double body = (double)((kblocks + sp - 1) / sp) * (load > mma ? load : mma);
+                const double path = waves * ((body > fma ? body : fma) + 600.0) + (sp > 1 ? 1500.0 : 0.0) + 16.0 * own;
+                const double cost = (path > memory ? path : memory) + 0.1 * path;
                 if (best_cost < 0 || cost < best_cost * 0.97) {
                     best_cost = cost;
                     best = Shape{cg, tn, sp};
@@ -799,9 +883,10 @@ inline Shape choose_shape(const Problem& p, bool dense, int sm_count, int forced
     return best;
 }
 
-inline bool make_plan(const Problem& p, bool dense, bool early, int sm_count, int forced_cg, EncodeTiledFn enc, Plan* out) {
+inline bool make_plan(const Problem& p, const Want& w, EncodeTiledFn enc, Plan* out) {
     if (!supports(p) || !enc) return false;
-    const Shape sh = choose_shape(p, dense, sm_count, forced_cg);
+    const bool dense = w.dense;
+    const Shape sh = choose_shape(p, w);
     Geo& g = out->geo;
     const int64_t rows = p.x_rows < p.out_rows ? p.x_rows : p.out_rows;
     out->cg = sh.cg;
@@ -811,7 +896,7 @@ inline bool make_plan(const Problem& p, bool dense, bool early, int sm_count, in
     g.kblocks = (int32_t)((p.K + BK - 1) / BK);
     g.w_mn = !(p.w_ks == 1 && (p.w_ns * 2) % 16 == 0 && p.w_ns >= p.K);
     g.dense_rows = dense ? (int32_t)rows : -1;
-    g.early = early ? 1 : 0;
+    g.early = w.early ? 1 : 0;
     g.out_vec = out_vec_ok(p);
     const int64_t segs = dense ? 1 : p.batches;
     g.keep_w = rows > (int64_t)sh.tn * segs ? 1 : 0;
@@ -822,7 +907,8 @@ inline bool make_plan(const Problem& p, bool dense, bool early, int sm_count, in
     const int red = sh.splits > 1 ? sh.splits * (((sh.tn + sh.splits - 1) / sh.splits + 3) & ~3) * WROWS * 4 : 0;
     for (g.stages = 12; g.stages >= 2; --g.stages) {
         g.off_out = g.stages * g.stage_bytes;
-        g.off_red = g.off_out + EPI_WARPS * STAGE_ROWS;
+        g.off_delta = g.off_out + EPI_WARPS * STAGE_ROWS;
+        g.off_red = g.off_delta + (w.lora == LORA_FMA ? ((sh.tn + sh.splits - 1) / sh.splits + 3) / 4 * 4 * WROWS * 4 : 0);
         g.off_seg = g.off_red + red;
         g.off_bar = (g.off_seg + (int)segs * (int)sizeof(Seg) + 15) & ~15;
         out->smem_bytes = g.off_bar + 8 * (3 * g.stages + 6) + 1024;
@@ -854,7 +940,7 @@ inline bool make_plan(const Problem& p, bool dense, bool early, int sm_count, in
     const int64_t most_segs = segs < rows ? segs : rows;
     const int64_t tiles = (rows / sh.tn + most_segs + 1) * g.nblk;
     const int csize = sh.cg == 2 ? 2 : sh.splits;
-    int64_t clusters = sm_count / csize;
+    int64_t clusters = w.clusters[csize == 1 ? 0 : csize == 2 ? 1 : csize == 4 ? 2 : 3];
     if (tiles < clusters) clusters = tiles;
     out->grid = (int)(clusters < 1 ? 1 : clusters) * csize;
     return true;
@@ -862,20 +948,56 @@ inline bool make_plan(const Problem& p, bool dense, bool early, int sm_count, in
 
 struct PlanKey {
     Problem p;
-    int32_t device, sm_count, dense, early, forced_cg, pad;
+    Want w;
+    int32_t device;
 };
 
-inline bool cached_plan(const Problem& p, bool dense, bool early, int sm_count, int forced_cg, EncodeTiledFn enc, Plan* out) {
+// Clusters of 1, 2, 4 and 8 CTAs (one per SM) that the current device holds at
+// a time: a GPC whose SM count the size does not divide leaves some idle.
+inline bool cluster_capacity(int device, int sm_count, int (&out)[4]) {
+    static std::mutex mu;
+    static int known[64][4];
+    std::lock_guard<std::mutex> lk(mu);
+    if (device < 0 || device >= 64) return false;
+    if (!known[device][0]) {
+        auto kern = gemm_kernel<1, LORA_NONE>;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT) != cudaSuccess) return false;
+        int got[4] = {sm_count, sm_count / 2, 0, 0};
+        for (int lg = 1; lg < 4; ++lg) {
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 1u << lg;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)(sm_count >> lg << lg));
+            cfg.blockDim = dim3(threads_of(LORA_NONE));
+            cfg.dynamicSmemBytes = SMEM_LIMIT;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&got[lg], kern, &cfg) != cudaSuccess || got[lg] < 1) return false;
+        }
+        for (int lg = 0; lg < 4; ++lg) known[device][lg] = got[lg];
+    }
+    for (int lg = 0; lg < 4; ++lg) out[lg] = known[device][lg];
+    return true;
+}
+
+// Plans of recent calls, keyed by every field of the problem, the wishes and the device.
+inline bool cached_plan(const Problem& p, bool dense, bool early, int lora, int R, int sm_count, int forced_cg,
+                        EncodeTiledFn enc, Plan* out) {
     static PlanCache<PlanKey, Plan> cache;
     PlanKey key;
     std::memset(&key, 0, sizeof(key));
     std::memcpy(&key.p, &p, sizeof(Problem));
-    key.sm_count = sm_count;
-    key.dense = dense;
-    key.early = early;
-    key.forced_cg = forced_cg;
-    if (cudaGetDevice(&key.device) != cudaSuccess) return false;
-    return cache.get(key, out, [&](Plan* pl) { return make_plan(p, dense, early, sm_count, forced_cg, enc, pl); });
+    key.w.dense = dense;
+    key.w.early = early;
+    key.w.lora = lora;
+    key.w.R = R;
+    key.w.sm_count = sm_count;
+    key.w.forced_cg = forced_cg;
+    if (cudaGetDevice(&key.device) != cudaSuccess || !cluster_capacity(key.device, sm_count, key.w.clusters)) return false;
+    return cache.get(key, out, [&](Plan* pl) { return make_plan(p, key.w, enc, pl); });
 }
 
 template <int CG, int LORA>

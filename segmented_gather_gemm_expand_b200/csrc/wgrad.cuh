@@ -285,8 +285,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     } else {
         // ------------------------------------------------------------ epilogue
         const int quad = warp % 4, half = (warp - 2) / 4;
-        const grp::Lora none = {};
-        uint16_t* stage = reinterpret_cast<uint16_t*>(smem + g.off_out + (warp - 2) * grp::STAGE_ROWS);
+        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + g.off_out + (warp - 2) * grp::STAGE_ROWS);
         uint32_t n = 0;
         for (int32_t id = cid; id < total; id += ncl, ++n) {
             int32_t e, k0, n0;
@@ -298,21 +297,23 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
             if (!warp_wait(smem_u32(&acc_full[acc]), (n >> 1) & 1, abort_flag, DEVERR_TIMEOUT_EPILOGUE)) break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + acc * (uint32_t)g.acc_stride + ((uint32_t)(quad * 32) << 16);
-            if (any || !p.add) {
-                for (int c = half * 32; c < g.ts; c += 64) {
+            const auto drained = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && id + 2 * ncl < total) mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[acc]), 0));
+            };
+            const int64_t row0 = (int64_t)e * g.rows_per_group + n0;
+            if (any) {
+                grp::drain(taddr, half * 32, g.ts, row0, valid, col, 0.f, nullptr, p, stage, g.out_vec, drained);
+            } else {
+                drained();
+                for (int c = half * 32; c < g.ts && !p.add; c += 64) {
                     float v[32];
-                    tmem_ld32(taddr + (uint32_t)c, reinterpret_cast<uint32_t(&)[32]>(v));
-                    tmem_ld_wait();
-                    if (!any)
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = 0.f;
-                    grp::finish<32, grp::LORA_NONE>(v, (int64_t)e * g.rows_per_group + n0 + c, min(32, valid - c), col, col < p.N,
-                                           0.f, p, none, bf16, stage, g.out_vec);
+                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                    grp::put<32>(v, row0 + c, min(32, valid - c), col, p, stage, g.out_vec);
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0 && id + 2 * ncl < total) mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[acc]), 0));
         }
     }
 
