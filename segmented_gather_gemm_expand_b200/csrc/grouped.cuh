@@ -31,8 +31,9 @@
 // The low-rank part of a shared projection comes in one of two ways (LoraMode):
 //   LORA_MMA   as further K steps of the same accumulator, for batches whose
 //          segments are long enough to share an MMA: for every run of rows with
-//          one adapter in a token tile, one stage per 32 ranks holds B[a]'s rows
-//          (TMA) and t's rows (warp 10), zero outside the run.  t is fp32 and
+//          one adapter in a token tile and every 32 ranks, one stage holds B[a]'s
+//          rows (TMA) and one of two buffers t's rows, zero outside the run, which
+//          warps 10 and 11 write up to a tile ahead of the MMAs.  t is fp32 and
 //          enters as the sum of two half-precision parts (hi, and what is left
 //          of it, rounded), three where out is fp32: relative errors of 2^-16
 //          (2^-24) against out's own rounding of 2^-9 (2^-24).
@@ -60,9 +61,10 @@ constexpr int BK = 64;                  // K columns per stage: 128-byte rows
 constexpr int WROWS = 128;              // weight rows per CTA
 constexpr int W_TILE = WROWS * BK * 2;  // 16 KB
 constexpr int EPI_WARPS = 8;
-constexpr int LORA_WARP = 2 + EPI_WARPS;   // LORA_MMA only
+constexpr int LORA_WARP = 2 + EPI_WARPS;   // first of the warps that write t (LORA_MMA only)
+constexpr int LORA_WARPS = 2;
 enum LoraMode { LORA_NONE = 0, LORA_FMA = 1, LORA_MMA = 2 };
-constexpr int threads_of(int lora) { return 64 + 32 * EPI_WARPS + (lora == LORA_MMA ? 32 : 0); }
+constexpr int threads_of(int lora) { return 64 + 32 * EPI_WARPS + (lora == LORA_MMA ? 32 * LORA_WARPS : 0); }
 constexpr int NUM_XMAPS = 4;            // x boxes of 16, 32, 64, 128 rows
 constexpr int MAX_SPLITS = 8;
 constexpr int STAGE_ROWS = 32 * 64;     // epilogue: a warp's 32 x 32 halves
@@ -81,7 +83,7 @@ struct Geo {
     int32_t tn;           // most tokens per tile
     int32_t splits;       // CTAs that share a tile by cutting K (single form)
     int32_t stages, stage_bytes;
-    int32_t off_out, off_delta, off_red, off_seg, off_bar;
+    int32_t off_t, t_bytes, off_out, off_delta, off_red, off_seg, off_bar;
     int32_t out_vec;      // half output in 16-byte pieces
     int32_t acc_stride, tmem_cols;
     int32_t w_mn;         // the weights' N axis is the contiguous one
@@ -320,52 +322,56 @@ __device__ __forceinline__ void drain(uint32_t taddr, int c0, int ts, int64_t ro
     }
 }
 
-// The part of v that the parts before have not covered, rounded to the half
+// The part of (a, b) that the parts before have not covered, rounded to the half
 // type: hi = rounded(v), then rounded(v - hi), ...  fp16 saturates (what is left
 // goes to the next part); an infinity or NaN stays in the first part alone.
-__device__ __forceinline__ uint32_t next_part(float& v, bool bf16) {
-    float h = v;
-    if (!bf16 && fabsf(v) > 65504.f && fabsf(v) <= 3.4e38f) h = copysignf(65504.f, v);
-    const uint32_t bits = float_to_half_bits(h, bf16);
-    const float back = half_bits_to_float(bits, bf16);
-    v = fabsf(back) <= 3.4e38f ? v - back : 0.f;
+__device__ __forceinline__ uint32_t next_part(float& a, float& b, bool bf16) {
+    constexpr float MAX32 = 3.402823466e38f;
+    float x = a, y = b;
+    if (!bf16) {
+        if (fabsf(x) <= MAX32) x = fminf(fmaxf(x, -65504.f), 65504.f);
+        if (fabsf(y) <= MAX32) y = fminf(fmaxf(y, -65504.f), 65504.f);
+    }
+    const uint32_t bits = pack2(x, y, bf16);
+    const float2 back = unpack2(bits, bf16);
+    a = fabsf(back.x) <= MAX32 ? a - back.x : 0.f;
+    b = fabsf(back.y) <= MAX32 ? b - back.y : 0.f;
     return bits;
 }
 
-// A low-rank stage's t: rows row0 .. row0 + 127 of t, ranks [r0, r0 + C), as a
+// A low-rank step's t: rows row0 .. row0 + 127 of t, ranks [r0, r0 + C), as a
 // K-major tile with 128-byte swizzle: `parts` groups of C columns (C = 32 for
 // two parts, 16 for three), zero outside the run and past the last rank.  A
-// lane holds four rows of 16 ranks, all requested at once.
+// lane holds two rows (`first`, `first` + 64) of 16 ranks, all requested at once.
 struct TRows {
-    float4 q[4][4];
+    float4 q[2][4];
 };
 
-__device__ __forceinline__ void load_t(TRows& x, int64_t row0, int rows, const Run& run, int r, const Lora& lo, int lane) {
+__device__ __forceinline__ void load_t(TRows& x, int64_t row0, int rows, const Run& run, int r, const Lora& lo, int first) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t row = row0 + lane + 32 * i;
-        const bool in = lane + 32 * i < rows && row >= run.begin && row < run.end;
+    for (int i = 0; i < 2; ++i) {
+        const int64_t row = row0 + first + 64 * i;
+        const bool in = first + 64 * i < rows && row >= run.begin && row < run.end;
         const float4* src = reinterpret_cast<const float4*>(lo.t + row * lo.R + r);   // R, r: multiples of 8
 #pragma unroll
         for (int k = 0; k < 4; ++k) x.q[i][k] = in && r + 4 * k < lo.R ? src[k] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
-__device__ __forceinline__ void store_t(uint8_t* dst, TRows& x, int rows, int c, int parts, int lane, bool bf16) {
+__device__ __forceinline__ void store_t(uint8_t* dst, TRows& x, int rows, int c, int parts, int first, bool bf16) {
     const int C = parts == 2 ? 32 : 16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = lane + 32 * i;
+    for (int i = 0; i < 2; ++i) {
+        const int row = first + 64 * i;
         if (row >= rows) continue;
         for (int part = 0; part < parts; ++part) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float4 &a = x.q[i][2 * h], &b = x.q[i][2 * h + 1];
-                uint32_t w[8] = {next_part(a.x, bf16), next_part(a.y, bf16), next_part(a.z, bf16), next_part(a.w, bf16),
-                                 next_part(b.x, bf16), next_part(b.y, bf16), next_part(b.z, bf16), next_part(b.w, bf16)};
+                const uint32_t w0 = next_part(a.x, a.y, bf16), w1 = next_part(a.z, a.w, bf16);
+                const uint32_t w2 = next_part(b.x, b.y, bf16), w3 = next_part(b.z, b.w, bf16);
                 const int chunk = (part * C + c) / 8 + h;
-                *reinterpret_cast<uint4*>(dst + row * 128 + ((chunk ^ (row & 7)) << 4)) =
-                    make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+                *reinterpret_cast<uint4*>(dst + row * 128 + ((chunk ^ (row & 7)) << 4)) = make_uint4(w0, w1, w2, w3);
             }
         }
     }
@@ -376,7 +382,6 @@ __global__ void __launch_bounds__(threads_of(LORA), 1)
 gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtensorMap wmap,
             const __grid_constant__ CUtensorMap bmap, const Problem p, const Geo g, const Lora lo) {
     constexpr int THREADS = threads_of(LORA);
-    constexpr uint32_t T_ARRIVALS = LORA == LORA_MMA ? CG : 0;   // arrivals of the warps that write t
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ int s_abort;
@@ -395,18 +400,20 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* red_full = acc_empty + 2;
     uint64_t* red_free = red_full + 1;
-    uint64_t* t_go = red_free + 1;   // LORA_MMA: the stage is free for t (one phase per low-rank stage it serves)
+    uint64_t* t_full = red_free + 1;   // LORA_MMA: two buffers of t besides the stages
+    uint64_t* t_empty = t_full + 2;
 
     if (tid == 0) {
         s_abort = 0;
         for (uint32_t i = 0; i < S; ++i) {
-            mbar_init(smem_u32(&full[i]), 1 + T_ARRIVALS);   // the first CTA of a pair announces the bytes of both
+            mbar_init(smem_u32(&full[i]), 1);   // the first CTA of a pair announces the bytes of both
             mbar_init(smem_u32(&empty[i]), 1);
-            if (LORA == LORA_MMA) mbar_init(smem_u32(&t_go[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&acc_full[i]), 1);
             mbar_init(smem_u32(&acc_empty[i]), CG * EPI_WARPS);
+            mbar_init(smem_u32(&t_full[i]), CG * LORA_WARPS);
+            mbar_init(smem_u32(&t_empty[i]), 1);
         }
         mbar_init(smem_u32(red_full), 1);   // the expected bytes, then the stores' own counts
         mbar_init(smem_u32(red_free), csize * EPI_WARPS);
@@ -499,10 +506,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                         // arrival with release semantics costs a memory barrier per stage (1640 cycles a stage
                         // instead of 512).  The second CTA cannot run a phase ahead, since it waits for `empty`.
                         const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
-                        if (crank == 0) {
-                            mbar_expect_tx(smem_u32(&full[s]), 2 * bytes);
-                            if (T_ARRIVALS) mbar_arrive_n(smem_u32(&full[s]), T_ARRIVALS);
-                        }
+                        if (crank == 0) mbar_expect_tx(smem_u32(&full[s]), 2 * bytes);
                         if (g.w_mn) {
                             tma_load_3d_pair(ws, &wmap, n0, kb * BK, t.group, bar, pol_w);
                             tma_load_3d_pair(ws + W_TILE / 2, &wmap, n0 + 64, kb * BK, t.group, bar, pol_w);
@@ -513,7 +517,6 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                     } else {
                         const uint32_t bar = smem_u32(&full[s]);
                         mbar_expect_tx(bar, bytes);
-                        if (T_ARRIVALS) mbar_arrive_n(bar, T_ARRIVALS);
                         if (g.w_mn) {
                             tma_load_3d(ws, &wmap, n0, kb * BK, t.group, bar, pol_w);
                             tma_load_3d(ws + W_TILE / 2, &wmap, n0 + 64, kb * BK, t.group, bar, pol_w);
@@ -537,9 +540,6 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                                 ok = false;
                                 break;
                             }
-                            // warp 10 cannot wait for `empty` itself: it skips the K stages, and a parity
-                            // tells neighbouring phases apart only
-                            mbar_arrive(smem_u32(&t_go[s]));
                             const uint32_t ws = smem_u32(smem + s * g.stage_bytes);
                             if (CG == 2) {
                                 if (crank == 0) mbar_expect_tx(smem_u32(&full[s]), 2 * W_TILE);
@@ -566,48 +566,49 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
             }
         }
         __syncwarp();
-    } else if (LORA == LORA_MMA && warp == LORA_WARP) {
-        // ------------------------------------------------------------ t into the low-rank stages
+    } else if (LORA == LORA_MMA && warp >= LORA_WARP) {
+        // ------------------------------------------------------------ t, ahead of the MMAs by up to two low-rank steps
         if (g.early) grid_dependency_wait();
-        uint32_t q = 0, phases = 0;   // phases: one bit per stage
+        const int first = (warp - LORA_WARP) * 32 + lane;
+        uint32_t m = 0;
         bool ok = true;
         for (int32_t id = cid; ok && lora_here && id < total; id += ncl) {
             decode_tile(segs, nseg, g, id, WT, t);
-            q += (uint32_t)(kb1 - kb0);
             const int32_t hs = t.ts / CG;
             const int32_t row0 = t.row0 + (CG == 2 ? (int32_t)crank * hs : 0);
             const int32_t nruns = lo.runs[t.row0].count;
             for (int32_t r = 0; ok && r < nruns; ++r) {
                 const Run run = lo.runs[t.row0 + r];
-                for (int32_t r0 = 0; r0 < lo.R; r0 += t_ranks, ++q) {
-                    const uint32_t s = q % S;
-                    const int ranks = min(t_ranks, lo.R - r0);
+                for (int32_t r0 = 0; r0 < lo.R; r0 += t_ranks, ++m) {
+                    const uint32_t buf = m & 1;
                     TRows x;
-                    load_t(x, row0, hs, run, r0, lo, lane);
-                    if (!warp_wait(smem_u32(&t_go[s]), (phases >> s) & 1, abort_flag, DEVERR_TIMEOUT_CONVERT)) {
+                    load_t(x, row0, hs, run, r0, lo, first);
+                    if (!warp_wait(smem_u32(&t_empty[buf]), ((m >> 1) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_CONVERT)) {
                         ok = false;
                         break;
                     }
-                    phases ^= 1u << s;
-                    uint8_t* dst = smem + s * g.stage_bytes + W_TILE;
-                    store_t(dst, x, hs, 0, lo.parts, lane, bf16);
-                    if (ranks > 16) {
-                        load_t(x, row0, hs, run, r0 + 16, lo, lane);
-                        store_t(dst, x, hs, 16, lo.parts, lane, bf16);
+                    uint8_t* dst = smem + g.off_t + buf * g.t_bytes;
+                    store_t(dst, x, hs, 0, lo.parts, first, bf16);
+                    if (min(t_ranks, lo.R - r0) > 16) {
+                        load_t(x, row0, hs, run, r0 + 16, lo, first);
+                        store_t(dst, x, hs, 16, lo.parts, first, bf16);
                     }
                     asm volatile("fence.proxy.async;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) {
-                        if (CG == 2) mbar_arrive_cluster(map_to_rank(smem_u32(&full[s]), 0));
-                        else mbar_arrive(smem_u32(&full[s]));
+                        if (CG == 2 && crank != 0) mbar_arrive_cluster(map_to_rank(smem_u32(&t_full[buf]), 0));
+                        else mbar_arrive(smem_u32(&t_full[buf]));
                     }
                 }
             }
         }
+        // the commits of the other CTA's MMAs free the buffers: none may be under way when this CTA ends
+        for (int i = 0; CG == 2 && ok && i < 2; ++i, ++m)
+            ok = warp_wait(smem_u32(&t_empty[m & 1]), ((m >> 1) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_CONVERT);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA (the pair's first CTA)
         if ((CG == 1 || crank == 0) && elect_one()) {
-            uint32_t s = 0, phase = 0, n = 0;
+            uint32_t s = 0, phase = 0, n = 0, m = 0;
             bool ok = true;
             // K step of 16 inside a stage: 32 bytes along a K-major row, 16 rows of an N-major tile
             const uint64_t w_step = (uint64_t)((g.w_mn ? 16 * 128 : 32) >> 4);
@@ -652,8 +653,15 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                                 ok = false;
                                 break;
                             }
+                            const uint32_t buf = m & 1;
+                            if (!mbar_wait(smem_u32(&t_full[buf]), (m >> 1) & 1, abort_flag, DEVERR_TIMEOUT_MMA)) {
+                                ok = false;
+                                break;
+                            }
+                            ++m;
                             tc_fence_after();
-                            const uint64_t ad = bk0 + s * stage_step, bd = bd0 + s * stage_step;
+                            const uint64_t ad = bk0 + s * stage_step;
+                            const uint64_t bd = smem_desc(smem_u32(smem + g.off_t + buf * g.t_bytes), 16, 1024, 2);
                             const int steps = (min(t_ranks, lo.R - r0) + 15) / 16;
                             for (int part = 0; part < lo.parts; ++part)
                                 for (int kk = 0; kk < steps; ++kk) {
@@ -661,8 +669,13 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                                     if (CG == 2) tc_mma_pair(d, ad + kk * 2, td, idesc_t, 1u);
                                     else tc_mma(d, ad + kk * 2, td, idesc_t, 1u);
                                 }
-                            if (CG == 2) tc_commit_pair(smem_u32(&empty[s]));
-                            else tc_commit(smem_u32(&empty[s]));
+                            if (CG == 2) {
+                                tc_commit_pair(smem_u32(&empty[s]));
+                                tc_commit_pair(smem_u32(&t_empty[buf]));
+                            } else {
+                                tc_commit(smem_u32(&empty[s]));
+                                tc_commit(smem_u32(&t_empty[buf]));
+                            }
                             if (++s == S) {
                                 s = 0;
                                 phase ^= 1;
@@ -906,12 +919,14 @@ inline bool make_plan(const Problem& p, const Want& w, EncodeTiledFn enc, Plan* 
     g.stage_bytes = W_TILE + (sh.tn / sh.cg) * 128;
     const int red = sh.splits > 1 ? sh.splits * (((sh.tn + sh.splits - 1) / sh.splits + 3) & ~3) * WROWS * 4 : 0;
     for (g.stages = 12; g.stages >= 2; --g.stages) {
-        g.off_out = g.stages * g.stage_bytes;
+        g.off_t = g.stages * g.stage_bytes;
+        g.t_bytes = w.lora == LORA_MMA ? (sh.tn / sh.cg < 64 ? 64 : sh.tn / sh.cg) * 128 : 0;
+        g.off_out = g.off_t + 2 * g.t_bytes;
         g.off_delta = g.off_out + EPI_WARPS * STAGE_ROWS;
         g.off_red = g.off_delta + (w.lora == LORA_FMA ? ((sh.tn + sh.splits - 1) / sh.splits + 3) / 4 * 4 * WROWS * 4 : 0);
         g.off_seg = g.off_red + red;
         g.off_bar = (g.off_seg + (int)segs * (int)sizeof(Seg) + 15) & ~15;
-        out->smem_bytes = g.off_bar + 8 * (3 * g.stages + 6) + 1024;
+        out->smem_bytes = g.off_bar + 8 * (2 * g.stages + 10) + 1024;
         if (out->smem_bytes <= SMEM_LIMIT) break;
     }
     if (g.stages < 2) return false;
