@@ -39,7 +39,8 @@
 //          (2^-24) against out's own rounding of 2^-9 (2^-24).
 //   LORA_FMA   on the CUDA cores in fp32, by the epilogue's warps while the K loop
 //          runs (they keep it in shared memory until the sums are there): single
-//          tokens with an adapter each, or a B that TMA cannot read.
+//          tokens with an adapter each, or a B that TMA cannot read.  Warp 10 loads
+//          each token's 128 rows of B and its row of t into a ring.
 //
 // Every wait is bounded and reports a timeout through the device error word.
 #pragma once
@@ -64,10 +65,15 @@ constexpr int EPI_WARPS = 8;
 constexpr int LORA_WARP = 2 + EPI_WARPS;   // first of the warps that write t (LORA_MMA only)
 constexpr int LORA_WARPS = 2;
 enum LoraMode { LORA_NONE = 0, LORA_FMA = 1, LORA_MMA = 2 };
-constexpr int threads_of(int lora) { return 64 + 32 * EPI_WARPS + (lora == LORA_MMA ? 32 * LORA_WARPS : 0); }
+constexpr int B_WARP = 2 + EPI_WARPS;      // loads B for LORA_FMA
+constexpr int threads_of(int lora) {
+    return 64 + 32 * EPI_WARPS + (lora == LORA_MMA ? 32 * LORA_WARPS : lora == LORA_FMA ? 32 : 0);
+}
+constexpr int B_RING = 24 * 1024;          // LORA_FMA: buffered rows of B for each half of the epilogue's warps
+constexpr int B_SLOTS = 8;                 // at most
+constexpr int T_ROW = 64 * 4;              // a slot's ranks of t, fp32
 constexpr int NUM_XMAPS = 4;            // x boxes of 16, 32, 64, 128 rows
 constexpr int MAX_SPLITS = 8;
-constexpr int STAGE_ROWS = 32 * 64;     // epilogue: a warp's 32 x 32 halves
 constexpr int BAND = 8;                 // token tiles walked together before the next weight tile
 constexpr int SEG_CAP = 4096;           // most segments a launch takes
 constexpr int SMEM_LIMIT = 232448 - 1024;
@@ -83,8 +89,10 @@ struct Geo {
     int32_t tn;           // most tokens per tile
     int32_t splits;       // CTAs that share a tile by cutting K (single form)
     int32_t stages, stage_bytes;
-    int32_t off_t, t_bytes, off_out, off_delta, off_red, off_seg, off_bar;
+    int32_t b_ranks, b_slots, b_bytes;   // LORA_FMA: ranks per buffer (8 to 64; 0: B is not loaded by TMA), buffers per half
+    int32_t off_t, t_bytes, off_tr, off_out, off_delta, off_red, off_seg, off_bar;
     int32_t out_vec;      // half output in 16-byte pieces
+    int32_t turn_bytes;   // shared memory in which an epilogue warp turns its halves round
     int32_t acc_stride, tmem_cols;
     int32_t w_mn;         // the weights' N axis is the contiguous one
     int32_t dense_rows;   // >= 0: one segment of that many rows with group 0; -1: the call's segments
@@ -196,6 +204,37 @@ __device__ __forceinline__ void lora_delta(float (&d)[8], int64_t row, int valid
             if (a[j] >= 0 && n_ok)
                 d[j] = fmaf(t[j * lo.R + r0],
                             half_bits_to_float(__ldg(b + (int64_t)a[j] * lo.b_as + r0 * lo.b_ks), bf16), d[j]);
+}
+
+// One token's low-rank sum over a buffered piece of B (the lane's row of 128,
+// `ranks` (8 to 64) halves each, swizzled by TMA so that 8 lanes' 16-byte reads
+// touch every bank once): d += sum_k t[k] * B[k].
+__device__ __forceinline__ float lora_dot(const uint8_t* piece, int row, int width, int ranks, const float* t, bool bf16) {
+    const int bytes = width * 2;
+    const uint8_t* r = piece + row * bytes;
+    const int turn = bytes == 128 ? row & 7 : bytes == 64 ? (row >> 1) & 3 : bytes == 32 ? (row >> 2) & 1 : 0;
+    float d0 = 0.f, d1 = 0.f;
+#pragma unroll 2
+    for (int k = 0; k < ranks; k += 8) {
+        const float4 x = *reinterpret_cast<const float4*>(t + k), y = *reinterpret_cast<const float4*>(t + k + 4);
+        const uint4 u = *reinterpret_cast<const uint4*>(r + (((k >> 3) ^ turn) << 4));
+        const float2 a = unpack2(u.x, bf16), b = unpack2(u.y, bf16), c = unpack2(u.z, bf16), e = unpack2(u.w, bf16);
+        d0 = fmaf(x.x, a.x, d0);
+        d1 = fmaf(x.y, a.y, d1);
+        d0 = fmaf(x.z, b.x, d0);
+        d1 = fmaf(x.w, b.y, d1);
+        d0 = fmaf(y.x, c.x, d0);
+        d1 = fmaf(y.y, c.y, d1);
+        d0 = fmaf(y.z, e.x, d0);
+        d1 = fmaf(y.w, e.y, d1);
+    }
+    return d0 + d1;
+}
+
+// The i-th token that a half of the epilogue's warps finishes: 32 of every 64
+// (a shared tile: 8 of every 16).
+__device__ __forceinline__ int half_token(int half, int i, bool shared) {
+    return shared ? (i >> 3) * 16 + half * 8 + (i & 7) : (i >> 5) * 64 + half * 32 + (i & 31);
 }
 
 // Adds the old output (add mode), rounds once and stores rows row .. row +
@@ -342,23 +381,25 @@ __device__ __forceinline__ uint32_t next_part(float& a, float& b, bool bf16) {
 // A low-rank step's t: rows row0 .. row0 + 127 of t, ranks [r0, r0 + C), as a
 // K-major tile with 128-byte swizzle: `parts` groups of C columns (C = 32 for
 // two parts, 16 for three), zero outside the run and past the last rank.  A
-// lane holds two rows (`first`, `first` + 64) of 16 ranks, all requested at once.
+// lane holds two rows (`first`, `first` + 64) of up to 32 ranks, all requested
+// at once, and for the step after the one it writes.
 struct TRows {
-    float4 q[2][4];
+    float4 q[2][8];
 };
 
-__device__ __forceinline__ void load_t(TRows& x, int64_t row0, int rows, const Run& run, int r, const Lora& lo, int first) {
+__device__ __forceinline__ void load_t(TRows& x, int64_t row0, int rows, const Run& run, int r, int ranks, const Lora& lo,
+                                       int first) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int64_t row = row0 + first + 64 * i;
         const bool in = first + 64 * i < rows && row >= run.begin && row < run.end;
         const float4* src = reinterpret_cast<const float4*>(lo.t + row * lo.R + r);   // R, r: multiples of 8
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x.q[i][k] = in && r + 4 * k < lo.R ? src[k] : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < 8; ++k) x.q[i][k] = in && 4 * k < ranks ? src[k] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
-__device__ __forceinline__ void store_t(uint8_t* dst, TRows& x, int rows, int c, int parts, int first, bool bf16) {
+__device__ __forceinline__ void store_t(uint8_t* dst, TRows& x, int rows, int ranks, int parts, int first, bool bf16) {
     const int C = parts == 2 ? 32 : 16;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -366,16 +407,24 @@ __device__ __forceinline__ void store_t(uint8_t* dst, TRows& x, int rows, int c,
         if (row >= rows) continue;
         for (int part = 0; part < parts; ++part) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < 4; ++h) {
+                if (h >= 2 && ranks <= 16) continue;   // whole K steps of 16
                 float4 &a = x.q[i][2 * h], &b = x.q[i][2 * h + 1];
                 const uint32_t w0 = next_part(a.x, a.y, bf16), w1 = next_part(a.z, a.w, bf16);
                 const uint32_t w2 = next_part(b.x, b.y, bf16), w3 = next_part(b.z, b.w, bf16);
-                const int chunk = (part * C + c) / 8 + h;
+                const int chunk = part * C / 8 + h;
                 *reinterpret_cast<uint4*>(dst + row * 128 + ((chunk ^ (row & 7)) << 4)) = make_uint4(w0, w1, w2, w3);
             }
         }
     }
 }
+
+// The low-rank steps of a CTA's tiles in order: tile, run, ranks.
+struct LoraStep {
+    int32_t id, r, r0, nruns;
+    Tile t;
+    Run run;
+};
 
 template <int CG, int LORA>
 __global__ void __launch_bounds__(threads_of(LORA), 1)
@@ -402,6 +451,8 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
     uint64_t* red_free = red_full + 1;
     uint64_t* t_full = red_free + 1;   // LORA_MMA: two buffers of t besides the stages
     uint64_t* t_empty = t_full + 2;
+    uint64_t* b_full = t_empty + 2;    // LORA_FMA: [half][slot]
+    uint64_t* b_empty = b_full + 2 * B_SLOTS;
 
     if (tid == 0) {
         s_abort = 0;
@@ -415,6 +466,10 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
             mbar_init(smem_u32(&t_full[i]), CG * LORA_WARPS);
             mbar_init(smem_u32(&t_empty[i]), 1);
         }
+        for (int i = 0; LORA == LORA_FMA && i < 2 * B_SLOTS; ++i) {
+            mbar_init(smem_u32(&b_full[i]), 1);
+            mbar_init(smem_u32(&b_empty[i]), EPI_WARPS / 2);
+        }
         mbar_init(smem_u32(red_full), 1);   // the expected bytes, then the stores' own counts
         mbar_init(smem_u32(red_free), csize * EPI_WARPS);
         fence_barrier_init();
@@ -422,7 +477,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
     if (warp == 0 && lane == 0) {
         for (int k = 0; k < NUM_XMAPS; ++k) prefetch_tmap(&xmaps.m[k]);
         prefetch_tmap(&wmap);
-        if (LORA == LORA_MMA) prefetch_tmap(&bmap);
+        if (LORA != LORA_NONE) prefetch_tmap(&bmap);
     }
     if (warp == 1) {
         if (CG == 2) tmem_alloc_pair(smem_u32(&s_tmem_base), (uint32_t)g.tmem_cols);
@@ -570,41 +625,98 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
         // ------------------------------------------------------------ t, ahead of the MMAs by up to two low-rank steps
         if (g.early) grid_dependency_wait();
         const int first = (warp - LORA_WARP) * 32 + lane;
+        const auto settle = [&](LoraStep& x) {   // to the next step that exists, from a place that may hold none
+            while (x.id < total && (x.r < 0 || x.r >= x.nruns)) {
+                if (x.r >= 0) x.id += ncl;
+                if (x.id >= total) break;
+                decode_tile(segs, nseg, g, x.id, WT, x.t);
+                x.nruns = lo.runs[x.t.row0].count;
+                x.r = 0;
+                x.r0 = 0;
+            }
+            if (x.id < total) x.run = lo.runs[x.t.row0 + x.r];
+        };
+        const auto request = [&](TRows& v, const LoraStep& x) {
+            const int32_t hs = x.t.ts / CG;
+            load_t(v, x.t.row0 + (CG == 2 ? (int32_t)crank * hs : 0), hs, x.run, x.r0, min(t_ranks, lo.R - x.r0), lo, first);
+        };
+        LoraStep step = {lora_here ? cid : total, -1, 0, 0, {}, {}};
+        TRows v;
         uint32_t m = 0;
         bool ok = true;
-        for (int32_t id = cid; ok && lora_here && id < total; id += ncl) {
-            decode_tile(segs, nseg, g, id, WT, t);
-            const int32_t hs = t.ts / CG;
-            const int32_t row0 = t.row0 + (CG == 2 ? (int32_t)crank * hs : 0);
-            const int32_t nruns = lo.runs[t.row0].count;
-            for (int32_t r = 0; ok && r < nruns; ++r) {
-                const Run run = lo.runs[t.row0 + r];
-                for (int32_t r0 = 0; r0 < lo.R; r0 += t_ranks, ++m) {
-                    const uint32_t buf = m & 1;
-                    TRows x;
-                    load_t(x, row0, hs, run, r0, lo, first);
-                    if (!warp_wait(smem_u32(&t_empty[buf]), ((m >> 1) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_CONVERT)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* dst = smem + g.off_t + buf * g.t_bytes;
-                    store_t(dst, x, hs, 0, lo.parts, first, bf16);
-                    if (min(t_ranks, lo.R - r0) > 16) {
-                        load_t(x, row0, hs, run, r0 + 16, lo, first);
-                        store_t(dst, x, hs, 16, lo.parts, first, bf16);
-                    }
-                    asm volatile("fence.proxy.async;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (CG == 2 && crank != 0) mbar_arrive_cluster(map_to_rank(smem_u32(&t_full[buf]), 0));
-                        else mbar_arrive(smem_u32(&t_full[buf]));
-                    }
-                }
+        settle(step);
+        if (step.id < total) request(v, step);
+        for (; step.id < total; ++m) {
+            const uint32_t buf = m & 1;
+            if (!warp_wait(smem_u32(&t_empty[buf]), ((m >> 1) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_CONVERT)) {
+                ok = false;
+                break;
+            }
+            store_t(smem + g.off_t + buf * g.t_bytes, v, step.t.ts / CG, min(t_ranks, lo.R - step.r0), lo.parts, first, bf16);
+            step.r0 += t_ranks;
+            if (step.r0 >= lo.R) {
+                step.r0 = 0;
+                ++step.r;
+            }
+            settle(step);
+            if (step.id < total) request(v, step);
+            asm volatile("fence.proxy.async;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2 && crank != 0) mbar_arrive_cluster(map_to_rank(smem_u32(&t_full[buf]), 0));
+                else mbar_arrive(smem_u32(&t_full[buf]));
             }
         }
         // the commits of the other CTA's MMAs free the buffers: none may be under way when this CTA ends
         for (int i = 0; CG == 2 && ok && i < 2; ++i, ++m)
             ok = warp_wait(smem_u32(&t_empty[m & 1]), ((m >> 1) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_CONVERT);
+    } else if (LORA == LORA_FMA && warp == B_WARP) {
+        // ------------------------------------------------------------ B and t of the tokens that this CTA finishes
+        if (g.early) grid_dependency_wait();
+        if (g.b_ranks > 0) {
+            const uint64_t pol = policy_evict_first();
+            const bool one = elect_one();
+            uint32_t slot[2] = {0, 0}, phase[2] = {1, 1};
+            bool ok = true;
+            for (int32_t id = cid; ok && id < total; id += ncl) {
+                decode_tile(segs, nseg, g, id, WT, t);
+                const int tw = csize > 1 ? ((t.ts + (int)csize - 1) / (int)csize + 3) & ~3 : t.ts;
+                const int t0 = (int)crank * tw, cnt = min(tw, t.rows - t0);
+                for (int i0 = 0; ok && half_token(0, i0, csize > 1) < cnt; i0 += 32) {
+                    int32_t mine[2];   // adapters of 32 tokens of each half, one per lane
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int tok = half_token(h, i0 + lane, csize > 1);
+                        mine[h] = tok < cnt ? lo.row_adapter[t.row0 + t0 + tok] : -1;
+                    }
+                    for (int i = 0; ok && i < 64; ++i) {
+                        const int h = i & 1;
+                        const int32_t a = __shfl_sync(0xffffffffu, h ? mine[1] : mine[0], i >> 1);
+                        if (a < 0) continue;
+                        const int64_t row = (int64_t)t.row0 + t0 + half_token(h, i0 + (i >> 1), csize > 1);
+                        for (int r0 = 0; ok && r0 < lo.R; r0 += g.b_ranks) {
+                            const uint32_t sl = h ? slot[1] : slot[0], ph = h ? phase[1] : phase[0];
+                            const uint32_t bar = smem_u32(&b_full[h * B_SLOTS + sl]), q = (uint32_t)(h * g.b_slots) + sl;
+                            ok = warp_wait(smem_u32(&b_empty[h * B_SLOTS + sl]), ph, abort_flag, DEVERR_TIMEOUT_PRODUCER);
+                            if (ok && one) {
+                                const uint32_t tb = (uint32_t)min(g.b_ranks, lo.R - r0) * 4u;
+                                mbar_expect_tx(bar, (uint32_t)g.b_bytes + tb);
+                                tma_load_3d(smem_u32(smem + g.off_t) + q * g.b_bytes, &bmap, r0, t.n0, a, bar, pol);
+                                bulk_load(smem_u32(smem + g.off_tr) + q * T_ROW, lo.t + row * lo.R + r0, tb, bar, pol);
+                            }
+                            const bool wrap = sl + 1 == (uint32_t)g.b_slots;
+                            if (h) {
+                                slot[1] = wrap ? 0 : sl + 1;
+                                phase[1] ^= wrap;
+                            } else {
+                                slot[0] = wrap ? 0 : sl + 1;
+                                phase[0] ^= wrap;
+                            }
+                        }
+                    }
+                }
+            }
+        }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA (the pair's first CTA)
         if ((CG == 1 || crank == 0) && elect_one()) {
@@ -697,7 +809,8 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
         }
         const int quad = warp % 4, half = (warp - 2) / 4;
         const int nl = quad * 32 + lane;
-        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + g.off_out + (warp - 2) * STAGE_ROWS);
+        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + g.off_out + (warp - 2) * g.turn_bytes);
+        uint32_t b_slot = 0, b_phase = 0;
         uint32_t n = 0, reds = 0;   // reds: exchanges in which this CTA owned tokens
         for (int32_t id = cid; id < total; id += ncl, ++n) {
             decode_tile(segs, nseg, g, id, WT, t);
@@ -711,13 +824,42 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
             float* delta = reinterpret_cast<float*>(smem + g.off_delta) + nl;           // [token][weight row]
             if (LORA == LORA_FMA) {
                 // while the K loop runs: the low-rank part of the tokens that this warp will store
-                for (int j0 = csize > 1 ? half * 8 : half * 32; j0 < cnt;) {
-                    float d[8];
-                    lora_delta(d, (int64_t)t.row0 + t0 + j0, cnt - j0, col, n_ok, lo, bf16);
+                if (g.b_ranks > 0) {
+                    bool ok = true;
+                    for (int i0 = 0; ok && half_token(half, i0, csize > 1) < cnt; i0 += 32) {
+                        const int mine = half_token(half, i0 + lane, csize > 1);
+                        const unsigned on = __ballot_sync(
+                            0xffffffffu, mine < cnt && lo.row_adapter[(int64_t)t.row0 + t0 + min(mine, cnt - 1)] >= 0);
+                        for (int i = 0; ok && i < 32; ++i) {
+                            const int tok = half_token(half, i0 + i, csize > 1);
+                            if (tok >= cnt) break;
+                            float d = 0.f;
+                            for (int r0 = 0; ok && ((on >> i) & 1) && r0 < lo.R; r0 += g.b_ranks) {
+                                const uint32_t at = (uint32_t)half * B_SLOTS + b_slot, q = (uint32_t)(half * g.b_slots) + b_slot;
+                                ok = warp_wait(smem_u32(&b_full[at]), b_phase, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
+                                if (!ok) break;
+                                d += lora_dot(smem + g.off_t + q * g.b_bytes, nl, g.b_ranks, min(g.b_ranks, lo.R - r0),
+                                              reinterpret_cast<const float*>(smem + g.off_tr + q * T_ROW), bf16);
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(smem_u32(&b_empty[at]));
+                                if (++b_slot == (uint32_t)g.b_slots) {
+                                    b_slot = 0;
+                                    b_phase ^= 1;
+                                }
+                            }
+                            delta[tok * WROWS] = d;
+                        }
+                    }
+                    if (!ok) break;
+                } else {
+                    for (int i = 0; half_token(half, i, csize > 1) < cnt; i += 8) {
+                        const int j0 = half_token(half, i, csize > 1);
+                        float d[8];
+                        lora_delta(d, (int64_t)t.row0 + t0 + j0, cnt - j0, col, n_ok, lo, bf16);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j0 + j < tw) delta[(j0 + j) * WROWS] = d[j];
-                    j0 += csize > 1 ? 16 : (j0 & 31) == 24 ? 40 : 8;
+                        for (int j = 0; j < 8; ++j)
+                            if (j0 + j < tw) delta[(j0 + j) * WROWS] = d[j];
+                    }
                 }
             }
             if (!warp_wait(smem_u32(&acc_full[acc]), (n >> 1) & 1, abort_flag, DEVERR_TIMEOUT_EPILOGUE)) break;
@@ -840,24 +982,58 @@ struct Shape {
     int cg, tn, splits;
 };
 
+// Ranks that one TMA box of B holds for LORA_FMA: the rank padded to a power of two, at most 64.
+inline int b_box_ranks(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 64; }
+
+constexpr int turn_bytes(int splits) { return splits > 1 ? 8 * 64 : 32 * 64; }   // 8 or 32 tokens x 32 halves per warp
+
 // What a plan is made for, besides the problem.
 struct Want {
     bool dense;      // one segment of all rows
     bool early;
     int lora;        // LoraMode
     int R;
+    int b_tma;       // LORA_FMA: TMA can read B
     int sm_count;
     int clusters[4]; // clusters of 1, 2, 4, 8 CTAs that fit on the device at a time
     int forced_cg;   // 0: the cost model chooses
 };
 
-// The form with the least estimated time, in SM cycles.  A CTA's stage takes as
-// long as its MMAs (2 cycles per token column for 128 weight rows and 64 of K)
-// or its loads (64 bytes a cycle from L2); a tile adds a fixed cost, a shared
-// one the exchange of the partial sums, LORA_FMA its reads of B and its
-// arithmetic.  The whole takes at least as long as memory needs for the weights
-// (3500 bytes a cycle).  Segments are taken as equally long, since their
-// lengths are on the device.
+// Rows of the TMA box of x that holds this many.
+inline int x_box_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
+// Shared memory of a form besides the stages and the segment table.
+struct Extra {
+    int t, b_ranks, b_slots, out, delta, red;
+    int total() const { return 2 * t + 2 * b_slots * (b_ranks * WROWS * 2 + T_ROW) + out + delta + red; }
+};
+
+inline Extra extra_of(const Shape& sh, const Want& w) {
+    Extra e;
+    const int own = ((sh.tn + sh.splits - 1) / sh.splits + 3) & ~3;   // tokens a CTA finishes
+    e.t = w.lora == LORA_MMA ? x_box_rows(sh.tn / sh.cg < 64 ? 64 : sh.tn / sh.cg) * 128 : 0;
+    e.b_ranks = w.lora == LORA_FMA && w.b_tma ? b_box_ranks(w.R) : 0;
+    e.b_slots = 0;
+    if (e.b_ranks) {
+        e.b_slots = B_RING / (e.b_ranks * WROWS * 2);
+        e.b_slots = e.b_slots > B_SLOTS ? B_SLOTS : e.b_slots < 2 ? 2 : e.b_slots;
+    }
+    e.out = EPI_WARPS * turn_bytes(sh.splits);
+    e.delta = w.lora == LORA_FMA ? own * WROWS * 4 : 0;
+    e.red = sh.splits > 1 ? sh.splits * own * WROWS * 4 : 0;
+    return e;
+}
+
+inline int stage_bytes(const Shape& sh) { return W_TILE + x_box_rows(sh.tn / sh.cg) * 128; }
+
+// The form with the least estimated time, in SM cycles.  A tile takes the
+// longest of: its loads at 64 bytes a cycle (weights, x, and B for LORA_FMA),
+// its MMAs (2 cycles per token column for 128 weight rows and 64 of K),
+// LORA_FMA's arithmetic, and the loads' latency over the stages under way;
+// plus a fixed cost, and for a shared tile the exchange of the partial sums.
+// The whole takes at least as long as memory needs for the weights (3500 bytes
+// a cycle).  Segments are taken as equally long, since their lengths are on the
+// device.
 inline Shape choose_shape(const Problem& p, const Want& w) {
     const int64_t rows = p.x_rows < p.out_rows ? p.x_rows : p.out_rows;
     const int64_t segs = w.dense ? 1 : (p.batches < rows ? p.batches : rows);
@@ -867,28 +1043,37 @@ inline Shape choose_shape(const Problem& p, const Want& w) {
     const double memory = experts * (double)p.N * p.K * 2.0 / 3500.0;
     Shape best{1, 32, 1};
     double best_cost = -1;
-    const int tns[2][3] = {{32, 64, 128}, {64, 128, 256}};
+    const int tns[2][5] = {{32, 48, 64, 96, 128}, {64, 96, 128, 192, 256}};
     for (int cg = 1; cg <= 2; ++cg) {
         if (w.lora == LORA_FMA ? cg == 2 : w.forced_cg && cg != w.forced_cg) continue;
-        for (int ti = 0; ti < 3; ++ti) {
+        for (int ti = 0; ti < 5; ++ti) {
             const int tn = tns[cg - 1][ti];
             const int64_t nt = (mean + tn - 1) / tn;
             const int64_t ts = ((mean + nt - 1) / nt + 16 * cg - 1) / (16 * cg) * (16 * cg);
             const int64_t tiles = segs * nt * ((p.N + WROWS * cg - 1) / (WROWS * cg));
             for (int lg = 0, sp = 1; sp <= (cg == 1 ? MAX_SPLITS : 1); sp *= 2, ++lg) {
                 if (sp > 1 && kblocks < 4 * sp) break;
+                const Shape sh{cg, tn, sp};
+                const Extra e = extra_of(sh, w);
+                const int stages = (SMEM_LIMIT - 4096 - e.total()) / stage_bytes(sh);
+                if (stages < 2) continue;
                 const int64_t workers = w.clusters[cg == 2 ? 1 : lg] > 0 ? w.clusters[cg == 2 ? 1 : lg] : 1;
                 const int64_t waves = (tiles + workers - 1) / workers;
-                const double load = (W_TILE + (double)ts / cg * 128) / 64.0;
-                const double mma = 2.0 * ts;
+                const double kb = (double)((kblocks + sp - 1) / sp);
                 const double own = (double)((ts + sp - 1) / sp);   // tokens a CTA finishes
-                const double fma = w.lora == LORA_FMA ? own * w.R * (256.0 / 50.0 + 2.0) : 0.0;
-                const double body = (double)((kblocks + sp - 1) / sp) * (load > mma ? load : mma);
-                const double path = waves * ((body > fma ? body : fma) + 600.0) + (sp > 1 ? 1500.0 : 0.0) + 16.0 * own;
+                const double load = (kb * (W_TILE + x_box_rows((int)(ts / cg)) * 128.0) + own * e.b_ranks * WROWS * 2.0) / 64.0;
+                const double mma = kb * 2.0 * ts;
+                const double alu = w.lora != LORA_FMA ? 0.0 : own * w.R * (w.b_tma ? 4.0 : 30.0) + 1000.0;
+                const double late = kb * 1500.0 / stages;
+                double body = load > mma ? load : mma;
+                if (body < alu) body = alu;
+                if (body < late) body = late;
+                const double exchange = sp > 1 ? 1200.0 + 16.0 * ts : 0.0;
+                const double path = waves * (body + exchange + 600.0) + 16.0 * own;
                 const double cost = (path > memory ? path : memory) + 0.1 * path;
                 if (best_cost < 0 || cost < best_cost * 0.97) {
                     best_cost = cost;
-                    best = Shape{cg, tn, sp};
+                    best = sh;
                 }
             }
         }
@@ -916,17 +1101,22 @@ inline bool make_plan(const Problem& p, const Want& w, EncodeTiledFn enc, Plan* 
     g.acc_stride = sh.tn < 32 ? 32 : sh.tn;
     g.tmem_cols = 32;
     while (g.tmem_cols < 2 * g.acc_stride) g.tmem_cols *= 2;
-    g.stage_bytes = W_TILE + (sh.tn / sh.cg) * 128;
-    const int red = sh.splits > 1 ? sh.splits * (((sh.tn + sh.splits - 1) / sh.splits + 3) & ~3) * WROWS * 4 : 0;
+    g.stage_bytes = stage_bytes(sh);
+    g.turn_bytes = turn_bytes(sh.splits);
+    const Extra e = extra_of(sh, w);
+    g.t_bytes = e.t;
+    g.b_ranks = e.b_ranks;
+    g.b_slots = e.b_slots;
+    g.b_bytes = e.b_ranks * WROWS * 2;
     for (g.stages = 12; g.stages >= 2; --g.stages) {
-        g.off_t = g.stages * g.stage_bytes;
-        g.t_bytes = w.lora == LORA_MMA ? (sh.tn / sh.cg < 64 ? 64 : sh.tn / sh.cg) * 128 : 0;
-        g.off_out = g.off_t + 2 * g.t_bytes;
-        g.off_delta = g.off_out + EPI_WARPS * STAGE_ROWS;
-        g.off_red = g.off_delta + (w.lora == LORA_FMA ? ((sh.tn + sh.splits - 1) / sh.splits + 3) / 4 * 4 * WROWS * 4 : 0);
-        g.off_seg = g.off_red + red;
+        g.off_t = g.stages * g.stage_bytes;                       // t or B (1024-byte aligned: swizzled)
+        g.off_tr = g.off_t + 2 * e.t + 2 * e.b_slots * g.b_bytes;
+        g.off_out = g.off_tr + 2 * e.b_slots * T_ROW;
+        g.off_delta = g.off_out + e.out;
+        g.off_red = g.off_delta + e.delta;
+        g.off_seg = g.off_red + e.red;
         g.off_bar = (g.off_seg + (int)segs * (int)sizeof(Seg) + 15) & ~15;
-        out->smem_bytes = g.off_bar + 8 * (2 * g.stages + 10) + 1024;
+        out->smem_bytes = g.off_bar + 8 * (2 * g.stages + 10 + 4 * B_SLOTS) + 1024;
         if (out->smem_bytes <= SMEM_LIMIT) break;
     }
     if (g.stages < 2) return false;
@@ -999,7 +1189,7 @@ inline bool cluster_capacity(int device, int sm_count, int (&out)[4]) {
 }
 
 // Plans of recent calls, keyed by every field of the problem, the wishes and the device.
-inline bool cached_plan(const Problem& p, bool dense, bool early, int lora, int R, int sm_count, int forced_cg,
+inline bool cached_plan(const Problem& p, bool dense, bool early, int lora, int R, bool b_tma, int sm_count, int forced_cg,
                         EncodeTiledFn enc, Plan* out) {
     static PlanCache<PlanKey, Plan> cache;
     PlanKey key;
@@ -1009,6 +1199,7 @@ inline bool cached_plan(const Problem& p, bool dense, bool early, int lora, int 
     key.w.early = early;
     key.w.lora = lora;
     key.w.R = R;
+    key.w.b_tma = b_tma;
     key.w.sm_count = sm_count;
     key.w.forced_cg = forced_cg;
     if (cudaGetDevice(&key.device) != cudaSuccess || !cluster_capacity(key.device, sm_count, key.w.clusters)) return false;
@@ -1049,17 +1240,22 @@ inline int32_t dense_tile_rows(const Geo& g, int cg) {
     return nt > 0 ? ((rows + nt - 1) / nt + step - 1) / step * step : step;
 }
 
-// Tensor map of lora_b (adapters, N, R) for LORA_MMA; false where TMA cannot read it.
-inline bool encode_b(const Lora& lo, int64_t N, int64_t adapters, EncodeTiledFn enc, CUtensorMap* out) {
+// Tensor map of lora_b (adapters, N, R) with boxes of `ranks` x 128 rows, rows
+// swizzled by their width; false where TMA cannot read it.
+inline bool encode_b(const Lora& lo, int ranks, int64_t N, int64_t adapters, EncodeTiledFn enc, CUtensorMap* out) {
     if (!enc || !lo.b_vec || lo.R % 8 || lo.b_ns < lo.R || adapters >= (int64_t(1) << 31)) return false;
     if (lo.b_ns >= (int64_t(1) << 38) || lo.b_as >= (int64_t(1) << 38)) return false;
     if (adapters > 1 && lo.b_as < (N - 1) * lo.b_ns + lo.R) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)lo.R, (cuuint64_t)N, (cuuint64_t)adapters};
     const cuuint64_t strides[2] = {(cuuint64_t)(lo.b_ns * 2),
                                    (cuuint64_t)(adapters > 1 ? lo.b_as * 2 : (N * lo.b_ns * 2 + 15) / 16 * 16)};
-    const cuuint32_t box[3] = {64, WROWS, 1}, ones[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)ranks, WROWS, 1}, ones[3] = {1, 1, 1};
+    const CUtensorMapSwizzle sw = ranks == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                  : ranks == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                  : ranks == 16 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                                : CU_TENSOR_MAP_SWIZZLE_NONE;
     return enc(out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(lo.b), dims, strides, box, ones,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

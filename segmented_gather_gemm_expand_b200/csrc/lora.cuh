@@ -32,6 +32,7 @@ row_runs_kernel(Problem p, int32_t* row_adapter, grp::Run* runs, int32_t tile_ro
     __shared__ Segment s_seg[ROWS_THREADS];
     __shared__ int32_t s_a[ROWS_THREADS + 1];
     __shared__ int32_t s_warp[ROWS_THREADS / 32];
+    __shared__ unsigned s_change[ROWS_THREADS / 32];
     tc::grid_dependency_wait();
     tc::grid_dependents_launch();
     const int tid = threadIdx.x;
@@ -52,9 +53,12 @@ row_runs_kernel(Problem p, int32_t* row_adapter, grp::Run* runs, int32_t tile_ro
     s_a[tid + 1] = a;
     if (tid == 0) s_a[0] = -1;
     __syncthreads();
-    const bool begins = a >= 0 && s_a[tid] != a;
-    const unsigned mask = __ballot_sync(0xffffffffu, begins);
-    if (tid % 32 == 0) s_warp[tid / 32] = __popc(mask);
+    const bool changes = s_a[tid] != a, begins = a >= 0 && changes;
+    const unsigned mask = __ballot_sync(0xffffffffu, begins), change = __ballot_sync(0xffffffffu, changes);
+    if (tid % 32 == 0) {
+        s_warp[tid / 32] = __popc(mask);
+        s_change[tid / 32] = change;
+    }
     __syncthreads();
     int32_t at = __popc(mask & ((1u << (tid % 32)) - 1)), total = 0;
     for (int w = 0; w < ROWS_THREADS / 32; ++w) {
@@ -62,10 +66,12 @@ row_runs_kernel(Problem p, int32_t* row_adapter, grp::Run* runs, int32_t tile_ro
         total += s_warp[w];
     }
     if (begins) {
-        int32_t end = tid + 1;
-        while (end < ROWS_THREADS && s_a[end + 1] == a) ++end;
-        grp::Run r{a, (int32_t)row, (int32_t)(row0 + end), total};
-        runs[row0 + at] = r;
+        // the run ends at the next change: in this warp, or the first one of a later warp
+        unsigned after = change & ~((2u << (tid % 32)) - 1);
+        int w = tid / 32;
+        while (!after && ++w < ROWS_THREADS / 32) after = s_change[w];
+        const int32_t end = after ? w * 32 + __ffs(after) - 1 : ROWS_THREADS;
+        runs[row0 + at] = grp::Run{a, (int32_t)row, (int32_t)(row0 + end), total};
     }
     if (tid == 0 && total == 0) runs[row0] = grp::Run{-1, 0, 0, 0};
 }

@@ -543,7 +543,7 @@ int validate_grouped(const sgmv_tensor* x, const sgmv_tensor* w, const sgmv_tens
 
 int choose_grouped(const Call& c, const DeviceInfo& dev, int forced, grp::Plan* pl) {
     const bool tc_ok = forced != SGMV_VARIANT_SIMT && dev.cc_major == 10 &&
-                       grp::cached_plan(c.p, false, false, grp::LORA_NONE, 0, dev.sm_count, forced_cg(forced), tc::encode_fn(), pl);
+                       grp::cached_plan(c.p, false, false, grp::LORA_NONE, 0, false, dev.sm_count, forced_cg(forced), tc::encode_fn(), pl);
     return large_variant(tc_ok, forced);
 }
 
@@ -700,10 +700,13 @@ int choose_lora(LoraCall* c, const DeviceInfo& dev, int forced, char* ws, size_t
     }
     const bool tc = forced != SGMV_VARIANT_SIMT && dev.cc_major == 10;
     // K steps pay from a few rows per segment on: a run costs an MMA over its whole token tile
-    const bool mma = tc && c->low_rank && c->rows >= kMmaRunRows * c->shrink.batches &&
-                     grp::encode_b(c->lo, c->base.N, c->shrink.lora_num, tc::encode_fn(), &pl->bm);
+    const bool long_runs = c->rows >= kMmaRunRows * c->shrink.batches;
+    const bool b_tma = tc && c->low_rank &&
+                       grp::encode_b(c->lo, long_runs ? 64 : grp::b_box_ranks(c->lo.R), c->base.N, c->shrink.lora_num,
+                                     tc::encode_fn(), &pl->bm);
+    const bool mma = b_tma && long_runs;
     pl->lora = !c->low_rank ? grp::LORA_NONE : mma ? grp::LORA_MMA : grp::LORA_FMA;
-    const bool tc_ok = tc && grp::cached_plan(c->base, true, c->low_rank, pl->lora, c->lo.R, dev.sm_count,
+    const bool tc_ok = tc && grp::cached_plan(c->base, true, c->low_rank, pl->lora, c->lo.R, b_tma, dev.sm_count,
                                               forced_cg(forced), tc::encode_fn(), &pl->base);
     pl->variant = large_variant(tc_ok, forced);
     if (pl->variant < 0) return pl->variant;
@@ -721,7 +724,7 @@ int choose_lora(LoraCall* c, const DeviceInfo& dev, int forced, char* ws, size_t
             const size_t room = ws_bytes > (size_t)c->off_part ? ws_bytes - (size_t)c->off_part : 0;
             while (sp > 1 && (size_t)shr::workspace_bytes_for(c->shrink, sp) > room) sp /= 2;
             pl->splits = sp;
-        } else if (grp::cached_plan(c->shrink, false, false, grp::LORA_NONE, 0, dev.sm_count, 0, tc::encode_fn(),
+        } else if (grp::cached_plan(c->shrink, false, false, grp::LORA_NONE, 0, false, dev.sm_count, 0, tc::encode_fn(),
                                     &pl->product)) {
             pl->shrink = LoraPlan::PRODUCT;
         }
@@ -754,7 +757,7 @@ int run_lora(const LoraCall& c, const DeviceInfo& dev, const LoraPlan& pl, char*
     if (pl.variant == SGMV_VARIANT_TC) {
         switch (pl.lora) {
             case grp::LORA_MMA: return grp::launch<grp::LORA_MMA>(pl.base, pl.bm, c.base, c.lo, st);
-            case grp::LORA_FMA: return grp::launch_kernel<1, grp::LORA_FMA>(pl.base, CUtensorMap{}, c.base, c.lo, st);
+            case grp::LORA_FMA: return grp::launch_kernel<1, grp::LORA_FMA>(pl.base, pl.bm, c.base, c.lo, st);
             default: return grp::launch<grp::LORA_NONE>(pl.base, CUtensorMap{}, c.base, c.lo, st);
         }
     }

@@ -285,7 +285,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     } else {
         // ------------------------------------------------------------ epilogue
         const int quad = warp % 4, half = (warp - 2) / 4;
-        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + g.off_out + (warp - 2) * grp::STAGE_ROWS);
+        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + g.off_out + (warp - 2) * grp::turn_bytes(1));
         uint32_t n = 0;
         for (int32_t id = cid; id < total; id += ncl, ++n) {
             int32_t e, k0, n0;
@@ -394,7 +394,7 @@ inline bool make_plan(const Problem& p, int64_t y_cs, int64_t out_gs, int64_t ou
     while (g.tmem_cols < 2 * g.acc_stride) g.tmem_cols *= 2;
     for (g.stages = 7; g.stages >= 2; --g.stages) {
         g.off_out = g.stages * STAGE;
-        g.off_seg = g.off_out + EPI_WARPS * grp::STAGE_ROWS;
+        g.off_seg = g.off_out + EPI_WARPS * grp::turn_bytes(1);
         g.off_exp = g.off_seg + (int)p.batches * (int)sizeof(Seg);
         g.off_bar = (g.off_exp + (int)p.lora_num * (int)sizeof(Exp) + 15) & ~15;
         out->smem_bytes = g.off_bar + 8 * (3 * g.stages + 4) + 1024;
