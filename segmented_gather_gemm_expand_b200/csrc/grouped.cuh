@@ -96,6 +96,8 @@ struct Geo {
     int32_t acc_stride, tmem_cols;
     int32_t w_mn;         // the weights' N axis is the contiguous one
     int32_t dense_rows;   // >= 0: one segment of that many rows with group 0; -1: the call's segments
+    int32_t dense_ts, dense_tiles;       // its tile height and token tiles
+    int32_t off_runs, max_runs;          // LORA_MMA: runs, each token tile's first run, the call's segments
     int32_t early;        // the preceding kernel is the adapters' shrink, which writes neither x nor weights
     int32_t keep_w;       // weights are read by several token tiles: keep them in L2
 };
@@ -104,17 +106,18 @@ struct XMaps {
     CUtensorMap m[NUM_XMAPS];
 };
 
-// A run of neighbouring rows of one token tile that share an adapter.
+// Rows of one token tile that belong to one segment with an adapter.
 struct Run {
-    int32_t adapter, begin, end;   // rows [begin, end)
-    int32_t count;                 // in the tile's first record: runs of the tile (may be 0)
+    int32_t adapter, begin, end;   // rows [begin, end), counted from the tile's first
 };
 
 // The low-rank part and the bias of a shared projection.
 struct Lora {
     const float* t;              // (rows, R) fp32: x A^T
     const int32_t* row_adapter;  // LORA_FMA, (rows): adapter, -1 for none
-    const Run* runs;             // LORA_MMA, (rows): the runs of a tile from its first row's place on
+    MetaVec start, len, idx;     // LORA_MMA: the call's segments
+    int32_t batches;
+    int64_t adapters;
     const void* b;               // (adapters, N, R), the weights' dtype
     int64_t b_as, b_ns, b_ks;
     int32_t R;
@@ -126,18 +129,22 @@ struct Lora {
 
 struct Tile {
     int32_t row0, rows, ts, n0, group;
+    int32_t tok;   // token tile within the segment
 };
 
 __device__ __forceinline__ void decode_tile(const Seg* segs, int32_t nseg, const Geo& g, int32_t id, int32_t wtile,
                                             Tile& t) {
-    const int32_t key = id / g.nblk;
-    int lo = 0, hi = nseg - 1;   // last segment whose prefix <= key (empty ones share their successor's)
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (segs[mid].prefix <= key) lo = mid;
-        else hi = mid - 1;
+    Seg s{0, g.dense_rows, 0, g.dense_ts, 0};
+    if (g.dense_rows < 0) {
+        const int32_t key = id / g.nblk;
+        int lo = 0, hi = nseg - 1;   // last segment whose prefix <= key (empty ones share their successor's)
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (segs[mid].prefix <= key) lo = mid;
+            else hi = mid - 1;
+        }
+        s = segs[lo];
     }
-    const Seg s = segs[lo];
     const int32_t nt = (s.rows + s.ts - 1) / s.ts;
     // bands of BAND token tiles; within a band the token tile is fastest, so the
     // CTAs at work share few weight tiles and few x tiles
@@ -151,6 +158,60 @@ __device__ __forceinline__ void decode_tile(const Seg* segs, int32_t nseg, const
     t.rows = min(s.ts, s.rows - tok * s.ts);
     t.ts = s.ts;
     t.group = s.group;
+    t.tok = tok;
+}
+
+// The runs of every token tile of a dense call, in segment order: `runs`, and
+// first[i] .. first[i + 1] for tile i.  Built by warps 2 and up (they alone
+// synchronise, on barrier 2) while the first loads are under way; overlapping
+// segments may fill the list early (max_runs), the same way in every CTA.
+template <int WARPS>
+__device__ __forceinline__ void build_runs(const Geo& g, const Lora& lo, Run* runs, int32_t* first, Run* segs, int warp,
+                                           int lane) {
+    constexpr int THREADS = WARPS * 32;
+    for (int32_t b = warp * 32 + lane; b < lo.batches; b += THREADS) {
+        const int64_t start = load_meta(lo.start, b), len = load_meta(lo.len, b), a = load_meta(lo.idx, b);
+        const int64_t end = len > g.dense_rows - start ? (int64_t)g.dense_rows : start + len;
+        const bool ok = a >= 0 && a < lo.adapters && start >= 0 && start < g.dense_rows && len > 0;
+        segs[b] = ok ? Run{(int32_t)a, (int32_t)start, (int32_t)end} : Run{-1, 0, 0};
+    }
+    bar_sync(2, THREADS);
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int32_t i = warp; i < g.dense_tiles; i += WARPS) {
+            const int32_t r0 = i * g.dense_ts, r1 = min(r0 + g.dense_ts, g.dense_rows);
+            int32_t at = pass ? first[i] : 0;
+            for (int32_t b0 = 0; b0 < lo.batches; b0 += 32) {
+                const Run s = b0 + lane < lo.batches ? segs[b0 + lane] : Run{-1, 0, 0};
+                const bool in = s.begin < r1 && s.end > r0;
+                const unsigned mask = __ballot_sync(0xffffffffu, in);
+                if (pass && in) {
+                    const int32_t k = at + __popc(mask & ((1u << lane) - 1));
+                    if (k < g.max_runs) runs[k] = Run{s.adapter, max(s.begin, r0) - r0, min(s.end, r1) - r0};
+                }
+                at += __popc(mask);
+            }
+            if (!pass && lane == 0) first[i + 1] = at;
+        }
+        bar_sync(2, THREADS);
+        if (!pass) {
+            if (warp == 0) {   // counts to places
+                int32_t run = 0;
+                for (int32_t i0 = 0; i0 < g.dense_tiles; i0 += 32) {
+                    const int32_t i = i0 + lane, n = i < g.dense_tiles ? first[i + 1] : 0;
+                    int32_t v = n;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
+                        if (lane >= o) v += u;
+                    }
+                    if (i < g.dense_tiles) first[i + 1] = min(run + v, g.max_runs);
+                    run += __shfl_sync(0xffffffffu, v, 31);
+                }
+                if (lane == 0) first[0] = 0;
+            }
+            bar_sync(2, THREADS);
+        }
+    }
 }
 
 // d[j] = sum_k t[row + j, k] * B[adapter of row + j][n, k] for j < valid, in
@@ -378,32 +439,32 @@ __device__ __forceinline__ uint32_t next_part(float& a, float& b, bool bf16) {
     return bits;
 }
 
-// A low-rank step's t: rows row0 .. row0 + 127 of t, ranks [r0, r0 + C), as a
-// K-major tile with 128-byte swizzle: `parts` groups of C columns (C = 32 for
-// two parts, 16 for three), zero outside the run and past the last rank.  A
-// lane holds two rows (`first`, `first` + 64) of up to 32 ranks, all requested
-// at once, and for the step after the one it writes.
+// A low-rank step's t: `rows` (at most 128) rows of t from row0 on, ranks [r, r +
+// ranks), as a K-major tile with 128-byte swizzle: `parts` groups of C columns
+// (C = 32 for two parts, 16 for three), zero outside rows [begin, end) of the
+// tile and past the last rank.  One warp; a lane takes two rows at a time (i0 +
+// lane, i0 + lane + 32), all their ranks requested at once.
 struct TRows {
     float4 q[2][8];
 };
 
-__device__ __forceinline__ void load_t(TRows& x, int64_t row0, int rows, const Run& run, int r, int ranks, const Lora& lo,
-                                       int first) {
+__device__ __forceinline__ void load_t(TRows& x, int64_t row0, int i0, int begin, int end, int r, int ranks, const Lora& lo,
+                                       int lane) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int64_t row = row0 + first + 64 * i;
-        const bool in = first + 64 * i < rows && row >= run.begin && row < run.end;
-        const float4* src = reinterpret_cast<const float4*>(lo.t + row * lo.R + r);   // R, r: multiples of 8
+        const int k0 = i0 + lane + 32 * i;
+        const bool in = k0 >= begin && k0 < end;
+        const float4* src = reinterpret_cast<const float4*>(lo.t + (row0 + k0) * lo.R + r);   // R, r: multiples of 8
 #pragma unroll
         for (int k = 0; k < 8; ++k) x.q[i][k] = in && 4 * k < ranks ? src[k] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
-__device__ __forceinline__ void store_t(uint8_t* dst, TRows& x, int rows, int ranks, int parts, int first, bool bf16) {
+__device__ __forceinline__ void store_t(uint8_t* dst, TRows& x, int i0, int rows, int ranks, int parts, int lane, bool bf16) {
     const int C = parts == 2 ? 32 : 16;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int row = first + 64 * i;
+        const int row = i0 + lane + 32 * i;
         if (row >= rows) continue;
         for (int part = 0; part < parts; ++part) {
 #pragma unroll
@@ -419,12 +480,14 @@ __device__ __forceinline__ void store_t(uint8_t* dst, TRows& x, int rows, int ra
     }
 }
 
-// The low-rank steps of a CTA's tiles in order: tile, run, ranks.
-struct LoraStep {
-    int32_t id, r, r0, nruns;
-    Tile t;
-    Run run;
-};
+// The token columns of a run's MMA: the whole tile for a CTA pair, whose second
+// half of the columns is the other CTA's; the 16-column groups that the run
+// touches for a single CTA.
+template <int CG>
+__device__ __forceinline__ void run_columns(const Run& run, int32_t ts, int32_t& off, int32_t& cols) {
+    off = CG == 2 ? 0 : run.begin & ~15;
+    cols = CG == 2 ? ts : min(ts, (run.end + 15) & ~15) - off;
+}
 
 template <int CG, int LORA>
 __global__ void __launch_bounds__(threads_of(LORA), 1)
@@ -454,79 +517,99 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
     uint64_t* b_full = t_empty + 2;    // LORA_FMA: [half][slot]
     uint64_t* b_empty = b_full + 2 * B_SLOTS;
 
-    if (tid == 0) {
-        s_abort = 0;
-        for (uint32_t i = 0; i < S; ++i) {
-            mbar_init(smem_u32(&full[i]), 1);   // the first CTA of a pair announces the bytes of both
-            mbar_init(smem_u32(&empty[i]), 1);
+    // The table of runs (LORA_MMA) and its barrier.
+    uint64_t* runs_ready = b_empty + 2 * B_SLOTS;
+    Run* runs = reinterpret_cast<Run*>(smem + g.off_runs);
+    int32_t* first_run = reinterpret_cast<int32_t*>(runs + g.max_runs);
+    const bool dense = LORA != LORA_NONE || g.dense_rows >= 0;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            s_abort = 0;
+            for (uint32_t i = 0; i < S; ++i) {
+                mbar_init(smem_u32(&full[i]), 1);   // the first CTA of a pair announces the bytes of both
+                mbar_init(smem_u32(&empty[i]), 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_u32(&acc_full[i]), 1);
+                mbar_init(smem_u32(&acc_empty[i]), CG * EPI_WARPS);
+                mbar_init(smem_u32(&t_full[i]), CG);
+                mbar_init(smem_u32(&t_empty[i]), 1);
+            }
+            for (int i = 0; LORA == LORA_FMA && i < 2 * B_SLOTS; ++i) {
+                mbar_init(smem_u32(&b_full[i]), 1);
+                mbar_init(smem_u32(&b_empty[i]), EPI_WARPS / 2);
+            }
+            mbar_init(smem_u32(red_full), 1);   // the expected bytes, then the stores' own counts
+            mbar_init(smem_u32(red_free), csize * EPI_WARPS);
+            mbar_init(smem_u32(runs_ready), 1);
+            fence_barrier_init();
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&acc_full[i]), 1);
-            mbar_init(smem_u32(&acc_empty[i]), CG * EPI_WARPS);
-            mbar_init(smem_u32(&t_full[i]), CG * LORA_WARPS);
-            mbar_init(smem_u32(&t_empty[i]), 1);
-        }
-        for (int i = 0; LORA == LORA_FMA && i < 2 * B_SLOTS; ++i) {
-            mbar_init(smem_u32(&b_full[i]), 1);
-            mbar_init(smem_u32(&b_empty[i]), EPI_WARPS / 2);
-        }
-        mbar_init(smem_u32(red_full), 1);   // the expected bytes, then the stores' own counts
-        mbar_init(smem_u32(red_free), csize * EPI_WARPS);
-        fence_barrier_init();
-    }
-    if (warp == 0 && lane == 0) {
-        for (int k = 0; k < NUM_XMAPS; ++k) prefetch_tmap(&xmaps.m[k]);
-        prefetch_tmap(&wmap);
-        if (LORA != LORA_NONE) prefetch_tmap(&bmap);
-    }
-    if (warp == 1) {
+        __syncwarp();
+    } else if (warp == 1) {
         if (CG == 2) tmem_alloc_pair(smem_u32(&s_tmem_base), (uint32_t)g.tmem_cols);
         else tmem_alloc(smem_u32(&s_tmem_base), (uint32_t)g.tmem_cols);
+    } else if (warp == 2 && lane == 0) {
+        prefetch_tmap(&wmap);
+        for (int k = 0; k < NUM_XMAPS; ++k) prefetch_tmap(&xmaps.m[k]);
+        if (LORA != LORA_NONE) prefetch_tmap(&bmap);
     }
 
     // Everything below may read memory written by the preceding kernel, unless
-    // that is the adapters' shrink: then only the epilogue waits for it.
+    // that is the adapters' shrink: then only what reads t waits for it.
     if (!g.early) {
         grid_dependency_wait();
         grid_dependents_launch();
     }
 
-    // Segment table (guards of sgmv.h applied), tile size and tiles of earlier segments.
-    const int32_t nseg = g.dense_rows >= 0 ? 1 : (int32_t)p.batches;
-    constexpr int32_t STEP = 16 * CG;
-    for (int32_t b = tid; b < nseg; b += THREADS) {
-        Segment s;
-        if (g.dense_rows >= 0) s = Segment{0, g.dense_rows, 0};
-        else s = load_segment(p, b);
-        const int32_t rows = (int32_t)s.rows;
-        const int32_t nt = (rows + g.tn - 1) / g.tn;
-        const int32_t ts = nt > 0 ? ((rows + nt - 1) / nt + STEP - 1) / STEP * STEP : STEP;
-        segs[b] = Seg{(int32_t)s.row0, rows, (int32_t)s.adapter, ts, 0};
-    }
-    __syncthreads();
-    if (warp == 0) {
-        int32_t run = 0;
-        for (int32_t base = 0; base < nseg; base += 32) {
-            const int32_t b = base + lane;
-            const int32_t nt = b < nseg ? (segs[b].rows + segs[b].ts - 1) / segs[b].ts : 0;
-            int32_t v = nt;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int32_t t = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += t;
-            }
-            if (b < nseg) segs[b].prefix = run + v - nt;
-            run += __shfl_sync(0xffffffffu, v, 31);
+    const int32_t nseg = dense ? 1 : (int32_t)p.batches;
+    if (!dense) {
+        // Segment table (guards of sgmv.h applied), tile size and tiles of earlier segments.
+        constexpr int32_t STEP = 16 * CG;
+        for (int32_t b = tid; b < nseg; b += THREADS) {
+            const Segment s = load_segment(p, b);
+            const int32_t rows = (int32_t)s.rows;
+            const int32_t nt = (rows + g.tn - 1) / g.tn;
+            const int32_t ts = nt > 0 ? ((rows + nt - 1) / nt + STEP - 1) / STEP * STEP : STEP;
+            segs[b] = Seg{(int32_t)s.row0, rows, (int32_t)s.adapter, ts, 0};
         }
-        if (lane == 0) s_token_tiles = run;
+        __syncthreads();
+        if (warp == 0) {
+            int32_t run = 0;
+            for (int32_t base = 0; base < nseg; base += 32) {
+                const int32_t b = base + lane;
+                const int32_t nt = b < nseg ? (segs[b].rows + segs[b].ts - 1) / segs[b].ts : 0;
+                int32_t v = nt;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int32_t t = __shfl_up_sync(0xffffffffu, v, o);
+                    if (lane >= o) v += t;
+                }
+                if (b < nseg) segs[b].prefix = run + v - nt;
+                run += __shfl_sync(0xffffffffu, v, 31);
+            }
+            if (lane == 0) s_token_tiles = run;
+        }
     }
+    // A single CTA's producer needs nothing of the others for a dense call: it
+    // starts at once (the other roles would hold the first loads up by a
+    // microsecond).  The CTAs of a cluster meet before their first exchange, a
+    // pair before its first load.
+    const bool ahead = CG == 1 && dense && warp == 0;
     tc_fence_before();
-    if (csize > 1) cluster_sync();   // the barriers of the other CTAs are ready too
-    __syncthreads();
+    if (csize > 1) cluster_arrive();
+    if (CG == 1 && dense) {
+        if (warp == 0) bar_arrive(1, THREADS);
+        else bar_sync(1, THREADS);
+    } else {
+        __syncthreads();
+    }
+    if (CG == 2) cluster_wait();
+    if (CG == 1 && csize > 1 && warp >= 2) cluster_wait();
     tc_fence_after();
 
-    const uint32_t tmem_base = s_tmem_base;
-    const int32_t total = s_token_tiles * g.nblk;
+    const uint32_t tmem_base = ahead ? 0u : s_tmem_base;
+    const int32_t total = (dense ? g.dense_tiles : s_token_tiles) * g.nblk;
     volatile int* abort_flag = &s_abort;
     const bool bf16 = p.w_dt == SGMV_BF16;
     constexpr int32_t WT = WROWS * CG;
@@ -535,6 +618,11 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
     const bool lora_here = CG == 2 || crank == 0;   // of CTAs that share a tile, the first adds the low-rank part
     const int32_t t_ranks = lo.parts == 2 ? 32 : 16;
     Tile t;
+    if (LORA == LORA_MMA && warp >= 2) {
+        constexpr int WARPS = EPI_WARPS + LORA_WARPS;
+        build_runs<WARPS>(g, lo, runs, first_run, reinterpret_cast<Run*>(first_run + g.dense_tiles + 1), warp - 2, lane);
+        if (warp == 2 && lane == 0) mbar_arrive(smem_u32(runs_ready));
+    }
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -586,10 +674,10 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                     }
                 }
                 if (LORA == LORA_MMA && ok && lora_here) {
-                    if (g.early) grid_dependency_wait();   // the runs
-                    const int32_t nruns = lo.runs[t.row0].count;
-                    for (int32_t r = 0; ok && r < nruns; ++r) {
-                        const int32_t a = lo.runs[t.row0 + r].adapter;
+                    ok = mbar_wait(smem_u32(runs_ready), 0, abort_flag, DEVERR_TIMEOUT_PRODUCER);
+                    const int32_t last = ok ? first_run[t.tok + 1] : 0;
+                    for (int32_t r = ok ? first_run[t.tok] : 0; ok && r < last; ++r) {
+                        const int32_t a = runs[r].adapter;
                         for (int32_t r0 = 0; r0 < lo.R; r0 += t_ranks) {
                             if (!mbar_wait(smem_u32(&empty[s]), phase, abort_flag, DEVERR_TIMEOUT_PRODUCER)) {
                                 ok = false;
@@ -623,53 +711,45 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
         __syncwarp();
     } else if (LORA == LORA_MMA && warp >= LORA_WARP) {
         // ------------------------------------------------------------ t, ahead of the MMAs by up to two low-rank steps
+        // Each warp writes every second step, into its own buffer.
         if (g.early) grid_dependency_wait();
-        const int first = (warp - LORA_WARP) * 32 + lane;
-        const auto settle = [&](LoraStep& x) {   // to the next step that exists, from a place that may hold none
-            while (x.id < total && (x.r < 0 || x.r >= x.nruns)) {
-                if (x.r >= 0) x.id += ncl;
-                if (x.id >= total) break;
-                decode_tile(segs, nseg, g, x.id, WT, x.t);
-                x.nruns = lo.runs[x.t.row0].count;
-                x.r = 0;
-                x.r0 = 0;
-            }
-            if (x.id < total) x.run = lo.runs[x.t.row0 + x.r];
-        };
-        const auto request = [&](TRows& v, const LoraStep& x) {
-            const int32_t hs = x.t.ts / CG;
-            load_t(v, x.t.row0 + (CG == 2 ? (int32_t)crank * hs : 0), hs, x.run, x.r0, min(t_ranks, lo.R - x.r0), lo, first);
-        };
-        LoraStep step = {lora_here ? cid : total, -1, 0, 0, {}, {}};
-        TRows v;
-        uint32_t m = 0;
+        const uint32_t buf = (uint32_t)(warp - LORA_WARP);
+        uint8_t* dst = smem + g.off_t + buf * g.t_bytes;
+        uint32_t m = 0, mine = 0;
         bool ok = true;
-        settle(step);
-        if (step.id < total) request(v, step);
-        for (; step.id < total; ++m) {
-            const uint32_t buf = m & 1;
-            if (!warp_wait(smem_u32(&t_empty[buf]), ((m >> 1) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_CONVERT)) {
-                ok = false;
-                break;
-            }
-            store_t(smem + g.off_t + buf * g.t_bytes, v, step.t.ts / CG, min(t_ranks, lo.R - step.r0), lo.parts, first, bf16);
-            step.r0 += t_ranks;
-            if (step.r0 >= lo.R) {
-                step.r0 = 0;
-                ++step.r;
-            }
-            settle(step);
-            if (step.id < total) request(v, step);
-            asm volatile("fence.proxy.async;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-                if (CG == 2 && crank != 0) mbar_arrive_cluster(map_to_rank(smem_u32(&t_full[buf]), 0));
-                else mbar_arrive(smem_u32(&t_full[buf]));
+        for (int32_t id = cid; ok && lora_here && id < total; id += ncl) {
+            decode_tile(segs, nseg, g, id, WT, t);
+            const int32_t last = first_run[t.tok + 1];
+            for (int32_t r = first_run[t.tok]; ok && r < last; ++r) {
+                const Run run = runs[r];
+                int32_t off, cols;
+                run_columns<CG>(run, t.ts, off, cols);
+                // the rows of t that this CTA's columns are: all of a single CTA's, a half of a pair's
+                const int32_t base = CG == 2 ? (int32_t)crank * (t.ts / 2) : off, rows = CG == 2 ? t.ts / 2 : cols;
+                for (int32_t r0 = 0; ok && r0 < lo.R; r0 += t_ranks, ++m) {
+                    if ((m & 1) != buf) continue;
+                    const int ranks = min(t_ranks, lo.R - r0);
+                    TRows v;
+                    load_t(v, (int64_t)t.row0 + base, 0, run.begin - base, run.end - base, r0, ranks, lo, lane);
+                    ok = warp_wait(smem_u32(&t_empty[buf]), (mine & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_CONVERT);
+                    if (!ok) break;
+                    ++mine;
+                    store_t(dst, v, 0, rows, ranks, lo.parts, lane, bf16);
+                    if (rows > 64) {
+                        load_t(v, (int64_t)t.row0 + base, 64, run.begin - base, run.end - base, r0, ranks, lo, lane);
+                        store_t(dst, v, 64, rows, ranks, lo.parts, lane, bf16);
+                    }
+                    asm volatile("fence.proxy.async;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (CG == 2 && crank != 0) mbar_arrive_cluster(map_to_rank(smem_u32(&t_full[buf]), 0));
+                        else mbar_arrive(smem_u32(&t_full[buf]));
+                    }
+                }
             }
         }
         // the commits of the other CTA's MMAs free the buffers: none may be under way when this CTA ends
-        for (int i = 0; CG == 2 && ok && i < 2; ++i, ++m)
-            ok = warp_wait(smem_u32(&t_empty[m & 1]), ((m >> 1) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_CONVERT);
+        if (CG == 2 && ok) warp_wait(smem_u32(&t_empty[buf]), (mine & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_CONVERT);
     } else if (LORA == LORA_FMA && warp == B_WARP) {
         // ------------------------------------------------------------ B and t of the tokens that this CTA finishes
         if (g.early) grid_dependency_wait();
@@ -755,11 +835,13 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                     }
                 }
                 if (LORA == LORA_MMA && ok && lora_here) {
-                    if (g.early) grid_dependency_wait();
-                    const int32_t nruns = lo.runs[t.row0].count;
-                    const uint32_t idesc_t = instr_desc_mn(bf16, WT, t.ts);
+                    ok = mbar_wait(smem_u32(runs_ready), 0, abort_flag, DEVERR_TIMEOUT_MMA);
                     const uint64_t bk0 = smem_desc(smem_u32(smem), 16, 1024, 2);   // B's rows are K-major
-                    for (int32_t r = 0; ok && r < nruns; ++r) {
+                    const int32_t last = ok ? first_run[t.tok + 1] : 0;
+                    for (int32_t r = ok ? first_run[t.tok] : 0; ok && r < last; ++r) {
+                        int32_t off, cols;
+                        run_columns<CG>(runs[r], t.ts, off, cols);
+                        const uint32_t idesc_t = instr_desc_mn(bf16, WT, cols), dt = d + (uint32_t)off;
                         for (int32_t r0 = 0; r0 < lo.R; r0 += t_ranks) {
                             if (!mbar_wait(smem_u32(&full[s]), phase, abort_flag, DEVERR_TIMEOUT_MMA)) {
                                 ok = false;
@@ -778,8 +860,8 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                             for (int part = 0; part < lo.parts; ++part)
                                 for (int kk = 0; kk < steps; ++kk) {
                                     const uint64_t td = bd + (uint64_t)((part * t_ranks) / 8 + kk * 2);
-                                    if (CG == 2) tc_mma_pair(d, ad + kk * 2, td, idesc_t, 1u);
-                                    else tc_mma(d, ad + kk * 2, td, idesc_t, 1u);
+                                    if (CG == 2) tc_mma_pair(dt, ad + kk * 2, td, idesc_t, 1u);
+                                    else tc_mma(dt, ad + kk * 2, td, idesc_t, 1u);
                                 }
                             if (CG == 2) {
                                 tc_commit_pair(smem_u32(&empty[s]));
@@ -929,6 +1011,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
         }
     }
 
+    if (CG == 1 && csize > 1 && warp < 2) cluster_wait();   // the meeting at the start
     tc_fence_before();
     __syncthreads();
     if (csize > 1) cluster_sync();   // no CTA leaves while another may still signal it
@@ -994,8 +1077,9 @@ struct Want {
     int lora;        // LoraMode
     int R;
     int b_tma;       // LORA_FMA: TMA can read B
+    int segs;        // LORA_MMA: the call's segments
     int sm_count;
-    int clusters[4]; // clusters of 1, 2, 4, 8 CTAs that fit on the device at a time
+    int clusters[MAX_SPLITS]; // clusters of 1, 2, .. 8 CTAs that fit on the device at a time
     int forced_cg;   // 0: the cost model chooses
 };
 
@@ -1040,7 +1124,7 @@ inline Shape choose_shape(const Problem& p, const Want& w) {
     const int64_t mean = segs > 0 ? (rows + segs - 1) / segs : 1;
     const int64_t kblocks = (p.K + BK - 1) / BK;
     const double experts = w.dense ? 1 : (double)(segs < p.lora_num ? segs : p.lora_num);
-    const double memory = experts * (double)p.N * p.K * 2.0 / 3500.0;
+    const double bytes = experts * (double)p.N * p.K * 2.0;
     Shape best{1, 32, 1};
     double best_cost = -1;
     const int tns[2][5] = {{32, 48, 64, 96, 128}, {64, 96, 128, 192, 256}};
@@ -1051,13 +1135,14 @@ inline Shape choose_shape(const Problem& p, const Want& w) {
             const int64_t nt = (mean + tn - 1) / tn;
             const int64_t ts = ((mean + nt - 1) / nt + 16 * cg - 1) / (16 * cg) * (16 * cg);
             const int64_t tiles = segs * nt * ((p.N + WROWS * cg - 1) / (WROWS * cg));
-            for (int lg = 0, sp = 1; sp <= (cg == 1 ? MAX_SPLITS : 1); sp *= 2, ++lg) {
+            for (int sp = 1; sp <= (cg == 1 ? MAX_SPLITS : 1); ++sp) {
                 if (sp > 1 && kblocks < 4 * sp) break;
                 const Shape sh{cg, tn, sp};
                 const Extra e = extra_of(sh, w);
                 const int stages = (SMEM_LIMIT - 4096 - e.total()) / stage_bytes(sh);
                 if (stages < 2) continue;
-                const int64_t workers = w.clusters[cg == 2 ? 1 : lg] > 0 ? w.clusters[cg == 2 ? 1 : lg] : 1;
+                const int64_t workers = w.clusters[cg == 2 ? 1 : sp - 1];
+                if (workers < 1) continue;
                 const int64_t waves = (tiles + workers - 1) / workers;
                 const double kb = (double)((kblocks + sp - 1) / sp);
                 const double own = (double)((ts + sp - 1) / sp);   // tokens a CTA finishes
@@ -1068,8 +1153,16 @@ inline Shape choose_shape(const Problem& p, const Want& w) {
                 double body = load > mma ? load : mma;
                 if (body < alu) body = alu;
                 if (body < late) body = late;
+                // LORA_MMA: a step per run of a segment and 32 ranks, its t written by one warp of two
+                const double runs = (double)ts * w.segs / (rows > 0 ? rows : 1) + 1.0;
+                const double steps = w.lora == LORA_MMA ? runs * ((w.R + 31) / 32) * (cg == 2 ? 1500.0 : 700.0) : 0.0;
+                if (body < steps) body = steps;
                 const double exchange = sp > 1 ? 1200.0 + 16.0 * ts : 0.0;
                 const double path = waves * (body + exchange + 600.0) + 16.0 * own;
+                // memory: 3500 bytes a cycle, or the weights' stages under way over a latency of 2800 cycles
+                const double active = (double)(tiles < workers ? tiles : workers) * sp * cg;
+                const double under_way = active * stages * W_TILE / 2800.0;
+                const double memory = bytes / (under_way < 3500.0 ? under_way : 3500.0);
                 const double cost = (path > memory ? path : memory) + 0.1 * path;
                 if (best_cost < 0 || cost < best_cost * 0.97) {
                     best_cost = cost;
@@ -1108,6 +1201,11 @@ inline bool make_plan(const Problem& p, const Want& w, EncodeTiledFn enc, Plan* 
     g.b_ranks = e.b_ranks;
     g.b_slots = e.b_slots;
     g.b_bytes = e.b_ranks * WROWS * 2;
+    const int step = 16 * sh.cg, nt = dense ? (int)((rows + sh.tn - 1) / sh.tn) : 0;
+    g.dense_ts = nt > 0 ? (int)(((rows + nt - 1) / nt + step - 1) / step * step) : step;
+    g.dense_tiles = dense ? (int)((rows + g.dense_ts - 1) / g.dense_ts) : 0;
+    g.max_runs = w.lora == LORA_MMA ? w.segs + g.dense_tiles : 0;   // segments that do not overlap fit
+    const int table = w.lora == LORA_MMA ? (g.max_runs + w.segs) * (int)sizeof(Run) + (g.dense_tiles + 1) * 4 : 0;
     for (g.stages = 12; g.stages >= 2; --g.stages) {
         g.off_t = g.stages * g.stage_bytes;                       // t or B (1024-byte aligned: swizzled)
         g.off_tr = g.off_t + 2 * e.t + 2 * e.b_slots * g.b_bytes;
@@ -1115,8 +1213,9 @@ inline bool make_plan(const Problem& p, const Want& w, EncodeTiledFn enc, Plan* 
         g.off_delta = g.off_out + e.out;
         g.off_red = g.off_delta + e.delta;
         g.off_seg = g.off_red + e.red;
-        g.off_bar = (g.off_seg + (int)segs * (int)sizeof(Seg) + 15) & ~15;
-        out->smem_bytes = g.off_bar + 8 * (2 * g.stages + 10 + 4 * B_SLOTS) + 1024;
+        g.off_runs = (g.off_seg + (dense ? 0 : (int)segs * (int)sizeof(Seg)) + 15) & ~15;
+        g.off_bar = (g.off_runs + table + 15) & ~15;
+        out->smem_bytes = g.off_bar + 8 * (2 * g.stages + 11 + 4 * B_SLOTS) + 1024;
         if (out->smem_bytes <= SMEM_LIMIT) break;
     }
     if (g.stages < 2) return false;
@@ -1145,7 +1244,7 @@ inline bool make_plan(const Problem& p, const Want& w, EncodeTiledFn enc, Plan* 
     const int64_t most_segs = segs < rows ? segs : rows;
     const int64_t tiles = (rows / sh.tn + most_segs + 1) * g.nblk;
     const int csize = sh.cg == 2 ? 2 : sh.splits;
-    int64_t clusters = w.clusters[csize == 1 ? 0 : csize == 2 ? 1 : csize == 4 ? 2 : 3];
+    int64_t clusters = w.clusters[csize - 1];
     if (tiles < clusters) clusters = tiles;
     out->grid = (int)(clusters < 1 ? 1 : clusters) * csize;
     return true;
@@ -1157,39 +1256,43 @@ struct PlanKey {
     int32_t device;
 };
 
-// Clusters of 1, 2, 4 and 8 CTAs (one per SM) that the current device holds at
-// a time: a GPC whose SM count the size does not divide leaves some idle.
-inline bool cluster_capacity(int device, int sm_count, int (&out)[4]) {
+// Clusters of 1 to 8 CTAs (one per SM) that the current device holds at a time:
+// a GPC whose SM count the size does not divide leaves some idle.  0: unknown.
+inline bool cluster_capacity(int device, int sm_count, int (&out)[MAX_SPLITS]) {
     static std::mutex mu;
-    static int known[64][4];
+    static int known[64][MAX_SPLITS];
     std::lock_guard<std::mutex> lk(mu);
     if (device < 0 || device >= 64) return false;
     if (!known[device][0]) {
         auto kern = gemm_kernel<1, LORA_NONE>;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT) != cudaSuccess) return false;
-        int got[4] = {sm_count, sm_count / 2, 0, 0};
-        for (int lg = 1; lg < 4; ++lg) {
+        int got[MAX_SPLITS] = {sm_count};
+        for (int size = 2; size <= MAX_SPLITS; ++size) {
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = 1u << lg;
+            attr[0].val.clusterDim.x = (unsigned)size;
             attr[0].val.clusterDim.y = 1;
             attr[0].val.clusterDim.z = 1;
             cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3((unsigned)(sm_count >> lg << lg));
+            cfg.gridDim = dim3((unsigned)(sm_count / size * size));
             cfg.blockDim = dim3(threads_of(LORA_NONE));
             cfg.dynamicSmemBytes = SMEM_LIMIT;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
-            if (cudaOccupancyMaxActiveClusters(&got[lg], kern, &cfg) != cudaSuccess || got[lg] < 1) return false;
+            if (cudaOccupancyMaxActiveClusters(&got[size - 1], kern, &cfg) != cudaSuccess) {
+                (void)cudaGetLastError();
+                got[size - 1] = 0;
+            }
         }
-        for (int lg = 0; lg < 4; ++lg) known[device][lg] = got[lg];
+        if (got[1] < 1) return false;
+        for (int i = 0; i < MAX_SPLITS; ++i) known[device][i] = got[i];
     }
-    for (int lg = 0; lg < 4; ++lg) out[lg] = known[device][lg];
+    for (int i = 0; i < MAX_SPLITS; ++i) out[i] = known[device][i];
     return true;
 }
 
 // Plans of recent calls, keyed by every field of the problem, the wishes and the device.
-inline bool cached_plan(const Problem& p, bool dense, bool early, int lora, int R, bool b_tma, int sm_count, int forced_cg,
+inline bool cached_plan(const Problem& p, bool dense, bool early, int lora, int R, bool b_tma, int segs, int sm_count, int forced_cg,
                         EncodeTiledFn enc, Plan* out) {
     static PlanCache<PlanKey, Plan> cache;
     PlanKey key;
@@ -1200,6 +1303,7 @@ inline bool cached_plan(const Problem& p, bool dense, bool early, int lora, int 
     key.w.lora = lora;
     key.w.R = R;
     key.w.b_tma = b_tma;
+    key.w.segs = segs;
     key.w.sm_count = sm_count;
     key.w.forced_cg = forced_cg;
     if (cudaGetDevice(&key.device) != cudaSuccess || !cluster_capacity(key.device, sm_count, key.w.clusters)) return false;
@@ -1232,12 +1336,6 @@ int launch_kernel(const Plan& pl, const CUtensorMap& bm, const Problem& p, const
 template <int LORA>
 int launch(const Plan& pl, const CUtensorMap& bm, const Problem& p, const Lora& lo, cudaStream_t stream) {
     return pl.cg == 2 ? launch_kernel<2, LORA>(pl, bm, p, lo, stream) : launch_kernel<1, LORA>(pl, bm, p, lo, stream);
-}
-
-// Rows of the token tiles that the kernel cuts `rows` dense rows into.
-inline int32_t dense_tile_rows(const Geo& g, int cg) {
-    const int32_t rows = g.dense_rows, nt = (rows + g.tn - 1) / g.tn, step = 16 * cg;
-    return nt > 0 ? ((rows + nt - 1) / nt + step - 1) / step * step : step;
 }
 
 // Tensor map of lora_b (adapters, N, R) with boxes of `ranks` x 128 rows, rows

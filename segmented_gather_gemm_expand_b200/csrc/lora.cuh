@@ -22,22 +22,15 @@ __device__ __forceinline__ int32_t block_adapter(const Problem& p, int64_t row, 
     return *s_adapter;
 }
 
-// The adapter of every row, and for the tensor-core form the runs of rows that
-// share one in each token tile of tile_rows (at most 256) rows.  One block per
-// tile, one thread per row: it scans the segments, which the block stages in
-// shared memory 256 at a time; a run starts where the adapter changes.
+// The adapter of every row: one thread per row scans the segments, which the
+// block stages in shared memory 256 at a time.
 constexpr int ROWS_THREADS = 256;
-__global__ void __launch_bounds__(ROWS_THREADS)
-row_runs_kernel(Problem p, int32_t* row_adapter, grp::Run* runs, int32_t tile_rows, int64_t rows) {
+__global__ void __launch_bounds__(ROWS_THREADS) row_adapter_kernel(Problem p, int32_t* row_adapter, int64_t rows) {
     __shared__ Segment s_seg[ROWS_THREADS];
-    __shared__ int32_t s_a[ROWS_THREADS + 1];
-    __shared__ int32_t s_warp[ROWS_THREADS / 32];
-    __shared__ unsigned s_change[ROWS_THREADS / 32];
     tc::grid_dependency_wait();
     tc::grid_dependents_launch();
     const int tid = threadIdx.x;
-    const int64_t row0 = (int64_t)blockIdx.x * tile_rows, row = row0 + tid;
-    const bool mine = tid < tile_rows && row < rows;
+    const int64_t row = (int64_t)blockIdx.x * ROWS_THREADS + tid;
     int32_t a = -1;
     for (int64_t base = 0; base < p.batches; base += ROWS_THREADS) {
         __syncthreads();
@@ -47,33 +40,7 @@ row_runs_kernel(Problem p, int32_t* row_adapter, grp::Run* runs, int32_t tile_ro
         for (int i = 0; i < n; ++i)
             if (row >= s_seg[i].row0 && row < s_seg[i].row0 + s_seg[i].rows) a = (int32_t)s_seg[i].adapter;
     }
-    if (!mine) a = -1;
-    if (mine) row_adapter[row] = a;
-    if (!runs) return;
-    s_a[tid + 1] = a;
-    if (tid == 0) s_a[0] = -1;
-    __syncthreads();
-    const bool changes = s_a[tid] != a, begins = a >= 0 && changes;
-    const unsigned mask = __ballot_sync(0xffffffffu, begins), change = __ballot_sync(0xffffffffu, changes);
-    if (tid % 32 == 0) {
-        s_warp[tid / 32] = __popc(mask);
-        s_change[tid / 32] = change;
-    }
-    __syncthreads();
-    int32_t at = __popc(mask & ((1u << (tid % 32)) - 1)), total = 0;
-    for (int w = 0; w < ROWS_THREADS / 32; ++w) {
-        if (w < tid / 32) at += s_warp[w];
-        total += s_warp[w];
-    }
-    if (begins) {
-        // the run ends at the next change: in this warp, or the first one of a later warp
-        unsigned after = change & ~((2u << (tid % 32)) - 1);
-        int w = tid / 32;
-        while (!after && ++w < ROWS_THREADS / 32) after = s_change[w];
-        const int32_t end = after ? w * 32 + __ffs(after) - 1 : ROWS_THREADS;
-        runs[row0 + at] = grp::Run{a, (int32_t)row, (int32_t)(row0 + end), total};
-    }
-    if (tid == 0 && total == 0) runs[row0] = grp::Run{-1, 0, 0, 0};
+    if (row < rows) row_adapter[row] = a;
 }
 
 // t[row, j] = sum_k x^[row, k] * A[a][j, k] in fp32 for four ranks per block;
@@ -225,12 +192,9 @@ int launch_dependent(void (*kern)(KArgs...), dim3 grid, int threads, cudaStream_
     return cudaLaunchKernelEx(&cfg, kern, KArgs(args)...) == cudaSuccess ? SGMV_OK : SGMV_ERR_LAUNCH;
 }
 
-// runs: null where only the rows' adapters are wanted.
-inline int launch_row_runs(const Problem& p, int32_t* row_adapter, grp::Run* runs, int32_t tile_rows, int64_t rows,
-                           cudaStream_t stream) {
-    const int64_t blocks = (rows + tile_rows - 1) / tile_rows;
-    return launch_dependent(row_runs_kernel, dim3((unsigned)blocks), ROWS_THREADS, stream, p, row_adapter, runs, tile_rows,
-                            rows);
+inline int launch_row_adapter(const Problem& p, int32_t* row_adapter, int64_t rows, cudaStream_t stream) {
+    const int64_t blocks = (rows + ROWS_THREADS - 1) / ROWS_THREADS;
+    return launch_dependent(row_adapter_kernel, dim3((unsigned)blocks), ROWS_THREADS, stream, p, row_adapter, rows);
 }
 
 inline int launch_row_shrink(const Problem& p, float* t, int32_t* row_adapter, int64_t rows, cudaStream_t stream) {

@@ -543,7 +543,7 @@ int validate_grouped(const sgmv_tensor* x, const sgmv_tensor* w, const sgmv_tens
 
 int choose_grouped(const Call& c, const DeviceInfo& dev, int forced, grp::Plan* pl) {
     const bool tc_ok = forced != SGMV_VARIANT_SIMT && dev.cc_major == 10 &&
-                       grp::cached_plan(c.p, false, false, grp::LORA_NONE, 0, false, dev.sm_count, forced_cg(forced), tc::encode_fn(), pl);
+                       grp::cached_plan(c.p, false, false, grp::LORA_NONE, 0, false, 0, dev.sm_count, forced_cg(forced), tc::encode_fn(), pl);
     return large_variant(tc_ok, forced);
 }
 
@@ -609,7 +609,7 @@ struct LoraCall {
     int64_t rows;
     bool low_rank;            // there is a low-rank part to compute
     bool empty;
-    int64_t off_runs, off_t, off_part;  // workspace: row adapters, runs, t, partial sums of t
+    int64_t off_t, off_part;  // workspace: row adapters, t, partial sums of t
 };
 
 int validate_lora(const sgmv_tensor* x, const sgmv_tensor* w, const sgmv_tensor* bias, const sgmv_tensor* a,
@@ -673,8 +673,7 @@ int validate_lora(const sgmv_tensor* x, const sgmv_tensor* w, const sgmv_tensor*
         lo.bias = bias->data;
         lo.bias_s = bias->stride[0];
     }
-    call->off_runs = align256(call->rows * 4);
-    call->off_t = call->off_runs + align256(call->rows * (int64_t)sizeof(grp::Run));
+    call->off_t = align256(call->rows * 4);
     call->off_part = call->off_t + align256(call->rows * R * 4);
     return SGMV_OK;
 }
@@ -704,15 +703,20 @@ int choose_lora(LoraCall* c, const DeviceInfo& dev, int forced, char* ws, size_t
     const bool b_tma = tc && c->low_rank &&
                        grp::encode_b(c->lo, long_runs ? 64 : grp::b_box_ranks(c->lo.R), c->base.N, c->shrink.lora_num,
                                      tc::encode_fn(), &pl->bm);
-    const bool mma = b_tma && long_runs;
+    const bool mma = b_tma && long_runs && c->shrink.batches <= grp::SEG_CAP;
     pl->lora = !c->low_rank ? grp::LORA_NONE : mma ? grp::LORA_MMA : grp::LORA_FMA;
-    const bool tc_ok = tc && grp::cached_plan(c->base, true, c->low_rank, pl->lora, c->lo.R, b_tma, dev.sm_count,
+    const bool tc_ok = tc && grp::cached_plan(c->base, true, c->low_rank, pl->lora, c->lo.R, b_tma,
+                                              (int)c->shrink.batches, dev.sm_count,
                                               forced_cg(forced), tc::encode_fn(), &pl->base);
     pl->variant = large_variant(tc_ok, forced);
     if (pl->variant < 0) return pl->variant;
     pl->mma = mma && tc_ok;
     if (pl->mma) {
-        c->lo.runs = reinterpret_cast<const grp::Run*>(ws + c->off_runs);
+        c->lo.start = c->shrink.start;
+        c->lo.len = c->shrink.len;
+        c->lo.idx = c->shrink.idx;
+        c->lo.batches = (int32_t)c->shrink.batches;
+        c->lo.adapters = c->shrink.lora_num;
         c->lo.parts = c->base.out_dt == SGMV_F32 ? 3 : 2;
     }
     pl->shrink = c->low_rank ? LoraPlan::BY_ROW : LoraPlan::NONE;
@@ -724,7 +728,7 @@ int choose_lora(LoraCall* c, const DeviceInfo& dev, int forced, char* ws, size_t
             const size_t room = ws_bytes > (size_t)c->off_part ? ws_bytes - (size_t)c->off_part : 0;
             while (sp > 1 && (size_t)shr::workspace_bytes_for(c->shrink, sp) > room) sp /= 2;
             pl->splits = sp;
-        } else if (grp::cached_plan(c->shrink, false, false, grp::LORA_NONE, 0, false, dev.sm_count, 0, tc::encode_fn(),
+        } else if (grp::cached_plan(c->shrink, false, false, grp::LORA_NONE, 0, false, 0, dev.sm_count, 0, tc::encode_fn(),
                                     &pl->product)) {
             pl->shrink = LoraPlan::PRODUCT;
         }
@@ -737,12 +741,9 @@ int run_lora(const LoraCall& c, const DeviceInfo& dev, const LoraPlan& pl, char*
     int32_t* rows = reinterpret_cast<int32_t*>(ws);
     float* t = reinterpret_cast<float*>(ws + c.off_t);
     const Call shrink{c.shrink, 0, false};
-    // row_shrink_kernel finds the rows' adapters by itself
-    if (pl.shrink != LoraPlan::NONE && (pl.mma || pl.shrink != LoraPlan::BY_ROW)) {
-        grp::Run* runs = pl.mma ? reinterpret_cast<grp::Run*>(ws + c.off_runs) : nullptr;
-        const int32_t tile = pl.mma ? grp::dense_tile_rows(pl.base.geo, pl.base.cg) : lora::ROWS_THREADS;
-        if ((rc = lora::launch_row_runs(c.shrink, rows, runs, tile, c.rows, st))) return rc;
-    }
+    // row_shrink_kernel finds the rows' adapters by itself, the projection's K steps read the segments
+    if (!pl.mma && (pl.shrink == LoraPlan::BLOCKS || pl.shrink == LoraPlan::PRODUCT))
+        if ((rc = lora::launch_row_adapter(c.shrink, rows, c.rows, st))) return rc;
     switch (pl.shrink) {
         case LoraPlan::BY_ROW: rc = lora::launch_row_shrink(c.shrink, t, rows, c.rows, st); break;
         case LoraPlan::BLOCKS:
