@@ -69,9 +69,10 @@ constexpr int B_WARP = 2 + EPI_WARPS;      // loads B for LORA_FMA
 constexpr int threads_of(int lora) {
     return 64 + 32 * EPI_WARPS + (lora == LORA_MMA ? 32 * LORA_WARPS : lora == LORA_FMA ? 32 : 0);
 }
-constexpr int B_RING = 24 * 1024;          // LORA_FMA: buffered rows of B for each half of the epilogue's warps
+constexpr int B_RING = 16 * 1024;          // LORA_FMA: buffered rows of B for each half of the epilogue's warps
 constexpr int B_SLOTS = 8;                 // at most
-constexpr int T_ROW = 64 * 4;              // a slot's ranks of t, fp32
+constexpr int RING_MAX_RANK = 64;
+constexpr int T_ROW = RING_MAX_RANK * 4;   // a slot's row of t, fp32
 constexpr int NUM_XMAPS = 4;            // x boxes of 16, 32, 64, 128 rows
 constexpr int MAX_SPLITS = 8;
 constexpr int BAND = 8;                 // token tiles walked together before the next weight tile
@@ -89,7 +90,7 @@ struct Geo {
     int32_t tn;           // most tokens per tile
     int32_t splits;       // CTAs that share a tile by cutting K (single form)
     int32_t stages, stage_bytes;
-    int32_t b_ranks, b_slots, b_bytes;   // LORA_FMA: ranks per buffer (8 to 64; 0: B is not loaded by TMA), buffers per half
+    int32_t b_slots, b_bytes;   // LORA_FMA: a ring of tokens' B and t per half of the epilogue (0 slots: read directly), bytes of B in a slot
     int32_t off_t, t_bytes, off_tr, off_out, off_delta, off_red, off_seg, off_bar;
     int32_t out_vec;      // half output in 16-byte pieces
     int32_t turn_bytes;   // shared memory in which an epilogue warp turns its halves round
@@ -267,27 +268,35 @@ __device__ __forceinline__ void lora_delta(float (&d)[8], int64_t row, int valid
                             half_bits_to_float(__ldg(b + (int64_t)a[j] * lo.b_as + r0 * lo.b_ks), bf16), d[j]);
 }
 
-// One token's low-rank sum over a buffered piece of B (the lane's row of 128,
-// `ranks` (8 to 64) halves each, swizzled by TMA so that 8 lanes' 16-byte reads
-// touch every bank once): d += sum_k t[k] * B[k].
-__device__ __forceinline__ float lora_dot(const uint8_t* piece, int row, int width, int ranks, const float* t, bool bf16) {
-    const int bytes = width * 2;
-    const uint8_t* r = piece + row * bytes;
-    const int turn = bytes == 128 ? row & 7 : bytes == 64 ? (row >> 1) & 3 : bytes == 32 ? (row >> 2) & 1 : 0;
+// One token's low-rank sum over its buffered rows of B: row `row` of 128, R
+// halves each, back to back.  Eight lanes read 16 bytes each at a time; rows of
+// an even number of such pieces would meet in the same banks, so every lane
+// starts at a piece of its own (`turn`, from lora_turn) and goes round.
+__device__ __forceinline__ int lora_turn(int row, int R) {
+    const int pieces = R / 8, g = pieces & 1 ? 1 : pieces & 2 ? 2 : pieces & 4 ? 4 : 8;   // gcd(pieces, 8)
+    return (row * g / 8) % g;
+}
+
+__device__ __forceinline__ float lora_dot(const uint8_t* rows, int row, int R, int turn, const float* t, bool bf16) {
+    const uint4* b = reinterpret_cast<const uint4*>(rows + row * R * 2);
+    const float4* t4 = reinterpret_cast<const float4*>(t);
+    const int pieces = R / 8;
     float d0 = 0.f, d1 = 0.f;
+    int k = turn;
 #pragma unroll 2
-    for (int k = 0; k < ranks; k += 8) {
-        const float4 x = *reinterpret_cast<const float4*>(t + k), y = *reinterpret_cast<const float4*>(t + k + 4);
-        const uint4 u = *reinterpret_cast<const uint4*>(r + (((k >> 3) ^ turn) << 4));
-        const float2 a = unpack2(u.x, bf16), b = unpack2(u.y, bf16), c = unpack2(u.z, bf16), e = unpack2(u.w, bf16);
+    for (int i = 0; i < pieces; ++i) {
+        const float4 x = t4[2 * k], y = t4[2 * k + 1];
+        const uint4 u = b[k];
+        const float2 a = unpack2(u.x, bf16), c = unpack2(u.y, bf16), e = unpack2(u.z, bf16), f = unpack2(u.w, bf16);
         d0 = fmaf(x.x, a.x, d0);
         d1 = fmaf(x.y, a.y, d1);
-        d0 = fmaf(x.z, b.x, d0);
-        d1 = fmaf(x.w, b.y, d1);
-        d0 = fmaf(y.x, c.x, d0);
-        d1 = fmaf(y.y, c.y, d1);
-        d0 = fmaf(y.z, e.x, d0);
-        d1 = fmaf(y.w, e.y, d1);
+        d0 = fmaf(x.z, c.x, d0);
+        d1 = fmaf(x.w, c.y, d1);
+        d0 = fmaf(y.x, e.x, d0);
+        d1 = fmaf(y.y, e.y, d1);
+        d0 = fmaf(y.z, f.x, d0);
+        d1 = fmaf(y.w, f.y, d1);
+        if (++k == pieces) k = 0;
     }
     return d0 + d1;
 }
@@ -552,7 +561,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
     } else if (warp == 2 && lane == 0) {
         prefetch_tmap(&wmap);
         for (int k = 0; k < NUM_XMAPS; ++k) prefetch_tmap(&xmaps.m[k]);
-        if (LORA != LORA_NONE) prefetch_tmap(&bmap);
+        if (LORA == LORA_MMA) prefetch_tmap(&bmap);
     }
 
     // Everything below may read memory written by the preceding kernel, unless
@@ -753,7 +762,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
     } else if (LORA == LORA_FMA && warp == B_WARP) {
         // ------------------------------------------------------------ B and t of the tokens that this CTA finishes
         if (g.early) grid_dependency_wait();
-        if (g.b_ranks > 0) {
+        if (g.b_slots > 0) {
             const uint64_t pol = policy_evict_first();
             const bool one = elect_one();
             uint32_t slot[2] = {0, 0}, phase[2] = {1, 1};
@@ -774,24 +783,26 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                         const int32_t a = __shfl_sync(0xffffffffu, h ? mine[1] : mine[0], i >> 1);
                         if (a < 0) continue;
                         const int64_t row = (int64_t)t.row0 + t0 + half_token(h, i0 + (i >> 1), csize > 1);
-                        for (int r0 = 0; ok && r0 < lo.R; r0 += g.b_ranks) {
-                            const uint32_t sl = h ? slot[1] : slot[0], ph = h ? phase[1] : phase[0];
-                            const uint32_t bar = smem_u32(&b_full[h * B_SLOTS + sl]), q = (uint32_t)(h * g.b_slots) + sl;
-                            ok = warp_wait(smem_u32(&b_empty[h * B_SLOTS + sl]), ph, abort_flag, DEVERR_TIMEOUT_PRODUCER);
-                            if (ok && one) {
-                                const uint32_t tb = (uint32_t)min(g.b_ranks, lo.R - r0) * 4u;
-                                mbar_expect_tx(bar, (uint32_t)g.b_bytes + tb);
-                                tma_load_3d(smem_u32(smem + g.off_t) + q * g.b_bytes, &bmap, r0, t.n0, a, bar, pol);
-                                bulk_load(smem_u32(smem + g.off_tr) + q * T_ROW, lo.t + row * lo.R + r0, tb, bar, pol);
-                            }
-                            const bool wrap = sl + 1 == (uint32_t)g.b_slots;
-                            if (h) {
-                                slot[1] = wrap ? 0 : sl + 1;
-                                phase[1] ^= wrap;
-                            } else {
-                                slot[0] = wrap ? 0 : sl + 1;
-                                phase[0] ^= wrap;
-                            }
+                        const uint32_t sl = h ? slot[1] : slot[0], ph = h ? phase[1] : phase[0];
+                        const uint32_t bar = smem_u32(&b_full[h * B_SLOTS + sl]), q = (uint32_t)(h * g.b_slots) + sl;
+                        ok = warp_wait(smem_u32(&b_empty[h * B_SLOTS + sl]), ph, abort_flag, DEVERR_TIMEOUT_PRODUCER);
+                        if (ok && one) {
+                            // B's rows are contiguous (lora_b.b_ns == R): one copy of 128 rows, fewer at N's end
+                            const uint32_t bytes = (uint32_t)min((int64_t)WROWS, p.N - t.n0) * (uint32_t)lo.R * 2u;
+                            const uint32_t tb = (uint32_t)lo.R * 4u;
+                            mbar_expect_tx(bar, bytes + tb);
+                            bulk_load(smem_u32(smem + g.off_t) + q * g.b_bytes,
+                                      static_cast<const uint16_t*>(lo.b) + (int64_t)a * lo.b_as + (int64_t)t.n0 * lo.R, bytes,
+                                      bar, pol);
+                            bulk_load(smem_u32(smem + g.off_tr) + q * T_ROW, lo.t + row * lo.R, tb, bar, pol);
+                        }
+                        const bool wrap = sl + 1 == (uint32_t)g.b_slots;
+                        if (h) {
+                            slot[1] = wrap ? 0 : sl + 1;
+                            phase[1] ^= wrap;
+                        } else {
+                            slot[0] = wrap ? 0 : sl + 1;
+                            phase[0] ^= wrap;
                         }
                     }
                 }
@@ -893,6 +904,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
         const int nl = quad * 32 + lane;
         uint32_t* stage = reinterpret_cast<uint32_t*>(smem + g.off_out + (warp - 2) * g.turn_bytes);
         uint32_t b_slot = 0, b_phase = 0;
+        const int turn = LORA == LORA_FMA ? lora_turn(nl, lo.R) : 0;
         uint32_t n = 0, reds = 0;   // reds: exchanges in which this CTA owned tokens
         for (int32_t id = cid; id < total; id += ncl, ++n) {
             decode_tile(segs, nseg, g, id, WT, t);
@@ -906,7 +918,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
             float* delta = reinterpret_cast<float*>(smem + g.off_delta) + nl;           // [token][weight row]
             if (LORA == LORA_FMA) {
                 // while the K loop runs: the low-rank part of the tokens that this warp will store
-                if (g.b_ranks > 0) {
+                if (g.b_slots > 0) {
                     bool ok = true;
                     for (int i0 = 0; ok && half_token(half, i0, csize > 1) < cnt; i0 += 32) {
                         const int mine = half_token(half, i0 + lane, csize > 1);
@@ -916,12 +928,12 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                             const int tok = half_token(half, i0 + i, csize > 1);
                             if (tok >= cnt) break;
                             float d = 0.f;
-                            for (int r0 = 0; ok && ((on >> i) & 1) && r0 < lo.R; r0 += g.b_ranks) {
+                            if ((on >> i) & 1) {
                                 const uint32_t at = (uint32_t)half * B_SLOTS + b_slot, q = (uint32_t)(half * g.b_slots) + b_slot;
                                 ok = warp_wait(smem_u32(&b_full[at]), b_phase, abort_flag, DEVERR_TIMEOUT_EPILOGUE);
                                 if (!ok) break;
-                                d += lora_dot(smem + g.off_t + q * g.b_bytes, nl, g.b_ranks, min(g.b_ranks, lo.R - r0),
-                                              reinterpret_cast<const float*>(smem + g.off_tr + q * T_ROW), bf16);
+                                d = lora_dot(smem + g.off_t + q * g.b_bytes, nl, lo.R, turn,
+                                             reinterpret_cast<const float*>(smem + g.off_tr + q * T_ROW), bf16);
                                 __syncwarp();
                                 if (lane == 0) mbar_arrive(smem_u32(&b_empty[at]));
                                 if (++b_slot == (uint32_t)g.b_slots) {
@@ -1065,9 +1077,6 @@ struct Shape {
     int cg, tn, splits;
 };
 
-// Ranks that one TMA box of B holds for LORA_FMA: the rank padded to a power of two, at most 64.
-inline int b_box_ranks(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 64; }
-
 constexpr int turn_bytes(int splits) { return splits > 1 ? 8 * 64 : 32 * 64; }   // 8 or 32 tokens x 32 halves per warp
 
 // What a plan is made for, besides the problem.
@@ -1076,7 +1085,7 @@ struct Want {
     bool early;
     int lora;        // LoraMode
     int R;
-    int b_tma;       // LORA_FMA: TMA can read B
+    int ring;        // LORA_FMA: B's rows can be copied into a ring
     int segs;        // LORA_MMA: the call's segments
     int sm_count;
     int clusters[MAX_SPLITS]; // clusters of 1, 2, .. 8 CTAs that fit on the device at a time
@@ -1088,18 +1097,18 @@ inline int x_box_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : row
 
 // Shared memory of a form besides the stages and the segment table.
 struct Extra {
-    int t, b_ranks, b_slots, out, delta, red;
-    int total() const { return 2 * t + 2 * b_slots * (b_ranks * WROWS * 2 + T_ROW) + out + delta + red; }
+    int t, b_bytes, b_slots, out, delta, red;
+    int total() const { return 2 * t + 2 * b_slots * (b_bytes + T_ROW) + out + delta + red; }
 };
 
 inline Extra extra_of(const Shape& sh, const Want& w) {
     Extra e;
     const int own = ((sh.tn + sh.splits - 1) / sh.splits + 3) & ~3;   // tokens a CTA finishes
     e.t = w.lora == LORA_MMA ? x_box_rows(sh.tn / sh.cg < 64 ? 64 : sh.tn / sh.cg) * 128 : 0;
-    e.b_ranks = w.lora == LORA_FMA && w.b_tma ? b_box_ranks(w.R) : 0;
+    e.b_bytes = w.lora == LORA_FMA && w.ring ? w.R * WROWS * 2 : 0;
     e.b_slots = 0;
-    if (e.b_ranks) {
-        e.b_slots = B_RING / (e.b_ranks * WROWS * 2);
+    if (e.b_bytes) {
+        e.b_slots = B_RING / e.b_bytes;
         e.b_slots = e.b_slots > B_SLOTS ? B_SLOTS : e.b_slots < 2 ? 2 : e.b_slots;
     }
     e.out = EPI_WARPS * turn_bytes(sh.splits);
@@ -1135,7 +1144,7 @@ inline Shape choose_shape(const Problem& p, const Want& w) {
             const int64_t nt = (mean + tn - 1) / tn;
             const int64_t ts = ((mean + nt - 1) / nt + 16 * cg - 1) / (16 * cg) * (16 * cg);
             const int64_t tiles = segs * nt * ((p.N + WROWS * cg - 1) / (WROWS * cg));
-            for (int sp = 1; sp <= (cg == 1 ? MAX_SPLITS : 1); ++sp) {
+            for (int sp = 1; sp <= (cg == 1 ? MAX_SPLITS : 1); sp *= 2) {   // clusters of 3 measured slower than both 2 and 4
                 if (sp > 1 && kblocks < 4 * sp) break;
                 const Shape sh{cg, tn, sp};
                 const Extra e = extra_of(sh, w);
@@ -1146,9 +1155,9 @@ inline Shape choose_shape(const Problem& p, const Want& w) {
                 const int64_t waves = (tiles + workers - 1) / workers;
                 const double kb = (double)((kblocks + sp - 1) / sp);
                 const double own = (double)((ts + sp - 1) / sp);   // tokens a CTA finishes
-                const double load = (kb * (W_TILE + x_box_rows((int)(ts / cg)) * 128.0) + own * e.b_ranks * WROWS * 2.0) / 64.0;
+                const double load = (kb * (W_TILE + x_box_rows((int)(ts / cg)) * 128.0) + own * e.b_bytes) / 64.0;
                 const double mma = kb * 2.0 * ts;
-                const double alu = w.lora != LORA_FMA ? 0.0 : own * w.R * (w.b_tma ? 4.0 : 30.0) + 1000.0;
+                const double alu = w.lora != LORA_FMA ? 0.0 : own * w.R * (w.ring ? 4.0 : 30.0) + 1000.0;
                 const double late = kb * 1500.0 / stages;
                 double body = load > mma ? load : mma;
                 if (body < alu) body = alu;
@@ -1157,7 +1166,7 @@ inline Shape choose_shape(const Problem& p, const Want& w) {
                 const double runs = (double)ts * w.segs / (rows > 0 ? rows : 1) + 1.0;
                 const double steps = w.lora == LORA_MMA ? runs * ((w.R + 31) / 32) * (cg == 2 ? 1500.0 : 700.0) : 0.0;
                 if (body < steps) body = steps;
-                const double exchange = sp > 1 ? 1200.0 + 16.0 * ts : 0.0;
+                const double exchange = sp > 1 ? 3000.0 + 32.0 * ts : 0.0;
                 const double path = waves * (body + exchange + 600.0) + 16.0 * own;
                 // memory: 3500 bytes a cycle, or the weights' stages under way over a latency of 2800 cycles
                 const double active = (double)(tiles < workers ? tiles : workers) * sp * cg;
@@ -1198,9 +1207,8 @@ inline bool make_plan(const Problem& p, const Want& w, EncodeTiledFn enc, Plan* 
     g.turn_bytes = turn_bytes(sh.splits);
     const Extra e = extra_of(sh, w);
     g.t_bytes = e.t;
-    g.b_ranks = e.b_ranks;
     g.b_slots = e.b_slots;
-    g.b_bytes = e.b_ranks * WROWS * 2;
+    g.b_bytes = e.b_bytes;
     const int step = 16 * sh.cg, nt = dense ? (int)((rows + sh.tn - 1) / sh.tn) : 0;
     g.dense_ts = nt > 0 ? (int)(((rows + nt - 1) / nt + step - 1) / step * step) : step;
     g.dense_tiles = dense ? (int)((rows + g.dense_ts - 1) / g.dense_ts) : 0;
@@ -1292,7 +1300,7 @@ inline bool cluster_capacity(int device, int sm_count, int (&out)[MAX_SPLITS]) {
 }
 
 // Plans of recent calls, keyed by every field of the problem, the wishes and the device.
-inline bool cached_plan(const Problem& p, bool dense, bool early, int lora, int R, bool b_tma, int segs, int sm_count, int forced_cg,
+inline bool cached_plan(const Problem& p, bool dense, bool early, int lora, int R, bool ring, int segs, int sm_count, int forced_cg,
                         EncodeTiledFn enc, Plan* out) {
     static PlanCache<PlanKey, Plan> cache;
     PlanKey key;
@@ -1302,7 +1310,7 @@ inline bool cached_plan(const Problem& p, bool dense, bool early, int lora, int 
     key.w.early = early;
     key.w.lora = lora;
     key.w.R = R;
-    key.w.b_tma = b_tma;
+    key.w.ring = ring;
     key.w.segs = segs;
     key.w.sm_count = sm_count;
     key.w.forced_cg = forced_cg;
@@ -1338,22 +1346,20 @@ int launch(const Plan& pl, const CUtensorMap& bm, const Problem& p, const Lora& 
     return pl.cg == 2 ? launch_kernel<2, LORA>(pl, bm, p, lo, stream) : launch_kernel<1, LORA>(pl, bm, p, lo, stream);
 }
 
-// Tensor map of lora_b (adapters, N, R) with boxes of `ranks` x 128 rows, rows
-// swizzled by their width; false where TMA cannot read it.
-inline bool encode_b(const Lora& lo, int ranks, int64_t N, int64_t adapters, EncodeTiledFn enc, CUtensorMap* out) {
+// LORA_FMA: a token's 128 rows of B and its row of t are copies of whole 16-byte pieces.
+inline bool ring_ok(const Lora& lo) { return lo.b_vec && lo.R % 8 == 0 && lo.R <= RING_MAX_RANK && lo.b_ns == lo.R; }
+
+// Tensor map of lora_b (adapters, N, R) for LORA_MMA; false where TMA cannot read it.
+inline bool encode_b(const Lora& lo, int64_t N, int64_t adapters, EncodeTiledFn enc, CUtensorMap* out) {
     if (!enc || !lo.b_vec || lo.R % 8 || lo.b_ns < lo.R || adapters >= (int64_t(1) << 31)) return false;
     if (lo.b_ns >= (int64_t(1) << 38) || lo.b_as >= (int64_t(1) << 38)) return false;
     if (adapters > 1 && lo.b_as < (N - 1) * lo.b_ns + lo.R) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)lo.R, (cuuint64_t)N, (cuuint64_t)adapters};
     const cuuint64_t strides[2] = {(cuuint64_t)(lo.b_ns * 2),
                                    (cuuint64_t)(adapters > 1 ? lo.b_as * 2 : (N * lo.b_ns * 2 + 15) / 16 * 16)};
-    const cuuint32_t box[3] = {(cuuint32_t)ranks, WROWS, 1}, ones[3] = {1, 1, 1};
-    const CUtensorMapSwizzle sw = ranks == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
-                                  : ranks == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                  : ranks == 16 ? CU_TENSOR_MAP_SWIZZLE_32B
-                                                : CU_TENSOR_MAP_SWIZZLE_NONE;
+    const cuuint32_t box[3] = {64, WROWS, 1}, ones[3] = {1, 1, 1};
     return enc(out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(lo.b), dims, strides, box, ones,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

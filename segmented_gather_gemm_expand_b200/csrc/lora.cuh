@@ -12,6 +12,11 @@ namespace lora {
 
 // Adapter of `row` (-1: none), found by the whole block; segments do not overlap.
 __device__ __forceinline__ int32_t block_adapter(const Problem& p, int64_t row, int32_t* s_adapter) {
+    // a decode batch has one token per segment, in order: look there first
+    if (row < p.batches) {
+        const Segment s = load_segment(p, row);
+        if (s.rows > 0 && row >= s.row0 && row < s.row0 + s.rows) return (int32_t)s.adapter;
+    }
     if (threadIdx.x == 0) *s_adapter = -1;
     __syncthreads();
     for (int64_t b = threadIdx.x; b < p.batches; b += blockDim.x) {

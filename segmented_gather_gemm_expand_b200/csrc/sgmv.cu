@@ -700,12 +700,10 @@ int choose_lora(LoraCall* c, const DeviceInfo& dev, int forced, char* ws, size_t
     const bool tc = forced != SGMV_VARIANT_SIMT && dev.cc_major == 10;
     // K steps pay from a few rows per segment on: a run costs an MMA over its whole token tile
     const bool long_runs = c->rows >= kMmaRunRows * c->shrink.batches;
-    const bool b_tma = tc && c->low_rank &&
-                       grp::encode_b(c->lo, long_runs ? 64 : grp::b_box_ranks(c->lo.R), c->base.N, c->shrink.lora_num,
-                                     tc::encode_fn(), &pl->bm);
-    const bool mma = b_tma && long_runs && c->shrink.batches <= grp::SEG_CAP;
+    const bool mma = tc && c->low_rank && long_runs && c->shrink.batches <= grp::SEG_CAP &&
+                     grp::encode_b(c->lo, c->base.N, c->shrink.lora_num, tc::encode_fn(), &pl->bm);
     pl->lora = !c->low_rank ? grp::LORA_NONE : mma ? grp::LORA_MMA : grp::LORA_FMA;
-    const bool tc_ok = tc && grp::cached_plan(c->base, true, c->low_rank, pl->lora, c->lo.R, b_tma,
+    const bool tc_ok = tc && grp::cached_plan(c->base, true, c->low_rank, pl->lora, c->lo.R, grp::ring_ok(c->lo),
                                               (int)c->shrink.batches, dev.sm_count,
                                               forced_cg(forced), tc::encode_fn(), &pl->base);
     pl->variant = large_variant(tc_ok, forced);
