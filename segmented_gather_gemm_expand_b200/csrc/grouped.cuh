@@ -69,7 +69,7 @@ constexpr int B_WARP = 2 + EPI_WARPS;      // loads B for LORA_FMA
 constexpr int threads_of(int lora) {
     return 64 + 32 * EPI_WARPS + (lora == LORA_MMA ? 32 * LORA_WARPS : lora == LORA_FMA ? 32 : 0);
 }
-constexpr int B_RING = 16 * 1024;          // LORA_FMA: buffered rows of B for each half of the epilogue's warps
+constexpr int B_RING = 32 * 1024;          // LORA_FMA: buffered rows of B for each half of the epilogue's warps
 constexpr int B_SLOTS = 8;                 // at most
 constexpr int RING_MAX_RANK = 64;
 constexpr int T_ROW = RING_MAX_RANK * 4;   // a slot's row of t, fp32
@@ -91,7 +91,7 @@ struct Geo {
     int32_t splits;       // CTAs that share a tile by cutting K (single form)
     int32_t stages, stage_bytes;
     int32_t b_slots, b_bytes;   // LORA_FMA: a ring of tokens' B and t per half of the epilogue (0 slots: read directly), bytes of B in a slot
-    int32_t off_t, t_bytes, off_tr, off_out, off_delta, off_red, off_seg, off_bar;
+    int32_t off_t, t_bytes, off_tr, off_out, off_red, off_seg, off_bar;
     int32_t out_vec;      // half output in 16-byte pieces
     int32_t turn_bytes;   // shared memory in which an epilogue warp turns its halves round
     int32_t acc_stride, tmem_cols;
@@ -301,11 +301,9 @@ __device__ __forceinline__ float lora_dot(const uint8_t* rows, int row, int R, i
     return d0 + d1;
 }
 
-// The i-th token that a half of the epilogue's warps finishes: 32 of every 64
-// (a shared tile: 8 of every 16).
-__device__ __forceinline__ int half_token(int half, int i, bool shared) {
-    return shared ? (i >> 3) * 16 + half * 8 + (i & 7) : (i >> 5) * 64 + half * 32 + (i & 31);
-}
+// LORA_FMA and shared tiles: the i-th token that a half of the epilogue's warps
+// finishes, 8 of every 16.
+__device__ __forceinline__ int half_token(int half, int i) { return (i >> 3) * 16 + half * 8 + (i & 7); }
 
 // Adds the old output (add mode), rounds once and stores rows row .. row +
 // valid - 1 of column n (= the warp's first column + lane).
@@ -316,7 +314,7 @@ __device__ __forceinline__ int half_token(int half, int i, bool shared) {
 // (`stage`) and stores 8 rows at a time, 16 bytes per lane: 32 tokens as pairs
 // (one packed conversion and one 4-byte store per pair and column, split again
 // after the read), 8 tokens as halves.  That needs 16-byte aligned output rows
-// and 32 columns inside the matrix; other warps store element by element.
+// of whole 16-byte pieces; other outputs are stored element by element.
 template <int NT>
 __device__ __forceinline__ void put(float (&v)[NT], int64_t row, int valid, int64_t n, const Problem& p, uint32_t* stage,
                                     bool out_vec) {
@@ -340,8 +338,9 @@ __device__ __forceinline__ void put(float (&v)[NT], int64_t row, int valid, int6
     }
     const bool ob = p.out_dt == SGMV_BF16;
     const int lane = threadIdx.x % 32;
-    if (out_vec && n - lane + 32 <= p.N) {
+    if (out_vec) {
         const int r = lane / 4, c = (lane % 4) * 8;
+        if (n - lane + c >= p.N) valid = 0;   // this lane's 8 columns are past the end (N: a multiple of 8)
         uint16_t* o = static_cast<uint16_t*>(p.out) + (base - lane + c);
         uint16_t* halves = reinterpret_cast<uint16_t*>(stage);   // [token][32 columns]
         if (p.add) {
@@ -351,8 +350,7 @@ __device__ __forceinline__ void put(float (&v)[NT], int64_t row, int valid, int6
                     *reinterpret_cast<uint4*>(halves + (j + r) * 32 + c) = *reinterpret_cast<const uint4*>(o + (j + r) * p.H);
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-                if (j < valid) v[j] += half_bits_to_float(halves[j * 32 + lane], ob);
+            for (int j = 0; j < NT; ++j) v[j] += half_bits_to_float(halves[j * 32 + lane], ob);   // rows past `valid` are not stored
             __syncwarp();
         }
         if (NT == 32) {
@@ -401,12 +399,10 @@ __device__ __forceinline__ void put(float (&v)[NT], int64_t row, int valid, int6
 
 // A warp's share of a tile in TMEM: columns (tokens) c0, c0 + 64, ... in pieces
 // of 32, the next piece under way while one is stored.  `drained` runs once
-// the last piece is in registers; delta (or null): what to add per token, in
-// the lane's column of a [token][128] array.
+// the last piece is in registers.
 template <class Drained>
 __device__ __forceinline__ void drain(uint32_t taddr, int c0, int ts, int64_t row0, int rows, int64_t n, float bias,
-                                      const float* delta, const Problem& p, uint32_t* stage, bool out_vec,
-                                      Drained&& drained) {
+                                      const Problem& p, uint32_t* stage, bool out_vec, Drained&& drained) {
     uint32_t next[32];
     float v[32];
     if (c0 >= ts) {
@@ -421,11 +417,6 @@ __device__ __forceinline__ void drain(uint32_t taddr, int c0, int ts, int64_t ro
         const bool more = c + 64 < ts;
         if (more) tmem_ld32(taddr + (uint32_t)c + 64, next);
         else drained();
-        if (delta) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (c + j < rows) v[j] += delta[(c + j) * WROWS];
-        }
         put<32>(v, row0 + c, min(32, rows - c), n, p, stage, out_vec);
         if (!more) break;
     }
@@ -498,8 +489,20 @@ __device__ __forceinline__ void run_columns(const Run& run, int32_t ts, int32_t&
     cols = CG == 2 ? ts : min(ts, (run.end + 15) & ~15) - off;
 }
 
+// The next box of x (16 << level rows) for `rows` more rows, a positive multiple of
+// 16: the smallest that holds them all if the stage has `room` for it (every
+// further box costs the producer time: 1230 us instead of 1176 for the experts'
+// prefill with exact boxes), else the largest within them.
+__device__ __forceinline__ int x_box(int rows, int room) {
+    const int up = rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3;
+    if ((16 << up) <= room) return up;
+    return rows >= 128 ? 3 : rows >= 64 ? 2 : rows >= 32 ? 1 : 0;
+}
+
+// LORA_FMA is held to 128 registers a thread (as for 512 threads): a CTA of the
+// shrink before it then fits beside it, and the weights stream while the shrink runs.
 template <int CG, int LORA>
-__global__ void __launch_bounds__(threads_of(LORA), 1)
+__global__ void __launch_bounds__(LORA == LORA_FMA ? 512 : threads_of(LORA), 1)
 gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtensorMap wmap,
             const __grid_constant__ CUtensorMap bmap, const Problem p, const Geo g, const Lora lo) {
     constexpr int THREADS = threads_of(LORA);
@@ -643,8 +646,12 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
             for (int32_t id = cid; ok && id < total; id += ncl) {
                 decode_tile(segs, nseg, g, id, WT, t);
                 const int32_t hs = t.ts / CG;   // token rows of this CTA
-                const int lvl = hs <= 16 ? 0 : hs <= 32 ? 1 : hs <= 64 ? 2 : 3;
-                const uint32_t bytes = W_TILE + (16u << lvl) * 128u;
+                const int room = g.tn / CG;
+                int x_rows = 0;                 // rows that the boxes bring
+                while (x_rows < hs) x_rows += 16 << x_box(hs - x_rows, room - x_rows);
+                const uint32_t bytes = W_TILE + (uint32_t)x_rows * 128u;
+                const int lvl0 = x_box(hs, room), rows0 = 16 << lvl0;   // the first box, nearly always the only one
+                const CUtensorMap* x0 = &xmaps.m[lvl0];
                 const int32_t xr = t.row0 + (CG == 2 ? (int32_t)crank * hs : 0);
                 const int32_t n0 = t.n0 + (CG == 2 ? (int32_t)crank * WROWS : 0);
                 for (int32_t kb = kb0; kb < kb1; ++kb) {
@@ -665,7 +672,12 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                         } else {
                             tma_load_3d_pair(ws, &wmap, kb * BK, n0, t.group, bar, pol_w);
                         }
-                        tma_load_2d_pair(xs, &xmaps.m[lvl], kb * BK, xr, bar, pol_x);
+                        tma_load_2d_pair(xs, x0, kb * BK, xr, bar, pol_x);
+                        for (int r = rows0; r < hs;) {
+                            const int lvl = x_box(hs - r, room - r);
+                            tma_load_2d_pair(xs + r * 128, &xmaps.m[lvl], kb * BK, xr + r, bar, pol_x);
+                            r += 16 << lvl;
+                        }
                     } else {
                         const uint32_t bar = smem_u32(&full[s]);
                         mbar_expect_tx(bar, bytes);
@@ -675,7 +687,12 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                         } else {
                             tma_load_3d(ws, &wmap, kb * BK, n0, t.group, bar, pol_w);
                         }
-                        tma_load_2d(xs, &xmaps.m[lvl], kb * BK, xr, bar, pol_x);
+                        tma_load_2d(xs, x0, kb * BK, xr, bar, pol_x);
+                        for (int r = rows0; r < hs;) {
+                            const int lvl = x_box(hs - r, room - r);
+                            tma_load_2d(xs + r * 128, &xmaps.m[lvl], kb * BK, xr + r, bar, pol_x);
+                            r += 16 << lvl;
+                        }
                     }
                     if (++s == S) {
                         s = 0;
@@ -771,18 +788,18 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                 decode_tile(segs, nseg, g, id, WT, t);
                 const int tw = csize > 1 ? ((t.ts + (int)csize - 1) / (int)csize + 3) & ~3 : t.ts;
                 const int t0 = (int)crank * tw, cnt = min(tw, t.rows - t0);
-                for (int i0 = 0; ok && half_token(0, i0, csize > 1) < cnt; i0 += 32) {
+                for (int i0 = 0; ok && half_token(0, i0) < cnt; i0 += 32) {
                     int32_t mine[2];   // adapters of 32 tokens of each half, one per lane
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int tok = half_token(h, i0 + lane, csize > 1);
+                        const int tok = half_token(h, i0 + lane);
                         mine[h] = tok < cnt ? lo.row_adapter[t.row0 + t0 + tok] : -1;
                     }
                     for (int i = 0; ok && i < 64; ++i) {
                         const int h = i & 1;
                         const int32_t a = __shfl_sync(0xffffffffu, h ? mine[1] : mine[0], i >> 1);
                         if (a < 0) continue;
-                        const int64_t row = (int64_t)t.row0 + t0 + half_token(h, i0 + (i >> 1), csize > 1);
+                        const int64_t row = (int64_t)t.row0 + t0 + half_token(h, i0 + (i >> 1));
                         const uint32_t sl = h ? slot[1] : slot[0], ph = h ? phase[1] : phase[0];
                         const uint32_t bar = smem_u32(&b_full[h * B_SLOTS + sl]), q = (uint32_t)(h * g.b_slots) + sl;
                         ok = warp_wait(smem_u32(&b_empty[h * B_SLOTS + sl]), ph, abort_flag, DEVERR_TIMEOUT_PRODUCER);
@@ -915,17 +932,18 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
             if (lo.bias && n_ok) bias = half_bits_to_float(static_cast<const uint16_t*>(lo.bias)[col * lo.bias_s], bf16);
             const int tw = csize > 1 && CG == 1 ? ((t.ts + (int)csize - 1) / (int)csize + 3) & ~3 : t.ts;
             const int t0 = CG == 1 ? (int)crank * tw : 0, cnt = min(tw, t.rows - t0);   // tokens this CTA finishes
-            float* delta = reinterpret_cast<float*>(smem + g.off_delta) + nl;           // [token][weight row]
+            const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+            const uint32_t delta = tmem_base + 2 * (uint32_t)g.acc_stride + lanes;   // LORA_FMA: a TMEM column per token
             if (LORA == LORA_FMA) {
                 // while the K loop runs: the low-rank part of the tokens that this warp will store
                 if (g.b_slots > 0) {
                     bool ok = true;
-                    for (int i0 = 0; ok && half_token(half, i0, csize > 1) < cnt; i0 += 32) {
-                        const int mine = half_token(half, i0 + lane, csize > 1);
+                    for (int i0 = 0; ok && half_token(half, i0) < cnt; i0 += 32) {
+                        const int mine = half_token(half, i0 + lane);
                         const unsigned on = __ballot_sync(
                             0xffffffffu, mine < cnt && lo.row_adapter[(int64_t)t.row0 + t0 + min(mine, cnt - 1)] >= 0);
                         for (int i = 0; ok && i < 32; ++i) {
-                            const int tok = half_token(half, i0 + i, csize > 1);
+                            const int tok = half_token(half, i0 + i);
                             if (tok >= cnt) break;
                             float d = 0.f;
                             if ((on >> i) & 1) {
@@ -941,27 +959,41 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                                     b_phase ^= 1;
                                 }
                             }
-                            delta[tok * WROWS] = d;
+                            tmem_st1(delta + (uint32_t)tok, __float_as_uint(d));
                         }
                     }
                     if (!ok) break;
                 } else {
-                    for (int i = 0; half_token(half, i, csize > 1) < cnt; i += 8) {
-                        const int j0 = half_token(half, i, csize > 1);
+                    for (int i = 0; half_token(half, i) < cnt; i += 8) {
+                        const int j0 = half_token(half, i);
                         float d[8];
                         lora_delta(d, (int64_t)t.row0 + t0 + j0, cnt - j0, col, n_ok, lo, bf16);
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            if (j0 + j < tw) delta[(j0 + j) * WROWS] = d[j];
+                            tmem_st1(delta + (uint32_t)(j0 + j), __float_as_uint(d[j]));
                     }
                 }
+                tmem_st_wait();
             }
             if (!warp_wait(smem_u32(&acc_full[acc]), (n >> 1) & 1, abort_flag, DEVERR_TIMEOUT_EPILOGUE)) break;
             tc_fence_after();
-            const uint32_t taddr = tmem_base + acc * (uint32_t)g.acc_stride + ((uint32_t)(quad * 32) << 16);
-            if (CG == 2 || csize == 1) {
-                drain(taddr, half * 32, t.ts, t.row0, t.rows, col, bias, LORA == LORA_FMA ? delta : nullptr, p, stage,
-                      g.out_vec, [&] {
+            const uint32_t taddr = tmem_base + acc * (uint32_t)g.acc_stride + lanes;
+            if (LORA == LORA_FMA && csize == 1) {
+                for (int j0 = half * 8; j0 < cnt; j0 += 16) {
+                    uint32_t a[8], b[8];
+                    tmem_ld8(taddr + (uint32_t)j0, a);
+                    tmem_ld8(delta + (uint32_t)j0, b);
+                    tmem_ld_wait(a, b);
+                    float v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(a[j]) + __uint_as_float(b[j]) + bias;
+                    put<8>(v, (int64_t)t.row0 + j0, min(8, cnt - j0), col, p, stage, g.out_vec);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && id + 2 * ncl < total) mbar_arrive(smem_u32(&acc_empty[acc]));
+            } else if (CG == 2 || csize == 1) {
+                drain(taddr, half * 32, t.ts, t.row0, t.rows, col, bias, p, stage, g.out_vec, [&] {
                           tc_fence_before();
                           __syncwarp();
                           if (lane == 0 && id + 2 * ncl < total) {   // somebody waits for it
@@ -1002,8 +1034,14 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                     for (int j0 = half * 8; j0 < cnt; j0 += 16) {
                         float v[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            v[j] = LORA == LORA_FMA ? bias + delta[min(j0 + j, tw - 1) * WROWS] : bias;
+                        for (int j = 0; j < 8; ++j) v[j] = bias;
+                        if (LORA == LORA_FMA) {
+                            uint32_t b[8];
+                            tmem_ld8(delta + (uint32_t)j0, b);
+                            tmem_ld_wait(b);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) v[j] += __uint_as_float(b[j]);
+                        }
                         for (int src = 0; src < (int)csize; ++src)
 #pragma unroll
                             for (int j = 0; j < 8; j += 4)
@@ -1070,14 +1108,12 @@ inline bool supports(const Problem& p) {
 
 // Half output rows can be written as 16-byte pieces.
 inline bool out_vec_ok(const Problem& p) {
-    return p.out_dt != SGMV_F32 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.H % 8 == 0;
+    return p.out_dt != SGMV_F32 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.H % 8 == 0 && p.N % 8 == 0;
 }
 
 struct Shape {
     int cg, tn, splits;
 };
-
-constexpr int turn_bytes(int splits) { return splits > 1 ? 8 * 64 : 32 * 64; }   // 8 or 32 tokens x 32 halves per warp
 
 // What a plan is made for, besides the problem.
 struct Want {
@@ -1092,32 +1128,31 @@ struct Want {
     int forced_cg;   // 0: the cost model chooses
 };
 
-// Rows of the TMA box of x that holds this many.
-inline int x_box_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+// 8 or 32 tokens x 32 halves per epilogue warp.
+inline int turn_bytes(const Shape& sh, const Want& w) { return sh.splits > 1 || w.lora == LORA_FMA ? 8 * 64 : 32 * 64; }
 
 // Shared memory of a form besides the stages and the segment table.
 struct Extra {
-    int t, b_bytes, b_slots, out, delta, red;
-    int total() const { return 2 * t + 2 * b_slots * (b_bytes + T_ROW) + out + delta + red; }
+    int t, b_bytes, b_slots, out, red;
+    int total() const { return 2 * t + 2 * b_slots * (b_bytes + T_ROW) + out + red; }
 };
 
 inline Extra extra_of(const Shape& sh, const Want& w) {
     Extra e;
     const int own = ((sh.tn + sh.splits - 1) / sh.splits + 3) & ~3;   // tokens a CTA finishes
-    e.t = w.lora == LORA_MMA ? x_box_rows(sh.tn / sh.cg < 64 ? 64 : sh.tn / sh.cg) * 128 : 0;
+    e.t = w.lora == LORA_MMA ? (sh.tn / sh.cg < 64 ? 64 : sh.tn / sh.cg) * 128 : 0;
     e.b_bytes = w.lora == LORA_FMA && w.ring ? w.R * WROWS * 2 : 0;
     e.b_slots = 0;
     if (e.b_bytes) {
         e.b_slots = B_RING / e.b_bytes;
         e.b_slots = e.b_slots > B_SLOTS ? B_SLOTS : e.b_slots < 2 ? 2 : e.b_slots;
     }
-    e.out = EPI_WARPS * turn_bytes(sh.splits);
-    e.delta = w.lora == LORA_FMA ? own * WROWS * 4 : 0;
+    e.out = EPI_WARPS * turn_bytes(sh, w);
     e.red = sh.splits > 1 ? sh.splits * own * WROWS * 4 : 0;
     return e;
 }
 
-inline int stage_bytes(const Shape& sh) { return W_TILE + x_box_rows(sh.tn / sh.cg) * 128; }
+inline int stage_bytes(const Shape& sh) { return W_TILE + sh.tn / sh.cg * 128; }
 
 // The form with the least estimated time, in SM cycles.  A tile takes the
 // longest of: its loads at 64 bytes a cycle (weights, x, and B for LORA_FMA),
@@ -1155,7 +1190,7 @@ inline Shape choose_shape(const Problem& p, const Want& w) {
                 const int64_t waves = (tiles + workers - 1) / workers;
                 const double kb = (double)((kblocks + sp - 1) / sp);
                 const double own = (double)((ts + sp - 1) / sp);   // tokens a CTA finishes
-                const double load = (kb * (W_TILE + x_box_rows((int)(ts / cg)) * 128.0) + own * e.b_bytes) / 64.0;
+                const double load = (kb * (W_TILE + ts / cg * 128.0) + own * e.b_bytes) / 64.0;
                 const double mma = kb * 2.0 * ts;
                 const double alu = w.lora != LORA_FMA ? 0.0 : own * w.R * (w.ring ? 4.0 : 30.0) + 1000.0;
                 const double late = kb * 1500.0 / stages;
@@ -1202,9 +1237,9 @@ inline bool make_plan(const Problem& p, const Want& w, EncodeTiledFn enc, Plan* 
     g.keep_w = rows > (int64_t)sh.tn * segs ? 1 : 0;
     g.acc_stride = sh.tn < 32 ? 32 : sh.tn;
     g.tmem_cols = 32;
-    while (g.tmem_cols < 2 * g.acc_stride) g.tmem_cols *= 2;
+    while (g.tmem_cols < 2 * g.acc_stride + (w.lora == LORA_FMA ? (sh.tn + 31) / 32 * 32 : 0)) g.tmem_cols *= 2;
     g.stage_bytes = stage_bytes(sh);
-    g.turn_bytes = turn_bytes(sh.splits);
+    g.turn_bytes = turn_bytes(sh, w);
     const Extra e = extra_of(sh, w);
     g.t_bytes = e.t;
     g.b_slots = e.b_slots;
@@ -1218,8 +1253,7 @@ inline bool make_plan(const Problem& p, const Want& w, EncodeTiledFn enc, Plan* 
         g.off_t = g.stages * g.stage_bytes;                       // t or B (1024-byte aligned: swizzled)
         g.off_tr = g.off_t + 2 * e.t + 2 * e.b_slots * g.b_bytes;
         g.off_out = g.off_tr + 2 * e.b_slots * T_ROW;
-        g.off_delta = g.off_out + e.out;
-        g.off_red = g.off_delta + e.delta;
+        g.off_red = g.off_out + e.out;
         g.off_seg = g.off_red + e.red;
         g.off_runs = (g.off_seg + (dense ? 0 : (int)segs * (int)sizeof(Seg)) + 15) & ~15;
         g.off_bar = (g.off_runs + table + 15) & ~15;

@@ -31,6 +31,7 @@ using grp::EPI_WARPS;
 constexpr int BT = 64;                     // tokens per stage
 constexpr int HALF = 64 * BT * 2;          // one box of 64 columns: 8 KB
 constexpr int STAGE = 4 * HALF;            // two boxes of X, two of dY
+constexpr int TURN = 32 * 64;              // epilogue: a warp's 32 x 32 halves
 constexpr int FIX_WARP = 2 + EPI_WARPS;
 constexpr int THREADS = 32 * (FIX_WARP + 1);
 constexpr int SMEM_LIMIT = grp::SMEM_LIMIT;
@@ -285,7 +286,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     } else {
         // ------------------------------------------------------------ epilogue
         const int quad = warp % 4, half = (warp - 2) / 4;
-        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + g.off_out + (warp - 2) * grp::turn_bytes(1));
+        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + g.off_out + (warp - 2) * TURN);
         uint32_t n = 0;
         for (int32_t id = cid; id < total; id += ncl, ++n) {
             int32_t e, k0, n0;
@@ -304,7 +305,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
             };
             const int64_t row0 = (int64_t)e * g.rows_per_group + n0;
             if (any) {
-                grp::drain(taddr, half * 32, g.ts, row0, valid, col, 0.f, nullptr, p, stage, g.out_vec, drained);
+                grp::drain(taddr, half * 32, g.ts, row0, valid, col, 0.f, p, stage, g.out_vec, drained);
             } else {
                 drained();
                 for (int c = half * 32; c < g.ts && !p.add; c += 64) {
@@ -394,7 +395,7 @@ inline bool make_plan(const Problem& p, int64_t y_cs, int64_t out_gs, int64_t ou
     while (g.tmem_cols < 2 * g.acc_stride) g.tmem_cols *= 2;
     for (g.stages = 7; g.stages >= 2; --g.stages) {
         g.off_out = g.stages * STAGE;
-        g.off_seg = g.off_out + EPI_WARPS * grp::turn_bytes(1);
+        g.off_seg = g.off_out + EPI_WARPS * TURN;
         g.off_exp = g.off_seg + (int)p.batches * (int)sizeof(Seg);
         g.off_bar = (g.off_exp + (int)p.lora_num * (int)sizeof(Exp) + 15) & ~15;
         out->smem_bytes = g.off_bar + 8 * (3 * g.stages + 4) + 1024;
