@@ -31,8 +31,6 @@ weights seen transposed, computes the input gradient), and
 ``sgmv_grouped_wgrad`` is the gradient by the weights.
 """
 import ctypes
-import struct
-import threading
 
 import torch
 
@@ -53,6 +51,7 @@ _DTYPES = {torch.float16: _abi.F16, torch.bfloat16: _abi.BF16, torch.float32: _a
            torch.int32: _abi.I32, torch.int64: _abi.I64}
 
 _lib = _abi.load()
+_binding = _abi.load_binding(_lib)
 
 
 class SgmvError(RuntimeError):
@@ -252,88 +251,34 @@ def plan(inputs, lora_b_weights, output_tensor, b_seq_start_loc, seq_len_tensor,
     return v.value
 
 
-# The large products marshal through one packed buffer per thread: a decode step
-# calls them for every layer, and building ctypes structures field by field
-# costs several times the launch itself (measured per call: 23 us against 8).
-_PACK = struct.Struct("=Qii8q").pack_into
-_PACK_SIZE = ctypes.sizeof(_abi.SgmvTensor)
-_PAD = ((), (0, 0, 0), (0, 0), (0,), ())   # by ndim: zeros that fill shape and stride up to four
-_local = threading.local()
-
-
-def _buffer():
-    buf = getattr(_local, "buf", None)
-    if buf is None:
-        buf = _local.buf = ctypes.create_string_buffer(_PACK_SIZE * 9)
-        base = ctypes.addressof(buf)
-        _local.ptrs = [base + i * _PACK_SIZE for i in range(9)]
-    return buf, _local.ptrs
-
-
-def _pack(tensors, device):
-    """Addresses of the tensors' descriptors (None for None), valid until this thread's next call."""
-    buf, ptrs = _buffer()
-    out = []
-    for i, t in enumerate(tensors):
-        if t is None:
-            out.append(None)
-            continue
-        if t.device != device:
-            raise ValueError("all tensors must be CUDA tensors on the same device")
-        n = t.dim()
-        if t.dtype not in _DTYPES:
-            raise TypeError(f"unsupported dtype {t.dtype}")
-        if not 1 <= n <= 4:
-            raise SgmvError(_abi.STATUS["SGMV_ERR_NDIM"], "tensor argument")
-        _PACK(buf, i * _PACK_SIZE, t.data_ptr(), _DTYPES[t.dtype], n, *t.shape, *_PAD[n], *t.stride(), *_PAD[n])
-        out.append(ptrs[i])
-    return out
-
-
-def _call(name, fn, device, *args):
-    """Calls fn with `device` current; raises SgmvError on a negative status."""
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args)
-    if rc != 0:
-        raise SgmvError(rc, name)
-
-
-def _device_of(output_tensor):
-    if not output_tensor.is_cuda:
-        raise ValueError("all tensors must be CUDA tensors on the same device")
-    return output_tensor.device
-
-
 def sgmv_lora_linear(inputs, weight, lora_a_weights, lora_b_weights, output_tensor, b_seq_start_loc, seq_len_tensor,
                      lora_indices_tensor, batches, max_seq_length, bias=None, workspace=None):
     """``output_tensor[r] = inputs[r] @ weight.T + bias + (inputs[r] @ A.T) @ B.T`` with the adapter (A, B) of row r's
     sequence; rows without one get the projection alone.  Every row is written.  ``workspace``: contiguous CUDA tensor
     of scratch of at least ``lora_linear_plan``'s first size (None only without adapters)."""
-    dev = _device_of(output_tensor)
-    d = _pack((inputs, weight, bias, lora_a_weights, lora_b_weights, output_tensor, b_seq_start_loc, seq_len_tensor,
-               lora_indices_tensor), dev)
-    wp, wb = None, 0
-    if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor on the same device")
-        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call("sgmv_lora_linear", _abi.fast.sgmv_lora_linear, dev, *d, int(batches), int(max_seq_length), wp, wb,
-          torch.cuda.current_stream(dev).cuda_stream)
+    rc = _binding.lora_linear(inputs, weight, bias, lora_a_weights, lora_b_weights, output_tensor, b_seq_start_loc,
+                              seq_len_tensor, lora_indices_tensor, batches, max_seq_length, workspace)
+    if rc != 0:
+        raise SgmvError(rc, "sgmv_lora_linear")
     return output_tensor
 
 
 def lora_linear_plan(inputs, weight, lora_a_weights, lora_b_weights, output_tensor, b_seq_start_loc, seq_len_tensor,
                      lora_indices_tensor, batches, max_seq_length, bias=None):
     """(variant, workspace bytes needed, workspace bytes preferred) of a lora_linear call."""
-    dev = _device_of(output_tensor)
-    d = _pack((inputs, weight, bias, lora_a_weights, lora_b_weights, output_tensor, b_seq_start_loc, seq_len_tensor,
-               lora_indices_tensor), dev)
+    x, w, out, s, l, idx = _args(inputs, weight, output_tensor, b_seq_start_loc, seq_len_tensor, lora_indices_tensor)
+    more = [lora_a_weights, lora_b_weights] + ([] if bias is None else [bias])
+    for t in more:
+        if not t.is_cuda or t.device != output_tensor.device:
+            raise ValueError("all tensors must be CUDA tensors on the same device")
+    a, b, *rest = [_desc(t) for t in more]
     v, need, pref = ctypes.c_int(0), ctypes.c_size_t(0), ctypes.c_size_t(0)
-    _call("sgmv_lora_linear_plan", _abi.fast.sgmv_lora_linear_plan, dev, *d, int(batches), int(max_seq_length),
-          ctypes.byref(v), ctypes.byref(need), ctypes.byref(pref))
+    with torch.cuda.device(output_tensor.device):
+        rc = _lib.sgmv_lora_linear_plan(ctypes.byref(x), ctypes.byref(w), ctypes.byref(rest[0]) if rest else None,
+                                        *[ctypes.byref(t) for t in (a, b, out, s, l, idx)], int(batches),
+                                        int(max_seq_length), ctypes.byref(v), ctypes.byref(need), ctypes.byref(pref))
+    if rc != 0:
+        raise SgmvError(rc, "sgmv_lora_linear_plan")
     return v.value, need.value, pref.value
 
 
@@ -342,44 +287,47 @@ def sgmv_grouped_gemm(inputs, weights, output_tensor, b_seq_start_loc, seq_len_t
     """``output_tensor[r] = inputs[r] @ weights[e].T`` (added to the old values when ``add_inputs``) for the rows of
     every segment with index e; other rows keep their bits.  ``weights`` is (E, N, K) with K or N contiguous: pass
     ``w.transpose(1, 2)`` for the input gradient."""
-    dev = _device_of(output_tensor)
-    d = _pack((inputs, weights, output_tensor, b_seq_start_loc, seq_len_tensor, group_indices_tensor), dev)
-    _call("sgmv_grouped_gemm", _abi.fast.sgmv_grouped_gemm, dev, *d, int(batches), int(max_seq_length),
-          int(bool(add_inputs)), torch.cuda.current_stream(dev).cuda_stream)
+    rc = _binding.grouped_gemm(inputs, weights, output_tensor, b_seq_start_loc, seq_len_tensor, group_indices_tensor,
+                               batches, max_seq_length, add_inputs)
+    if rc != 0:
+        raise SgmvError(rc, "sgmv_grouped_gemm")
     return output_tensor
-
-
-def grouped_gemm_plan(inputs, weights, output_tensor, b_seq_start_loc, seq_len_tensor, group_indices_tensor, batches,
-                      max_seq_length, add_inputs=False) -> int:
-    """Kernel variant a sgmv_grouped_gemm call with these arguments would launch (0 = none)."""
-    dev = _device_of(output_tensor)
-    d = _pack((inputs, weights, output_tensor, b_seq_start_loc, seq_len_tensor, group_indices_tensor), dev)
-    v = ctypes.c_int(0)
-    _call("sgmv_grouped_gemm_plan", _abi.fast.sgmv_grouped_gemm_plan, dev, *d, int(batches), int(max_seq_length),
-          int(bool(add_inputs)), ctypes.byref(v))
-    return v.value
 
 
 def sgmv_grouped_wgrad(grad_output, inputs, grad_weights, b_seq_start_loc, seq_len_tensor, group_indices_tensor,
                        batches, max_seq_length, add_inputs=False):
     """``grad_weights[e] = grad_output[rows of e].T @ inputs[rows of e]`` (added to the old values when
     ``add_inputs``) for every index e; an index without rows gets zeros (keeps its values when ``add_inputs``)."""
-    dev = _device_of(grad_weights)
-    d = _pack((grad_output, inputs, grad_weights, b_seq_start_loc, seq_len_tensor, group_indices_tensor), dev)
-    _call("sgmv_grouped_wgrad", _abi.fast.sgmv_grouped_wgrad, dev, *d, int(batches), int(max_seq_length),
-          int(bool(add_inputs)), torch.cuda.current_stream(dev).cuda_stream)
+    rc = _binding.grouped_wgrad(grad_output, inputs, grad_weights, b_seq_start_loc, seq_len_tensor,
+                                group_indices_tensor, batches, max_seq_length, add_inputs)
+    if rc != 0:
+        raise SgmvError(rc, "sgmv_grouped_wgrad")
     return grad_weights
+
+
+def _grouped_plan(name, tensors, batches, max_seq_length, add_inputs):
+    d = _args(*tensors)
+    v = ctypes.c_int(0)
+    with torch.cuda.device(tensors[2].device):
+        rc = getattr(_lib, name)(*[ctypes.byref(x) for x in d], int(batches), int(max_seq_length),
+                                 int(bool(add_inputs)), ctypes.byref(v))
+    if rc != 0:
+        raise SgmvError(rc, name)
+    return v.value
+
+
+def grouped_gemm_plan(inputs, weights, output_tensor, b_seq_start_loc, seq_len_tensor, group_indices_tensor, batches,
+                      max_seq_length, add_inputs=False) -> int:
+    """Kernel variant a sgmv_grouped_gemm call with these arguments would launch (0 = none)."""
+    return _grouped_plan("sgmv_grouped_gemm_plan", (inputs, weights, output_tensor, b_seq_start_loc, seq_len_tensor,
+                                                    group_indices_tensor), batches, max_seq_length, add_inputs)
 
 
 def grouped_wgrad_plan(grad_output, inputs, grad_weights, b_seq_start_loc, seq_len_tensor, group_indices_tensor,
                        batches, max_seq_length, add_inputs=False) -> int:
     """Kernel variant a sgmv_grouped_wgrad call with these arguments would launch (0 = none)."""
-    dev = _device_of(grad_weights)
-    d = _pack((grad_output, inputs, grad_weights, b_seq_start_loc, seq_len_tensor, group_indices_tensor), dev)
-    v = ctypes.c_int(0)
-    _call("sgmv_grouped_wgrad_plan", _abi.fast.sgmv_grouped_wgrad_plan, dev, *d, int(batches), int(max_seq_length),
-          int(bool(add_inputs)), ctypes.byref(v))
-    return v.value
+    return _grouped_plan("sgmv_grouped_wgrad_plan", (grad_output, inputs, grad_weights, b_seq_start_loc, seq_len_tensor,
+                                                     group_indices_tensor), batches, max_seq_length, add_inputs)
 
 
 def validate_metadata(b_seq_start_loc, seq_len_tensor, lora_indices_tensor, batches, lora_num,

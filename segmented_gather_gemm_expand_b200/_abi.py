@@ -45,11 +45,6 @@ def make_tensor(data_ptr, dtype, shape, strides):
     return t
 
 
-class _Fast:
-    """Entry points that take descriptors by address (filled by load())."""
-
-
-fast = _Fast()
 _lib = None
 
 
@@ -99,11 +94,6 @@ def load():
         fn.restype = plan.restype = i32
         fn.argtypes = [P, P, P, P, P, P, i64, i64, i32, vp]
         plan.argtypes = [P, P, P, P, P, P, i64, i64, i32, ctypes.POINTER(i32)]
-    # the same functions with descriptors passed as plain addresses
-    for name in ("sgmv_lora_linear", "sgmv_lora_linear_plan", "sgmv_grouped_gemm", "sgmv_grouped_gemm_plan",
-                 "sgmv_grouped_wgrad", "sgmv_grouped_wgrad_plan"):
-        args = [vp if a is P else a for a in getattr(lib, name).argtypes]
-        setattr(fast, name, ctypes.CFUNCTYPE(i32, *args)((name, lib)))
     lib.sgmv_validate_metadata.restype = i32
     lib.sgmv_validate_metadata.argtypes = [P, P, P, i64, i64, i64, vp, vp]
     lib.sgmv_status_string.restype = ctypes.c_char_p
@@ -116,3 +106,16 @@ def load():
     lib.sgmv_version.argtypes = []
     _lib = lib
     return lib
+
+
+def load_binding(lib):
+    """The extension that calls the large products (built beside the library), bound to lib's functions."""
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise ImportError("_binding.so not found or not loadable; build it with "
+                          "`python segmented_gather_gemm_expand_b200/build.py`") from e
+    address = [ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+               for n in ("sgmv_lora_linear", "sgmv_grouped_gemm", "sgmv_grouped_wgrad")]
+    _binding.init(*address)
+    return _binding

@@ -1,4 +1,5 @@
-"""Build libsgmv.so (the C-ABI CUDA library) in-tree for sm_100a.
+"""Build libsgmv.so (the C-ABI CUDA library) in-tree for sm_100a, and the
+CPython extension that marshals torch tensors for its large products.
 
 Usage: python segmented_gather_gemm_expand_b200/build.py [--force]
 (run as a script: importing the package needs the library this builds)
@@ -13,6 +14,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libsgmv.so")
+BINDING = os.path.join(HERE, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
@@ -25,7 +27,32 @@ def sources():
                   [os.path.join(INCLUDE, "sgmv.h")])
 
 
+def build_binding(force: bool = False) -> str:
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and os.path.exists(BINDING):
+        if os.path.getmtime(BINDING) >= max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "sgmv.h"))):
+            return BINDING
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", "/usr/local/cuda/include",
+           "-o", BINDING + ".tmp", src, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+           "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("the compiler failed building _binding.so")
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_binding(force)
     if not force and os.path.exists(LIB):
         newest = max(os.path.getmtime(s) for s in sources())
         if os.path.getmtime(LIB) >= newest:
