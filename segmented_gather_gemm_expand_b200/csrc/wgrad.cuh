@@ -11,12 +11,14 @@
 // A segment may start and end anywhere.  Its last block issues only the K=16
 // steps that hold rows, and the rows past the end in the last of them, which
 // belong to another segment (or are anything at all: 0 x NaN is NaN), are
-// zeroed in shared memory in both operands by a warp of their own (warp 10)
-// before the MMA sees the stage.
+// zeroed in shared memory in both operands by warps of their own (10 to 12, by
+// stage) before the MMA sees the stage.
 //
 // Several segments of one index add up in segment order in one accumulator.
-// Indexes without rows get zeros (or keep dW in add mode).  The tiles of the
-// longest indexes go first, so that the last round of the deal is short tiles.
+// Indexes without rows get zeros (or keep dW in add mode).  The tiles of long and
+// short indexes take turns (longest, shortest, second longest, ...): the MMAs
+// of a long one then hide the stores of short ones, whose tiles are all
+// epilogue, and the deal ends with middling ones.
 #pragma once
 
 #include "grouped.cuh"
@@ -33,7 +35,9 @@ constexpr int HALF = 64 * BT * 2;          // one box of 64 columns: 8 KB
 constexpr int STAGE = 4 * HALF;            // two boxes of X, two of dY
 constexpr int TURN = 32 * 64;              // epilogue: a warp's 32 x 32 halves
 constexpr int FIX_WARP = 2 + EPI_WARPS;
-constexpr int THREADS = 32 * (FIX_WARP + 1);
+constexpr int FIX_WARPS = 3;
+constexpr int WARPS = FIX_WARP + FIX_WARPS;
+constexpr int THREADS = 32 * WARPS;
 constexpr int SMEM_LIMIT = grp::SMEM_LIMIT;
 
 struct Geo {
@@ -46,13 +50,14 @@ struct Geo {
 };
 
 struct Seg {
-    int32_t row0, rows, next;   // next segment of the same index, -1 at the end
+    int32_t row0, rows, index;  // index -1: nothing to add
+    int32_t next;               // next segment of the same index, -1 at the end
 };
 
 struct Exp {
     int32_t first;              // first segment, -1 for none
     int32_t rows;               // tokens in all
-    int32_t order;              // place in descending order of rows -> index
+    int32_t order;              // place in the deal -> index
 };
 
 // p: x = X, w = dY (w_ns its row stride), lora_num = number of indexes, out = dW with row stride H and N = X's columns.
@@ -78,7 +83,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     if (tid == 0) {
         s_abort = 0;
         for (uint32_t i = 0; i < S; ++i) {
-            mbar_init(smem_u32(&full[i]), 2);   // two arrivals of the first CTA's producer, or one of each CTA's warp 10
+            mbar_init(smem_u32(&full[i]), 2);   // two arrivals of the first CTA's producer, or one of each CTA's zeroing warp
             mbar_init(smem_u32(&empty[i]), 1);
             mbar_init(smem_u32(&part[i]), 1);
         }
@@ -100,42 +105,38 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     const int32_t nseg = (int32_t)p.batches, nexp = (int32_t)p.lora_num;
     for (int32_t b = tid; b < nseg; b += THREADS) {
         const Segment s = load_segment(p, b);
-        segs[b] = Seg{(int32_t)s.row0, (int32_t)s.rows, s.rows > 0 ? (int32_t)s.adapter : -1};
+        segs[b] = Seg{(int32_t)s.row0, (int32_t)s.rows, s.rows > 0 ? (int32_t)s.adapter : -1, -1};
     }
     __syncthreads();
-    // the segments of an index as a list: `next` holds the index until every thread has found its successor
-    for (int32_t e = tid; e < nexp; e += THREADS) {
-        int32_t first = -1, rows = 0;
-        for (int32_t b = 0; b < nseg; ++b)
-            if (segs[b].next == e) {
-                if (first < 0) first = b;
-                rows += segs[b].rows;
-            }
-        exps[e].first = first;
-        exps[e].rows = rows;
-    }
-    for (int32_t base = 0; base < nseg; base += THREADS) {   // ascending: later segments still hold their index
-        const int32_t b = base + tid;
-        int32_t next = -1;
-        if (b < nseg && segs[b].next >= 0)
-            for (int32_t c = b + 1; c < nseg; ++c)
-                if (segs[c].next == segs[b].next) {
-                    next = c;
-                    break;
-                }
-        __syncthreads();
-        if (b < nseg) segs[b].next = next;
-        __syncthreads();
-    }
-    __syncthreads();
-    for (int32_t e = tid; e < nexp; e += THREADS) {
-        const int32_t mine = exps[e].rows;
-        int32_t place = 0;
-        for (int32_t o = 0; o < nexp; ++o) {
-            const int32_t r = exps[o].rows;
-            place += (r > mine || (r == mine && o < e)) ? 1 : 0;
+    // each index's segments as a list, and its rows: a warp per index, a lane per segment
+    for (int32_t e = warp; e < nexp; e += WARPS) {
+        int32_t first = -1, last = -1, rows = 0;
+        for (int32_t b0 = 0; b0 < nseg; b0 += 32) {
+            const int32_t b = b0 + lane;
+            const bool in = b < nseg && segs[b].index == e;
+            const unsigned mask = __ballot_sync(0xffffffffu, in);
+            if (!mask) continue;
+            rows += __reduce_add_sync(0xffffffffu, in ? segs[b].rows : 0);
+            const unsigned after = mask & ~((2u << lane) - 1);
+            if (in && after) segs[b].next = b0 + __ffs(after) - 1;
+            if (lane == 0 && last >= 0) segs[last].next = b0 + __ffs(mask) - 1;
+            if (first < 0) first = b0 + __ffs(mask) - 1;
+            last = b0 + 31 - __clz(mask);
         }
-        exps[place].order = e;
+        if (lane == 0) {
+            exps[e].first = first;
+            exps[e].rows = rows;
+        }
+    }
+    __syncthreads();
+    for (int32_t e = warp; e < nexp; e += WARPS) {
+        const int32_t mine = exps[e].rows;
+        int32_t place = 0;   // in descending order of rows
+        for (int32_t o0 = 0; o0 < nexp; o0 += 32) {
+            const int32_t o = o0 + lane, r = o < nexp ? exps[o].rows : -1;
+            place += __popc(__ballot_sync(0xffffffffu, r > mine || (r == mine && o < e)));
+        }
+        if (lane == 0) exps[2 * place < nexp ? 2 * place : 2 * (nexp - 1 - place) + 1].order = e;
     }
     tc_fence_before();
     cluster_sync();
@@ -256,7 +257,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
             }
         }
         __syncwarp();
-    } else if (warp == FIX_WARP) {
+    } else if (warp >= FIX_WARP) {
         // ------------------------------------------------------------ rows past a segment's end
         uint32_t q = 0, phase = 0;   // phase: one bit per stage (at most 32 stages)
         bool ok = true;
@@ -269,6 +270,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
                 q += (uint32_t)blocks;
                 if (rem % 16 == 0) continue;   // whole K steps (or a whole block)
                 const uint32_t s = (q - 1) % S;
+                if (s % FIX_WARPS != (uint32_t)(warp - FIX_WARP)) continue;   // a stage has one warp: it sees every phase
                 if (!warp_wait(smem_u32(&part[s]), (phase >> s) & 1, abort_flag, DEVERR_TIMEOUT_CONVERT)) {
                     ok = false;
                     break;
@@ -280,7 +282,10 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
                         *reinterpret_cast<uint4*>(smem + s * STAGE + i * HALF + rem * 128 + o) = make_uint4(0, 0, 0, 0);
                 asm volatile("fence.proxy.async;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&full[s]), 0));
+                if (lane == 0) {
+                    if (crank == 0) mbar_arrive(smem_u32(&full[s]));
+                    else mbar_arrive_cluster(map_to_rank(smem_u32(&full[s]), 0));
+                }
             }
         }
     } else {
