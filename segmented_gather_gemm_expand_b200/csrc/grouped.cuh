@@ -133,7 +133,7 @@ struct Tile {
     int32_t tok;   // token tile within the segment
 };
 
-__device__ __forceinline__ void decode_tile(const Seg* segs, int32_t nseg, const Geo& g, int32_t id, int32_t wtile,
+__host__ __device__ __forceinline__ void decode_tile(const Seg* segs, int32_t nseg, const Geo& g, int32_t id, int32_t wtile,
                                             Tile& t) {
     Seg s{0, g.dense_rows, 0, g.dense_ts, 0};
     if (g.dense_rows < 0) {
@@ -397,12 +397,60 @@ __device__ __forceinline__ void put(float (&v)[NT], int64_t row, int valid, int6
         if (j < valid) o[j * p.H] = (uint16_t)float_to_half_bits(v[j], ob);
 }
 
+// LORA_MMA, where an accumulator is an infinity or NaN: rows outside a run take
+// part in the run's MMA with t = 0, and 0 times an infinity in that adapter's B
+// would reach other requests' rows.  Where a run of the tile has such a value in
+// B's row n, the outputs of column n that are no finite numbers (of tokens tok ..
+// tok + valid - 1 of the tile, whose first row is row0) are computed again by the
+// formula, in fp32, each by the whole warp; `runs` first .. last are the tile's.
+template <int NT>
+__device__ __forceinline__ void repair_outputs(float (&v)[NT], int tok, int valid, int64_t row0, int64_t n, const Run* runs,
+                                               int first, int last, const Problem& p, const Lora& lo) {
+    float z = 0.f;   // NaN if any value is no finite number
+#pragma unroll
+    for (int j = 0; j < NT; ++j) z = fmaf(v[j], 0.f, z);
+    if (!__any_sync(0xffffffffu, z != 0.f)) return;
+    unsigned bad = 0;
+    if (z != 0.f && n < p.N) {
+        float b = 0.f;
+        for (int r = first; r < last; ++r)
+            for (int k = 0; k < lo.R; ++k)
+                b = fmaf(load_elem(lo.b, p.w_dt, (int64_t)runs[r].adapter * lo.b_as + n * lo.b_ns + k * lo.b_ks), 0.f, b);
+        if (b != 0.f)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) bad |= (j < valid && fmaf(v[j], 0.f, 0.f) != 0.f ? 1u : 0u) << j;
+    }
+    const int lane = threadIdx.x % 32;
+    while (const unsigned who = __ballot_sync(0xffffffffu, bad != 0)) {
+        const int src = __ffs(who) - 1, at = __shfl_sync(0xffffffffu, __ffs(bad) - 1, src);
+        const int64_t row = row0 + tok + at, col = n - lane + src;
+        float sum = 0.f;
+        for (int64_t k = lane; k < p.K; k += 32)
+            sum = fmaf(load_elem(p.x, p.x_dt, row * p.x_rs + k * p.x_cs), load_elem(p.w, p.w_dt, col * p.w_ns + k * p.w_ks), sum);
+        for (int r = first; r < last; ++r)
+            if (tok + at >= runs[r].begin && tok + at < runs[r].end)
+                for (int k = lane; k < lo.R; k += 32)
+                    sum = fmaf(lo.t[row * lo.R + k],
+                               load_elem(lo.b, p.w_dt, (int64_t)runs[r].adapter * lo.b_as + col * lo.b_ns + k * lo.b_ks), sum);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == src) {
+            bad &= bad - 1;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                if (j == at) v[j] = sum;
+        }
+    }
+}
+
 // A warp's share of a tile in TMEM: columns (tokens) c0, c0 + 64, ... in pieces
 // of 32, the next piece under way while one is stored.  `drained` runs once
-// the last piece is in registers.
-template <class Drained>
+// the last piece is in registers; repair(v, token) is for values that are no
+// finite numbers.
+template <class Drained, class Repair>
 __device__ __forceinline__ void drain(uint32_t taddr, int c0, int ts, int64_t row0, int rows, int64_t n, float bias,
-                                      const Problem& p, uint32_t* stage, bool out_vec, Drained&& drained) {
+                                      const Problem& p, uint32_t* stage, bool out_vec, Drained&& drained,
+                                      Repair&& repair) {
     uint32_t next[32];
     float v[32];
     if (c0 >= ts) {
@@ -413,7 +461,10 @@ __device__ __forceinline__ void drain(uint32_t taddr, int c0, int ts, int64_t ro
     for (int c = c0;; c += 64) {
         tmem_ld_wait(next);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(next[j]) + bias;
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(next[j]);
+        repair(v, c);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += bias;
         const bool more = c + 64 < ts;
         if (more) tmem_ld32(taddr + (uint32_t)c + 64, next);
         else drained();
@@ -1000,6 +1051,9 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                               if (CG == 2) mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[acc]), 0));
                               else mbar_arrive(smem_u32(&acc_empty[acc]));
                           }
+                      }, [&](float (&v)[32], int c) {
+                          if (LORA != LORA_MMA) return;
+                          repair_outputs<32>(v, c, t.rows - c, t.row0, col, runs, first_run[t.tok], first_run[t.tok + 1], p, lo);
                       });
             } else {
                 // Partial sums go to the CTA that owns the token, four tokens of a weight row
@@ -1034,7 +1088,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                     for (int j0 = half * 8; j0 < cnt; j0 += 16) {
                         float v[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] = bias;
+                        for (int j = 0; j < 8; ++j) v[j] = 0.f;
                         if (LORA == LORA_FMA) {
                             uint32_t b[8];
                             tmem_ld8(delta + (uint32_t)j0, b);
@@ -1052,6 +1106,11 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                                     v[j + 2] += f.z;
                                     v[j + 3] += f.w;
                                 }
+                        if (LORA == LORA_MMA)
+                            repair_outputs<8>(v, t0 + j0, cnt - j0, t.row0, col, runs, first_run[t.tok], first_run[t.tok + 1], p,
+                                              lo);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] += bias;
                         put<8>(v, (int64_t)t.row0 + t0 + j0, min(8, cnt - j0), col, p, stage, g.out_vec);
                     }
                 }

@@ -310,7 +310,8 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
             };
             const int64_t row0 = (int64_t)e * g.rows_per_group + n0;
             if (any) {
-                grp::drain(taddr, half * 32, g.ts, row0, valid, col, 0.f, p, stage, g.out_vec, drained);
+                grp::drain(taddr, half * 32, g.ts, row0, valid, col, 0.f, p, stage, g.out_vec, drained,
+                           [](float (&)[32], int) {});
             } else {
                 drained();
                 for (int c = half * 32; c < g.ts && !p.add; c += 64) {

@@ -429,3 +429,200 @@ def test_repeated_calls_give_the_same_bits():
     for o in outs:
         sg.sgmv_grouped_gemm(x, w, o, *m, 9, 1)
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+# ---------------------------------------------------------------- layouts, limits and values at the edges
+
+@pytest.mark.parametrize("lens", ["decode", "decode_many", "long"])
+@pytest.mark.parametrize("layout", ["rank5", "rank72", "turned", "pitched"])
+def test_lora_b_layouts(lens, layout):
+    """Ranks and B layouts that the copies of whole rows do not take, beside inputs that the tensor cores do."""
+    g = gen(21)
+    lens = {"decode": [1] * 33, "decode_many": [1] * 300, "long": [150, 300, 7]}[lens]
+    n, K, N, A = len(lens), 128, 200, 9
+    R = {"rank5": 5, "rank72": 72, "turned": 16, "pitched": 16}[layout]
+    m, T = meta(lens, [(5 * i) % (A + 1) - 1 for i in range(n)])
+    x, w, a = ints(g, (T, K), "bf16", 1), ints(g, (N, K), "bf16"), ints(g, (A, R, K), "bf16", 1)
+    b = {"turned": lambda: ints(g, (A, R, N), "bf16", 1).transpose(1, 2), "pitched": lambda: ints(g, (A, N, R + 8), "bf16", 1)[:, :, :R]}.get(
+        layout, lambda: ints(g, (A, N, R), "bf16", 1))()
+    for out_dt in ("bf16", "f32"):
+        out = torch.zeros(T, N, device="cuda", dtype=DT[out_dt])
+        assert sg.lora_linear_plan(x, w, a, b, out, *m, n, max(lens))[0] == sg.VARIANT_TC
+        run_lora(x, w, a, b, out, m, n, max(lens))
+        assert torch.equal(out, rounded(lora_ref(x, w, a, b, m, None, T), out_dt))
+
+
+def test_lora_weight_read_along_its_other_axis():
+    g = gen(22)
+    m, T = meta([90, 1, 60], [1, 0, 1])
+    x, w = ints(g, (T, 200), "f16", 1), ints(g, (200, 328), "f16").t()
+    a, b, out = ints(g, (2, 16, 200), "f16", 1), ints(g, (2, 328, 16), "f16", 1), torch.zeros(T, 328, device="cuda")
+    assert sg.lora_linear_plan(x, w, a, b, out, *m, 3, 90)[0] == sg.VARIANT_TC
+    run_lora(x, w, a, b, out, m, 3, 90)
+    assert torch.equal(out, lora_ref(x, w, a, b, m, None, T).float())
+
+
+@pytest.mark.parametrize("variant", [sg.VARIANT_AUTO, sg.VARIANT_TC_WIDE])
+@pytest.mark.parametrize("K,bad", [(256, float("inf")), (4096, float("nan"))])
+def test_one_requests_broken_adapter_or_row_stays_its_own(variant, K, bad):
+    """An adapter whose B holds infinities or NaN, and a row of x that does, reach their own rows only, also in a batch whose
+    runs share token tiles."""
+    g = gen(23)
+    m, T = meta([70, 33, 50, 20, 90], [0, 1, 2, 1, 0])
+    x, w, a, b = ints(g, (T, K), "bf16", 1), ints(g, (264, K), "bf16", 1), ints(g, (3, 16, K), "bf16", 1), ints(g, (3, 264, 16), "bf16", 1)
+    ref = lora_ref(x, w, a, b, m, None, T).float()
+    b[1, 5:200, 3] = bad
+    x[160, 7] = bad
+    out = torch.zeros(T, 264, device="cuda")
+    sg.set_variant(variant)
+    run_lora(x, w, a, b, out, m, 5, 90)
+    keep = torch.ones(T, dtype=torch.bool)
+    keep[70:103] = keep[153:173] = False
+    assert torch.equal(out[keep], ref[keep])
+    assert torch.equal(out[70:103, 200:], ref[70:103, 200:])   # the adapter's finite columns too
+    assert not torch.isfinite(out[160]).any()
+
+
+def test_lora_t_beyond_fp16():
+    """t is held in fp32: values past fp16's largest number enter the product whole."""
+    g = gen(24)
+    m, T = meta([40, 25], [0, 1])
+    x = torch.full((T, 512), 16.0, device="cuda", dtype=torch.float16)
+    a = torch.full((2, 16, 512), 16.0, device="cuda", dtype=torch.float16)   # t = 131072
+    w, b = ints(g, (264, 512), "f16", 1), ints(g, (2, 264, 16), "f16", 1)
+    out = torch.zeros(T, 264, device="cuda")
+    run_lora(x, w, a, b, out, m, 2, 40)
+    assert torch.equal(out, lora_ref(x, w, a, b, m, None, T).float())
+
+
+@pytest.mark.parametrize("count,length", [(4000, 2), (5000, 1)])
+def test_many_segments(count, length):
+    g = gen(25)
+    E = 50
+    m, T = meta([length] * count, [i % E for i in range(count)])
+    x, w, out = ints(g, (T, 64), "bf16"), ints(g, (E, 72, 64), "bf16"), torch.zeros(T, 72, device="cuda")
+    sg.sgmv_grouped_gemm(x, w, out, *m, count, length)
+    e = (torch.arange(T) // length % E).cuda()
+    assert torch.equal(out, torch.bmm(w.float()[e], x.float()[:, :, None])[:, :, 0])
+    dy, dw = ints(g, (T, 72), "bf16", 1), torch.zeros(E, 72, 64, device="cuda")
+    sg.sgmv_grouped_wgrad(dy, x, dw, *m, count, length)
+    ref = torch.zeros(E, 72, 64, device="cuda").index_add_(0, e, dy.float()[:, :, None] * x.float()[:, None, :])
+    assert torch.equal(dw, ref)
+    base, a, b = ints(g, (72, 64), "bf16"), ints(g, (E, 8, 64), "bf16", 1), ints(g, (E, 72, 8), "bf16", 1)
+    run_lora(x, base, a, b, out, m, count, length)
+    t = torch.bmm(a.float()[e], x.float()[:, :, None])
+    assert torch.equal(out, x.float() @ base.float().T + torch.bmm(b.float()[e], t)[:, :, 0])
+
+
+def test_outputs_and_weights_past_32_bit_offsets():
+    """Elements of the output and of the experts' weights at offsets beyond 2^31."""
+    g = gen(26)
+    T, N, K = 66000, 33000, 64      # 2.18e9 outputs
+    out = torch.zeros(T, N, device="cuda", dtype=torch.bfloat16)
+    m = [torch.tensor(v).cuda() for v in ([0, 65900], [70, 100], [0, 1])]
+    x, w = torch.zeros(T, K, device="cuda", dtype=torch.bfloat16), ints(g, (2, N, K), "bf16")
+    x[:70], x[65900:] = ints(g, (70, K), "bf16"), ints(g, (100, K), "bf16")
+    sg.sgmv_grouped_gemm(x, w, out, *m, 2, 100)
+    for a, b, e in ((0, 70, 0), (65900, 66000, 1)):
+        assert torch.equal(out[a:b], rounded(x[a:b].double() @ w[e].double().T, "bf16"))
+    assert not out[70:65900].any()
+    del out, w
+    E, N, K = 540, 1000, 4096       # 2.2e9 weights
+    w = torch.zeros(E, N, K, device="cuda", dtype=torch.bfloat16)
+    w[E - 1] = ints(g, (N, K), "bf16")
+    x, out = ints(g, (20, K), "bf16"), torch.zeros(20, N, device="cuda")
+    m, _ = meta([20], [E - 1])
+    sg.sgmv_grouped_gemm(x, w, out, *m, 1, 20)
+    assert torch.equal(out, (x.double() @ w[E - 1].double().T).float())
+    dy = ints(g, (20, N), "bf16", 1)
+    sg.sgmv_grouped_wgrad(dy, x, w, *m, 1, 20)
+    assert torch.equal(w[E - 1], rounded(dy.double().T @ x.double(), "bf16")) and not w[: E - 1].any()
+
+
+def test_inputs_and_output_of_different_row_counts():
+    g = gen(27)
+    m, _ = meta([64, 64], [0, 1])
+    x, w, out = ints(g, (100, 64), "bf16"), ints(g, (2, 40, 64), "bf16"), ints(g, (90, 40), "f32")
+    ref = grouped_ref(x, w, out, m, False).float()
+    sg.sgmv_grouped_gemm(x, w, out, *m, 2, 64)
+    assert torch.equal(out, ref)
+    a, b, base = ints(g, (2, 8, 64), "bf16", 1), ints(g, (2, 40, 8), "bf16", 1), ints(g, (40, 64), "bf16")
+    out = torch.full((130, 40), 5.0, device="cuda")
+    run_lora(x, base, a, b, out, m, 2, 64)
+    assert torch.equal(out[:100], lora_ref(x, base, a, b, m, None, 100).float()) and (out[100:] == 5).all()
+
+
+def test_empty_calls_and_workspace_refusals():
+    g = gen(28)
+    m, T = meta([3], [0])
+    x, w, a, b = ints(g, (T, 64), "bf16"), ints(g, (40, 64), "bf16"), ints(g, (1, 16, 64), "bf16"), ints(g, (1, 40, 16), "bf16")
+    out = torch.full((T, 40), 3.0, device="cuda")
+    _, need, pref = sg.lora_linear_plan(x, w, a, b, out, *m, 1, 3)
+    assert 0 < need <= pref
+    ws = torch.empty(pref + 16, dtype=torch.uint8, device="cuda")
+    for bad in (None, ws[: need - 1], ws[8:]):
+        with pytest.raises(sg.SgmvError) as e:
+            sg.sgmv_lora_linear(x, w, a, b, out, *m, 1, 3, workspace=bad)
+        assert e.value.code == -17
+    sg.sgmv_lora_linear(x[:0], w, a, b, out[:0], *m, 1, 3)
+    sg.sgmv_lora_linear(x, w[:0], a, b[:, :0], out[:, :0], *m, 1, 3)
+    sg.sgmv_grouped_gemm(x, w[None], out, *m, 0, 3)
+    assert (out == 3).all()
+    with pytest.raises(ValueError):
+        sg.sgmv_grouped_gemm(x, w[None].cpu(), out, *m, 1, 3)
+    with pytest.raises(TypeError):
+        sg.sgmv_grouped_gemm(x.double(), w[None], out, *m, 1, 3)
+    sg.set_variant(sg.VARIANT_DECODE)
+    for call in (lambda: sg.sgmv_grouped_gemm(x, w[None], out, *m, 1, 3), lambda: sg.sgmv_grouped_wgrad(x, x, torch.zeros(1, 64, 64).cuda(), *m, 1, 3),
+                 lambda: sg.sgmv_lora_linear(x, w, a, b, out, *m, 1, 3, workspace=ws)):
+        with pytest.raises(sg.SgmvError) as e:
+            call()
+        assert e.value.code == -13
+
+
+def test_call_reads_what_the_preceding_kernels_wrote():
+    """x, weights, adapters and metadata rewritten on the device right before each call."""
+    g = gen(29)
+    m, T = meta([30, 1, 40], [1, 0, 1])
+    x, w, a, b = ints(g, (T, 512), "bf16", 1), ints(g, (264, 512), "bf16", 1), ints(g, (2, 16, 512), "bf16", 1), ints(g, (2, 264, 16), "bf16", 1)
+    out = torch.zeros(T, 264, device="cuda")
+    _, _, pref = sg.lora_linear_plan(x, w, a, b, out, *m, 3, 40)
+    ws = torch.empty(pref, dtype=torch.uint8, device="cuda")
+    outs, refs = [], []
+    for i in range(6):
+        for t in (x, w, a, b):
+            t.mul_(-1 if i % 2 else 1).add_(1 if i % 3 else -1)
+        m[2].copy_(torch.tensor([i % 2, 1, -1 if i == 3 else (i + 1) % 2], dtype=torch.int32), non_blocking=True)
+        sg.sgmv_lora_linear(x, w, a, b, out, *m, 3, 40, workspace=ws)
+        outs.append(out.clone())
+        refs.append(lora_ref(x, w, a, b, m, None, T).float())
+    for o, r in zip(outs, refs):
+        assert torch.equal(o, r)
+
+
+def test_python_calls_on_another_device_than_the_current_one():
+    if torch.cuda.device_count() < 2:
+        pytest.skip("needs two GPUs")
+    g = gen(30)
+    with torch.cuda.device(1):
+        m, T = meta([9], [0])
+        x, w, out = ints(g, (T, 64), "bf16"), ints(g, (1, 40, 64), "bf16"), torch.zeros(T, 40, device="cuda")
+    sg.sgmv_grouped_gemm(x, w, out, *m, 1, 9)
+    torch.cuda.synchronize(1)
+    assert torch.equal(out, (x.double() @ w[0].double().T).float())
+
+
+def test_values_that_are_no_numbers_in_shared_inputs():
+    """NaN rows of x and infinite rows of the shared weight come out as the formula has them, at no other place."""
+    g = gen(31)
+    m, T = meta([140, 160], [0, 1])
+    x, w, a, b = ints(g, (T, 4096), "bf16", 1), ints(g, (264, 4096), "bf16", 1), ints(g, (2, 16, 4096), "bf16", 1), ints(g, (2, 264, 16), "bf16", 1)
+    ref = lora_ref(x, w, a, b, m, None, T).float()
+    x[::3] = float("nan")
+    w[7, 5] = float("inf")
+    out = torch.zeros(T, 264, device="cuda")
+    run_lora(x, w, a, b, out, m, 2, 160)
+    rows = torch.arange(T) % 3 != 0
+    cols = torch.arange(264) != 7
+    assert torch.isnan(out[::3]).all() and not torch.isfinite(out[:, 7]).any()
+    assert torch.equal(out[rows][:, cols], ref[rows][:, cols])
