@@ -75,6 +75,7 @@ constexpr int RING_MAX_RANK = 64;
 constexpr int T_ROW = RING_MAX_RANK * 4;   // a slot's row of t, fp32
 constexpr int NUM_XMAPS = 4;            // x boxes of 16, 32, 64, 128 rows
 constexpr int MAX_SPLITS = 8;
+constexpr int TURN = 2 * 8 * 64;        // shared memory in which an epilogue warp turns 8 x 32 halves round, twice
 constexpr int BAND = 8;                 // token tiles walked together before the next weight tile
 constexpr int SEG_CAP = 4096;           // most segments a launch takes
 constexpr int SMEM_LIMIT = 232448 - 1024;
@@ -93,7 +94,6 @@ struct Geo {
     int32_t b_slots, b_bytes;   // LORA_FMA: a ring of tokens' B and t per half of the epilogue (0 slots: read directly), bytes of B in a slot
     int32_t off_t, t_bytes, off_tr, off_out, off_red, off_seg, off_bar;
     int32_t out_vec;      // half output in 16-byte pieces
-    int32_t turn_bytes;   // shared memory in which an epilogue warp turns its halves round
     int32_t acc_stride, tmem_cols;
     int32_t w_mn;         // the weights' N axis is the contiguous one
     int32_t dense_rows;   // >= 0: one segment of that many rows with group 0; -1: the call's segments
@@ -305,95 +305,61 @@ __device__ __forceinline__ float lora_dot(const uint8_t* rows, int row, int R, i
 // finishes, 8 of every 16.
 __device__ __forceinline__ int half_token(int half, int i) { return (i >> 3) * 16 + half * 8 + (i & 7); }
 
-// Adds the old output (add mode), rounds once and stores rows row .. row +
-// valid - 1 of column n (= the warp's first column + lane).
-//
-// fp32 output: a warp's store is a row's 32 columns, 128 bytes.  Half output:
-// that would be NT stores of 64 bytes for NT rows, and a tile of 256 x 256
-// spent 8500 cycles on them; so the warp turns its piece round in shared memory
-// (`stage`) and stores 8 rows at a time, 16 bytes per lane: 32 tokens as pairs
-// (one packed conversion and one 4-byte store per pair and column, split again
-// after the read), 8 tokens as halves.  That needs 16-byte aligned output rows
-// of whole 16-byte pieces; other outputs are stored element by element.
-template <int NT>
-__device__ __forceinline__ void put(float (&v)[NT], int64_t row, int valid, int64_t n, const Problem& p, uint32_t* stage,
-                                    bool out_vec) {
+// Adds the old output (add mode), rounds once and stores eight rows, row .. row +
+// valid - 1, of column n (= the warp's first column + lane).  fp32: a warp's
+// store is a row's 32 columns, 128 bytes.  Halves: the warp turns its 8 x 32
+// piece round in shared memory (`turn`) and stores 16 bytes per lane; where the
+// output's rows are not whole 16-byte pieces (vec false), element by element.
+__device__ __forceinline__ void put8(float (&v)[8], int64_t row, int valid, int64_t n, const Problem& p, uint32_t* turn,
+                                     bool vec) {
     if (valid <= 0) return;
-    const bool n_ok = n < p.N;
     const int64_t base = row * p.H + n;
     if (p.out_dt == SGMV_F32) {
-        if (!n_ok) return;
+        if (n >= p.N) return;
         float* o = static_cast<float*>(p.out) + base;
         if (p.add) {
-            float old[NT];
+            float old[8];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) old[j] = j < valid ? o[j * p.H] : 0.f;
+            for (int j = 0; j < 8; ++j) old[j] = j < valid ? o[j * p.H] : 0.f;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) v[j] += old[j];
+            for (int j = 0; j < 8; ++j) v[j] += old[j];
         }
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < 8; ++j)
             if (j < valid) o[j * p.H] = v[j];
         return;
     }
     const bool ob = p.out_dt == SGMV_BF16;
-    const int lane = threadIdx.x % 32;
-    if (out_vec) {
-        const int r = lane / 4, c = (lane % 4) * 8;
-        if (n - lane + c >= p.N) valid = 0;   // this lane's 8 columns are past the end (N: a multiple of 8)
-        uint16_t* o = static_cast<uint16_t*>(p.out) + (base - lane + c);
-        uint16_t* halves = reinterpret_cast<uint16_t*>(stage);   // [token][32 columns]
+    if (vec) {
+        const int lane = threadIdx.x % 32, r = lane / 4, c = (lane % 4) * 8;
+        const bool mine = r < valid && n - lane + c < p.N;   // this lane's row and 8 columns (N: a multiple of 8)
+        uint16_t* o = static_cast<uint16_t*>(p.out) + (base - lane + r * p.H + c);
+        uint16_t* halves = reinterpret_cast<uint16_t*>(turn);   // [token][32 columns]
         if (p.add) {
-#pragma unroll
-            for (int j = 0; j < NT; j += 8)
-                if (j + r < valid)
-                    *reinterpret_cast<uint4*>(halves + (j + r) * 32 + c) = *reinterpret_cast<const uint4*>(o + (j + r) * p.H);
+            if (mine) *reinterpret_cast<uint4*>(halves + r * 32 + c) = *reinterpret_cast<const uint4*>(o);
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < NT; ++j) v[j] += half_bits_to_float(halves[j * 32 + lane], ob);   // rows past `valid` are not stored
+            for (int j = 0; j < 8; ++j) v[j] += half_bits_to_float(halves[j * 32 + lane], ob);   // rows past `valid` are not stored
             __syncwarp();
         }
-        if (NT == 32) {
 #pragma unroll
-            for (int j = 0; j < NT; j += 2) stage[j * 16 + lane] = pack2(v[j], v[j + 1], ob);   // [pair][32 columns]
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < NT; j += 16) {
-                const uint4 x = *reinterpret_cast<const uint4*>(stage + (j / 2 + r) * 32 + c);
-                const uint4 y = *reinterpret_cast<const uint4*>(stage + (j / 2 + r) * 32 + c + 4);
-                const int at = j + 2 * r;
-                if (at < valid)
-                    *reinterpret_cast<uint4*>(o + at * p.H) =
-                        make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.z, x.w, 0x5410),
-                                   __byte_perm(y.x, y.y, 0x5410), __byte_perm(y.z, y.w, 0x5410));
-                if (at + 1 < valid)
-                    *reinterpret_cast<uint4*>(o + (at + 1) * p.H) =
-                        make_uint4(__byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x7632),
-                                   __byte_perm(y.x, y.y, 0x7632), __byte_perm(y.z, y.w, 0x7632));
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < NT; ++j) halves[j * 32 + lane] = (uint16_t)float_to_half_bits(v[j], ob);
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < NT; j += 8)
-                if (j + r < valid)
-                    *reinterpret_cast<uint4*>(o + (j + r) * p.H) = *reinterpret_cast<const uint4*>(halves + (j + r) * 32 + c);
-        }
+        for (int j = 0; j < 8; ++j) halves[j * 32 + lane] = (uint16_t)float_to_half_bits(v[j], ob);
+        __syncwarp();
+        if (mine) *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(halves + r * 32 + c);
         __syncwarp();
         return;
     }
-    if (!n_ok) return;
+    if (n >= p.N) return;
     uint16_t* o = static_cast<uint16_t*>(p.out) + base;
     if (p.add) {
-        uint16_t old[NT];
+        uint16_t old[8];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) old[j] = j < valid ? o[j * p.H] : (uint16_t)0;
+        for (int j = 0; j < 8; ++j) old[j] = j < valid ? o[j * p.H] : (uint16_t)0;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) v[j] += half_bits_to_float(old[j], ob);
+        for (int j = 0; j < 8; ++j) v[j] += half_bits_to_float(old[j], ob);
     }
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < 8; ++j)
         if (j < valid) o[j * p.H] = (uint16_t)float_to_half_bits(v[j], ob);
 }
 
@@ -443,32 +409,55 @@ __device__ __forceinline__ void repair_outputs(float (&v)[NT], int tok, int vali
     }
 }
 
-// A warp's share of a tile in TMEM: columns (tokens) c0, c0 + 64, ... in pieces
-// of 32, the next piece under way while one is stored.  `drained` runs once
-// the last piece is in registers; repair(v, token) is for values that are no
+// A warp's share of a tile from TMEM to memory: 8 of every 16 columns (tokens),
+// from 8 * half on, the next 8 under way while these are stored.  One short loop
+// on purpose: straight-line code for 32 tokens at a time spent its time fetching
+// instructions (8500 cycles for 128 x 256 outputs).  `drained` runs once
+// the last values are in registers; repair(v, token) is for values that are no
 // finite numbers.
 template <class Drained, class Repair>
-__device__ __forceinline__ void drain(uint32_t taddr, int c0, int ts, int64_t row0, int rows, int64_t n, float bias,
-                                      const Problem& p, uint32_t* stage, bool out_vec, Drained&& drained,
-                                      Repair&& repair) {
-    uint32_t next[32];
-    float v[32];
-    if (c0 >= ts) {
+__device__ __forceinline__ void drain(uint32_t taddr, int half, int ts, int64_t row0, int rows, int64_t n, float bias,
+                                      const Problem& p, uint32_t* turn, bool vec, Drained&& drained, Repair&& repair) {
+    const int lane = threadIdx.x % 32, r = lane / 4, c8 = (lane % 4) * 8;
+    const bool ob = p.out_dt == SGMV_BF16;
+    const bool fast = vec && !p.add;
+    const bool c_ok = n - lane + c8 < p.N;                 // N: a multiple of 8 where vec
+    const uint32_t pick = r & 1 ? 0x7632u : 0x5410u;
+    uint16_t* o = static_cast<uint16_t*>(p.out) + ((row0 + half * 8 + r) * p.H + n - lane + c8);
+    const int64_t step = 16 * p.H;
+    uint32_t next[8];
+    float v[8];
+    int c = half * 8;
+    if (c >= rows) {
         drained();
         return;
     }
-    tmem_ld32(taddr + (uint32_t)c0, next);
-    for (int c = c0;; c += 64) {
+    tmem_ld8(taddr + (uint32_t)c, next);
+#pragma unroll 1
+    for (;; c += 16, o += step) {
         tmem_ld_wait(next);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(next[j]);
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(next[j]);
+        const bool more = c + 16 < rows;
+        if (more) tmem_ld8(taddr + (uint32_t)c + 16, next);
+        else drained();
         repair(v, c);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] += bias;
-        const bool more = c + 64 < ts;
-        if (more) tmem_ld32(taddr + (uint32_t)c + 64, next);
-        else drained();
-        put<32>(v, row0 + c, min(32, rows - c), n, p, stage, out_vec);
+        for (int j = 0; j < 8; ++j) v[j] += bias;
+        if (fast) {
+            // pairs of tokens share a conversion and a word: [pair][32 columns], two buffers in turn
+            uint32_t* s = turn + ((c >> 4) & 1) * 128;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j * 32 + lane] = pack2(v[2 * j], v[2 * j + 1], ob);
+            __syncwarp();
+            const uint4 x = *reinterpret_cast<const uint4*>(s + (r >> 1) * 32 + c8);
+            const uint4 y = *reinterpret_cast<const uint4*>(s + (r >> 1) * 32 + c8 + 4);
+            if (c_ok && c + r < rows)
+                *reinterpret_cast<uint4*>(o) = make_uint4(__byte_perm(x.x, x.y, pick), __byte_perm(x.z, x.w, pick),
+                                                          __byte_perm(y.x, y.y, pick), __byte_perm(y.z, y.w, pick));
+        } else {
+            put8(v, row0 + c, min(8, rows - c), n, p, turn, vec);
+        }
         if (!more) break;
     }
 }
@@ -970,7 +959,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
         }
         const int quad = warp % 4, half = (warp - 2) / 4;
         const int nl = quad * 32 + lane;
-        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + g.off_out + (warp - 2) * g.turn_bytes);
+        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + g.off_out + (warp - 2) * TURN);
         uint32_t b_slot = 0, b_phase = 0;
         const int turn = LORA == LORA_FMA ? lora_turn(nl, lo.R) : 0;
         uint32_t n = 0, reds = 0;   // reds: exchanges in which this CTA owned tokens
@@ -1038,22 +1027,22 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                     float v[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(a[j]) + __uint_as_float(b[j]) + bias;
-                    put<8>(v, (int64_t)t.row0 + j0, min(8, cnt - j0), col, p, stage, g.out_vec);
+                    put8(v, (int64_t)t.row0 + j0, min(8, cnt - j0), col, p, stage, g.out_vec);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0 && id + 2 * ncl < total) mbar_arrive(smem_u32(&acc_empty[acc]));
             } else if (CG == 2 || csize == 1) {
-                drain(taddr, half * 32, t.ts, t.row0, t.rows, col, bias, p, stage, g.out_vec, [&] {
+                drain(taddr, half, t.ts, t.row0, t.rows, col, bias, p, stage, g.out_vec, [&] {
                           tc_fence_before();
                           __syncwarp();
                           if (lane == 0 && id + 2 * ncl < total) {   // somebody waits for it
                               if (CG == 2) mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[acc]), 0));
                               else mbar_arrive(smem_u32(&acc_empty[acc]));
                           }
-                      }, [&](float (&v)[32], int c) {
+                      }, [&](float (&v)[8], int c) {
                           if (LORA != LORA_MMA) return;
-                          repair_outputs<32>(v, c, t.rows - c, t.row0, col, runs, first_run[t.tok], first_run[t.tok + 1], p, lo);
+                          repair_outputs<8>(v, c, t.rows - c, t.row0, col, runs, first_run[t.tok], first_run[t.tok + 1], p, lo);
                       });
             } else {
                 // Partial sums go to the CTA that owns the token, four tokens of a weight row
@@ -1111,7 +1100,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                                               lo);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) v[j] += bias;
-                        put<8>(v, (int64_t)t.row0 + t0 + j0, min(8, cnt - j0), col, p, stage, g.out_vec);
+                        put8(v, (int64_t)t.row0 + t0 + j0, min(8, cnt - j0), col, p, stage, g.out_vec);
                     }
                 }
                 __syncwarp();
@@ -1187,9 +1176,6 @@ struct Want {
     int forced_cg;   // 0: the cost model chooses
 };
 
-// 8 or 32 tokens x 32 halves per epilogue warp.
-inline int turn_bytes(const Shape& sh, const Want& w) { return sh.splits > 1 || w.lora == LORA_FMA ? 8 * 64 : 32 * 64; }
-
 // Shared memory of a form besides the stages and the segment table.
 struct Extra {
     int t, b_bytes, b_slots, out, red;
@@ -1206,7 +1192,7 @@ inline Extra extra_of(const Shape& sh, const Want& w) {
         e.b_slots = B_RING / e.b_bytes;
         e.b_slots = e.b_slots > B_SLOTS ? B_SLOTS : e.b_slots < 2 ? 2 : e.b_slots;
     }
-    e.out = EPI_WARPS * turn_bytes(sh, w);
+    e.out = EPI_WARPS * TURN;
     e.red = sh.splits > 1 ? sh.splits * own * WROWS * 4 : 0;
     return e;
 }
@@ -1298,7 +1284,6 @@ inline bool make_plan(const Problem& p, const Want& w, EncodeTiledFn enc, Plan* 
     g.tmem_cols = 32;
     while (g.tmem_cols < 2 * g.acc_stride + (w.lora == LORA_FMA ? (sh.tn + 31) / 32 * 32 : 0)) g.tmem_cols *= 2;
     g.stage_bytes = stage_bytes(sh);
-    g.turn_bytes = turn_bytes(sh, w);
     const Extra e = extra_of(sh, w);
     g.t_bytes = e.t;
     g.b_slots = e.b_slots;

@@ -29,11 +29,11 @@ namespace wgr {
 using namespace sgmv::tc;
 using grp::BAND;
 using grp::EPI_WARPS;
+using grp::TURN;
 
 constexpr int BT = 64;                     // tokens per stage
 constexpr int HALF = 64 * BT * 2;          // one box of 64 columns: 8 KB
 constexpr int STAGE = 4 * HALF;            // two boxes of X, two of dY
-constexpr int TURN = 32 * 64;              // epilogue: a warp's 32 x 32 halves
 constexpr int FIX_WARP = 2 + EPI_WARPS;
 constexpr int FIX_WARPS = 3;
 constexpr int WARPS = FIX_WARP + FIX_WARPS;
@@ -310,15 +310,13 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
             };
             const int64_t row0 = (int64_t)e * g.rows_per_group + n0;
             if (any) {
-                grp::drain(taddr, half * 32, g.ts, row0, valid, col, 0.f, p, stage, g.out_vec, drained,
-                           [](float (&)[32], int) {});
+                grp::drain(taddr, half, g.ts, row0, valid, col, 0.f, p, stage, g.out_vec, drained, [](float (&)[8], int) {});
             } else {
                 drained();
-                for (int c = half * 32; c < g.ts && !p.add; c += 64) {
-                    float v[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
-                    grp::put<32>(v, row0 + c, min(32, valid - c), col, p, stage, g.out_vec);
+#pragma unroll 1
+                for (int c = half * 8; c < valid && !p.add; c += 16) {
+                    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    grp::put8(v, row0 + c, min(8, valid - c), col, p, stage, g.out_vec);
                 }
             }
         }
