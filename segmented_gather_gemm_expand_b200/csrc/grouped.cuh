@@ -32,7 +32,7 @@
 //   LORA_MMA   as further K steps of the same accumulator, for batches whose
 //          segments are long enough to share an MMA: for every run of rows with
 //          one adapter in a token tile and every 32 ranks, one stage holds B[a]'s
-//          rows (TMA) and one of two buffers t's rows, zero outside the run, which
+//          rows (TMA) and a buffer of t's rows, zero outside the run, which
 //          warps 10 and 11 write up to a tile ahead of the MMAs.  t is fp32 and
 //          enters as the sum of two half-precision parts (hi, and what is left
 //          of it, rounded), three where out is fp32: relative errors of 2^-16
@@ -63,11 +63,13 @@ constexpr int WROWS = 128;              // weight rows per CTA
 constexpr int W_TILE = WROWS * BK * 2;  // 16 KB
 constexpr int EPI_WARPS = 8;
 constexpr int LORA_WARP = 2 + EPI_WARPS;   // first of the warps that write t (LORA_MMA only)
-constexpr int LORA_WARPS = 2;
+// LORA_MMA: warps that write t, each into a buffer of its own.  A single CTA's runs are short: four.
+constexpr int lora_warps(int cg) { return cg == 2 ? 2 : 4; }
+constexpr int MAX_T_BUFS = 4;
 enum LoraMode { LORA_NONE = 0, LORA_FMA = 1, LORA_MMA = 2 };
 constexpr int B_WARP = 2 + EPI_WARPS;      // loads B for LORA_FMA
-constexpr int threads_of(int lora) {
-    return 64 + 32 * EPI_WARPS + (lora == LORA_MMA ? 32 * LORA_WARPS : lora == LORA_FMA ? 32 : 0);
+constexpr int threads_of(int cg, int lora) {
+    return 64 + 32 * EPI_WARPS + (lora == LORA_MMA ? 32 * lora_warps(cg) : lora == LORA_FMA ? 32 : 0);
 }
 constexpr int B_RING = 32 * 1024;          // LORA_FMA: buffered rows of B for each half of the epilogue's warps
 constexpr int B_SLOTS = 8;                 // at most
@@ -542,10 +544,10 @@ __device__ __forceinline__ int x_box(int rows, int room) {
 // LORA_FMA is held to 128 registers a thread (as for 512 threads): a CTA of the
 // shrink before it then fits beside it, and the weights stream while the shrink runs.
 template <int CG, int LORA>
-__global__ void __launch_bounds__(LORA == LORA_FMA ? 512 : threads_of(LORA), 1)
+__global__ void __launch_bounds__(LORA == LORA_FMA ? 512 : threads_of(CG, LORA), 1)
 gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtensorMap wmap,
             const __grid_constant__ CUtensorMap bmap, const Problem p, const Geo g, const Lora lo) {
-    constexpr int THREADS = threads_of(LORA);
+    constexpr int THREADS = threads_of(CG, LORA), LORA_WARPS = lora_warps(CG);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ int s_abort;
@@ -564,9 +566,9 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* red_full = acc_empty + 2;
     uint64_t* red_free = red_full + 1;
-    uint64_t* t_full = red_free + 1;   // LORA_MMA: two buffers of t besides the stages
-    uint64_t* t_empty = t_full + 2;
-    uint64_t* b_full = t_empty + 2;    // LORA_FMA: [half][slot]
+    uint64_t* t_full = red_free + 1;   // LORA_MMA: buffers of t besides the stages
+    uint64_t* t_empty = t_full + MAX_T_BUFS;
+    uint64_t* b_full = t_empty + MAX_T_BUFS;    // LORA_FMA: [half][slot]
     uint64_t* b_empty = b_full + 2 * B_SLOTS;
 
     // The table of runs (LORA_MMA) and its barrier.
@@ -585,6 +587,8 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
             for (int i = 0; i < 2; ++i) {
                 mbar_init(smem_u32(&acc_full[i]), 1);
                 mbar_init(smem_u32(&acc_empty[i]), CG * EPI_WARPS);
+            }
+            for (int i = 0; i < MAX_T_BUFS; ++i) {
                 mbar_init(smem_u32(&t_full[i]), CG);
                 mbar_init(smem_u32(&t_empty[i]), 1);
             }
@@ -776,8 +780,8 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
         }
         __syncwarp();
     } else if (LORA == LORA_MMA && warp >= LORA_WARP) {
-        // ------------------------------------------------------------ t, ahead of the MMAs by up to two low-rank steps
-        // Each warp writes every second step, into its own buffer.
+        // ------------------------------------------------------------ t, ahead of the MMAs by up to a few low-rank steps
+        // The warps take the steps in turn, each with its own buffer.
         if (g.early) grid_dependency_wait();
         const uint32_t buf = (uint32_t)(warp - LORA_WARP);
         uint8_t* dst = smem + g.off_t + buf * g.t_bytes;
@@ -793,7 +797,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                 // the rows of t that this CTA's columns are: all of a single CTA's, a half of a pair's
                 const int32_t base = CG == 2 ? (int32_t)crank * (t.ts / 2) : off, rows = CG == 2 ? t.ts / 2 : cols;
                 for (int32_t r0 = 0; ok && r0 < lo.R; r0 += t_ranks, ++m) {
-                    if ((m & 1) != buf) continue;
+                    if (m % LORA_WARPS != buf) continue;
                     const int ranks = min(t_ranks, lo.R - r0);
                     TRows v;
                     load_t(v, (int64_t)t.row0 + base, 0, run.begin - base, run.end - base, r0, ranks, lo, lane);
@@ -915,8 +919,8 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                                 ok = false;
                                 break;
                             }
-                            const uint32_t buf = m & 1;
-                            if (!mbar_wait(smem_u32(&t_full[buf]), (m >> 1) & 1, abort_flag, DEVERR_TIMEOUT_MMA)) {
+                            const uint32_t buf = m % LORA_WARPS;
+                            if (!mbar_wait(smem_u32(&t_full[buf]), (m / LORA_WARPS) & 1, abort_flag, DEVERR_TIMEOUT_MMA)) {
                                 ok = false;
                                 break;
                             }
@@ -1179,12 +1183,14 @@ struct Want {
 // Shared memory of a form besides the stages and the segment table.
 struct Extra {
     int t, b_bytes, b_slots, out, red;
-    int total() const { return 2 * t + 2 * b_slots * (b_bytes + T_ROW) + out + red; }
+    int t_bufs;
+    int total() const { return t_bufs * t + 2 * b_slots * (b_bytes + T_ROW) + out + red; }
 };
 
 inline Extra extra_of(const Shape& sh, const Want& w) {
     Extra e;
     const int own = ((sh.tn + sh.splits - 1) / sh.splits + 3) & ~3;   // tokens a CTA finishes
+    e.t_bufs = lora_warps(sh.cg);
     e.t = w.lora == LORA_MMA ? (sh.tn / sh.cg < 64 ? 64 : sh.tn / sh.cg) * 128 : 0;
     e.b_bytes = w.lora == LORA_FMA && w.ring ? w.R * WROWS * 2 : 0;
     e.b_slots = 0;
@@ -1244,7 +1250,7 @@ inline Shape choose_shape(const Problem& p, const Want& w) {
                 if (body < late) body = late;
                 // LORA_MMA: a step per run of a segment and 32 ranks, its t written by one warp of two
                 const double runs = (double)ts * w.segs / (rows > 0 ? rows : 1) + 1.0;
-                const double steps = w.lora == LORA_MMA ? runs * ((w.R + 31) / 32) * (cg == 2 ? 1500.0 : 700.0) : 0.0;
+                const double steps = w.lora == LORA_MMA ? runs * ((w.R + 31) / 32) * (cg == 2 ? 1500.0 : 400.0) : 0.0;
                 if (body < steps) body = steps;
                 const double exchange = sp > 1 ? 3000.0 + 32.0 * ts : 0.0;
                 const double path = waves * (body + exchange + 600.0) + 16.0 * own;
@@ -1295,13 +1301,13 @@ inline bool make_plan(const Problem& p, const Want& w, EncodeTiledFn enc, Plan* 
     const int table = w.lora == LORA_MMA ? (g.max_runs + w.segs) * (int)sizeof(Run) + (g.dense_tiles + 1) * 4 : 0;
     for (g.stages = 12; g.stages >= 2; --g.stages) {
         g.off_t = g.stages * g.stage_bytes;                       // t or B (1024-byte aligned: swizzled)
-        g.off_tr = g.off_t + 2 * e.t + 2 * e.b_slots * g.b_bytes;
+        g.off_tr = g.off_t + e.t_bufs * e.t + 2 * e.b_slots * g.b_bytes;
         g.off_out = g.off_tr + 2 * e.b_slots * T_ROW;
         g.off_red = g.off_out + e.out;
         g.off_seg = g.off_red + e.red;
         g.off_runs = (g.off_seg + (dense ? 0 : (int)segs * (int)sizeof(Seg)) + 15) & ~15;
         g.off_bar = (g.off_runs + table + 15) & ~15;
-        out->smem_bytes = g.off_bar + 8 * (2 * g.stages + 11 + 4 * B_SLOTS) + 1024;
+        out->smem_bytes = g.off_bar + 8 * (2 * g.stages + 7 + 2 * MAX_T_BUFS + 4 * B_SLOTS) + 1024;
         if (out->smem_bytes <= SMEM_LIMIT) break;
     }
     if (g.stages < 2) return false;
@@ -1361,7 +1367,7 @@ inline bool cluster_capacity(int device, int sm_count, int (&out)[MAX_SPLITS]) {
             attr[0].val.clusterDim.z = 1;
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3((unsigned)(sm_count / size * size));
-            cfg.blockDim = dim3(threads_of(LORA_NONE));
+            cfg.blockDim = dim3(threads_of(1, LORA_NONE));
             cfg.dynamicSmemBytes = SMEM_LIMIT;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
@@ -1411,7 +1417,7 @@ int launch_kernel(const Plan& pl, const CUtensorMap& bm, const Problem& p, const
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)pl.grid);
-    cfg.blockDim = dim3(threads_of(LORA));
+    cfg.blockDim = dim3(threads_of(CG, LORA));
     cfg.dynamicSmemBytes = (size_t)pl.smem_bytes;
     cfg.stream = stream;
     cfg.attrs = attr;

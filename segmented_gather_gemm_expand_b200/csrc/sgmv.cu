@@ -456,8 +456,11 @@ namespace {
 // Rows up to which a shared projection's low-rank input is computed row by row
 // (an adapter per row) instead of in 128-row blocks of one adapter.
 constexpr int64_t kRowShrinkRows = 256;
-// Rows per segment from which the low-rank part runs on the tensor cores.
-constexpr int64_t kMmaRunRows = 16;
+// Rows per segment from which the low-rank part runs on the tensor cores: a step
+// per run against a copy of B per token.  Measured (us, on the CUDA cores
+// against the tensor cores): 240 rows in 24 segments 29.8, 32.5; 946 in 232
+// 43.7, 30.9; 512 in 256 85, 103.
+constexpr int64_t mma_run_rows(int64_t rows) { return rows > kRowShrinkRows ? 4 : 16; }
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
@@ -699,7 +702,7 @@ int choose_lora(LoraCall* c, const DeviceInfo& dev, int forced, char* ws, size_t
     }
     const bool tc = forced != SGMV_VARIANT_SIMT && dev.cc_major == 10;
     // K steps pay from a few rows per segment on: a run costs an MMA over its whole token tile
-    const bool long_runs = c->rows >= kMmaRunRows * c->shrink.batches;
+    const bool long_runs = c->rows >= mma_run_rows(c->rows) * c->shrink.batches;
     const bool mma = tc && c->low_rank && long_runs && c->shrink.batches <= grp::SEG_CAP &&
                      grp::encode_b(c->lo, c->base.N, c->shrink.lora_num, tc::encode_fn(), &pl->bm);
     pl->lora = !c->low_rank ? grp::LORA_NONE : mma ? grp::LORA_MMA : grp::LORA_FMA;
