@@ -1248,9 +1248,9 @@ inline Shape choose_shape(const Problem& p, const Want& w) {
                 double body = load > mma ? load : mma;
                 if (body < alu) body = alu;
                 if (body < late) body = late;
-                // LORA_MMA: a step per run of a segment and 32 ranks, its t written by one warp of two
+                // LORA_MMA: a step per run of a segment and 32 ranks, its t written by a warp of its own
                 const double runs = (double)ts * w.segs / (rows > 0 ? rows : 1) + 1.0;
-                const double steps = w.lora == LORA_MMA ? runs * ((w.R + 31) / 32) * (cg == 2 ? 1500.0 : 400.0) : 0.0;
+                const double steps = w.lora == LORA_MMA ? runs * ((w.R + 31) / 32) * (cg == 2 ? 2500.0 : 500.0) : 0.0;
                 if (body < steps) body = steps;
                 const double exchange = sp > 1 ? 3000.0 + 32.0 * ts : 0.0;
                 const double path = waves * (body + exchange + 600.0) + 16.0 * own;
