@@ -11,11 +11,13 @@
 // the wide side of the MMA.  A segment of L rows is cut into ceil(L / tn)
 // token tiles of equal size (rounded up), not into full tiles and a rest.
 //
-// Roles (320 threads per CTA): warp 0 loads with TMA (x rows in boxes of 16 to
-// 128 rows, weights 128 rows, 64 columns of K per stage, 128-byte swizzle),
-// warp 1 issues the MMAs into one of two TMEM accumulators, warps 2-9 read the
-// other accumulator back (lane = weight row, column = token), finish the sums
-// and store; 32 lanes store 32 neighbouring columns of a row.
+// Roles (320 threads per CTA, more with adapters): warp 0 loads with TMA (x rows
+// in boxes of 16 to 128 rows, weights 128 rows, 64 columns of K per stage,
+// 128-byte swizzle), warp 1 issues the MMAs into one of two TMEM accumulators,
+// warps 2-9 read the other accumulator back (lane = weight row, column =
+// token), finish the sums and store.  Producer and MMA roles are one elected
+// thread each: run by a warp with a lane's branch inside, the MMAs' operands
+// were rebuilt for every instruction (1120 TFLOP/s against 1390).
 // Rows of a load past the segment's end are other segments' rows or zeros:
 // they only reach accumulator columns that are not stored.
 //
@@ -23,24 +25,34 @@
 //   pair   CTA pairs (cta_group::2), 256 weight rows x up to 256 tokens.  Each
 //          CTA loads its 128 weight rows and half of the tokens, so a stage
 //          brings 64 MMA columns per KB instead of 43: compute-bound shapes.
+//          16384 ragged rows over 8 experts, 4096 -> 11008, bf16: 1023 us in a
+//          single launch (1445 TFLOP/s), the tensor pipe 95 % busy at the 1.34 GHz
+//          that the power limit leaves; 1200 us back to back.  Bound: power.
 //   single one CTA, 128 weight rows x up to 128 tokens; with few tiles, the
 //          CTAs of a cluster share one tile by cutting K, push their partial
 //          sums into each other's shared memory (every CTA owns a part of the
 //          tokens) and add them in rank order (deterministic): decode shapes.
+//          96 rows over 64 experts, 2048 -> 1408: 59 us, 6.3 TB/s of weights.
+//          Bound: memory, then the latency of the chain for the smallest calls.
 //
 // The low-rank part of a shared projection comes in one of two ways (LoraMode):
 //   LORA_MMA   as further K steps of the same accumulator, for batches whose
 //          segments are long enough to share an MMA: for every run of rows with
 //          one adapter in a token tile and every 32 ranks, one stage holds B[a]'s
 //          rows (TMA) and a buffer of t's rows, zero outside the run, which
-//          warps 10 and 11 write up to a tile ahead of the MMAs.  t is fp32 and
+//          warps of their own write some steps ahead of the MMAs.  t is fp32 and
 //          enters as the sum of two half-precision parts (hi, and what is left
 //          of it, rounded), three where out is fp32: relative errors of 2^-16
-//          (2^-24) against out's own rounding of 2^-9 (2^-24).
+//          (2^-24) against out's own rounding of 2^-9 (2^-24).  8764 rows of 16
+//          prompts, 4096 -> 12288, rank 16: 1483 us with FMAs in the epilogue, 710
+//          with these steps (the kernel alone 589, the tensor pipe 90 % busy; power).
 //   LORA_FMA   on the CUDA cores in fp32, by the epilogue's warps while the K loop
-//          runs (they keep it in shared memory until the sums are there): single
-//          tokens with an adapter each, or a B that TMA cannot read.  Warp 10 loads
-//          each token's 128 rows of B and its row of t into a ring.
+//          runs (they keep it in TMEM until the sums are there): single tokens
+//          with an adapter each, or a B that TMA cannot read.  Warp 10 copies
+//          each token's 128 rows of B and its row of t into a ring.  256 tokens
+//          of 256 adapters of rank 32, 5120 -> 5120: 56 us with the shrink before it
+//          (169 with B read lane by lane after the sums); 37 of them here,
+//          3.5 TB/s.  Bound: the bytes of W and B under way per SM.
 //
 // Every wait is bounded and reports a timeout through the device error word.
 #pragma once
@@ -220,7 +232,7 @@ __device__ __forceinline__ void build_runs(const Geo& g, const Lora& lo, Run* ru
 // d[j] = sum_k t[row + j, k] * B[adapter of row + j][n, k] for j < valid, in
 // fp32, 16 ranks at a time.  The B pieces of all eight tokens are requested
 // before the first is used: decode batches have an adapter per token, and one
-// after the other their latencies add up (48 tokens: 51 us against 26).
+// after the other their latencies add up (48 tokens took 51 us so).
 __device__ __forceinline__ void lora_delta(float (&d)[8], int64_t row, int valid, int64_t n, bool n_ok, const Lora& lo,
                                            bool bf16) {
     int a[8];

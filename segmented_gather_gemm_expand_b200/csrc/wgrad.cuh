@@ -16,9 +16,15 @@
 //
 // Several segments of one index add up in segment order in one accumulator.
 // Indexes without rows get zeros (or keep dW in add mode).  The tiles of long and
-// short indexes take turns (longest, shortest, second longest, ...): the MMAs
-// of a long one then hide the stores of short ones, whose tiles are all
-// epilogue, and the deal ends with middling ones.
+// short indexes take turns (longest, shortest, second longest, ...), so that the
+// stores of short ones, whose tiles are all epilogue, meet the MMAs of long ones.
+//
+// Measured: 16384 ragged rows of 8 experts, 4096 x 11008, bf16: 1200-1250 us
+// back to back (1200 TFLOP/s, the power limit).  8192 rows of 16 experts, 2048 x
+// 2816: 117-135 us by box, where the flops alone would take 57: 89 us with no
+// epilogue at all (8 K steps per tile on average; the longest cluster has 20 %
+// more than the mean), 28 more for the stores, which share the shared memory's
+// bandwidth with the MMAs' operands and TMA's writes.
 #pragma once
 
 #include "grouped.cuh"
