@@ -336,13 +336,19 @@ SGMV_API int bgmv_plan(const sgmv_tensor* inputs, const sgmv_tensor* lora_b, con
  *             least the size that sgmv_lora_linear_plan reports (the rows'
  *             adapters and t: about T * (R + 1) * 4 bytes), else
  *             SGMV_ERR_WORKSPACE; with the preferred size the sums of t may be
- *             split over more CTAs.  NULL will do for a call without adapters
+ *             split over more CTAs, and a lora_b whose rows are not contiguous
+ *             on 16-byte boundaries is laid out anew for segments of some
+ *             length.  NULL will do for a call without adapters
  *             (batches, lora_num or R zero).  Calls that run at the same time
  *             need separate workspaces, and so do captured graphs that may.
  *
  * Statuses beside the common ones: SGMV_ERR_RANK_MISMATCH (K or R differ
  * between tensors), SGMV_ERR_SLICE_SIZE (lora_b's N), SGMV_ERR_SHAPE (bias
  * length, lora_a's and lora_b's lora_num), SGMV_ERR_OUT_WIDTH.
+ *
+ * The input gradient, dX = dY W + (dY B[a]) A[a], is this product with
+ * transposed views: weight (K, N), lora_a (lora_num, R, N) a view of B, lora_b
+ * (lora_num, K, R) a view of A.
  *
  * The tensor-core path (SGMV_VARIANT_TC) needs inputs and weight in one half
  * dtype, K contiguous in inputs, K or N contiguous in weight, and their rows on

@@ -46,9 +46,12 @@
 //          (2^-24) against out's own rounding of 2^-9 (2^-24).  8764 rows of 16
 //          prompts, 4096 -> 12288, rank 16: 1483 us with FMAs in the epilogue, 710
 //          with these steps (the kernel alone 589, the tensor pipe 90 % busy; power).
+//          A B that TMA cannot read (a transposed view: the input gradient; ranks
+//          that leave rows off the 16-byte boundaries) is laid out anew, per
+//          segment, where the workspace has room.
 //   LORA_FMA   on the CUDA cores in fp32, by the epilogue's warps while the K loop
 //          runs (they keep it in TMEM until the sums are there): single tokens
-//          with an adapter each, or a B that TMA cannot read.  Warp 10 copies
+//          with an adapter each, or a B that TMA cannot read (without room).  Warp 10 copies
 //          each token's 128 rows of B and its row of t into a ring.  256 tokens
 //          of 256 adapters of rank 32, 5120 -> 5120: 56 us with the shrink before it
 //          (169 with B read lane by lane after the sums); 37 of them here,
@@ -123,7 +126,7 @@ struct XMaps {
 
 // Rows of one token tile that belong to one segment with an adapter.
 struct Run {
-    int32_t adapter, begin, end;   // rows [begin, end), counted from the tile's first
+    int32_t adapter, begin, end;   // B's matrix; rows [begin, end), counted from the tile's first
 };
 
 // The low-rank part and the bias of a shared projection.
@@ -138,6 +141,7 @@ struct Lora {
     int32_t R;
     int32_t parts;               // LORA_MMA: half-precision parts of t (2 or 3)
     int32_t b_vec;               // rows of B can be read as 16-byte pieces
+    int32_t by_seg;              // LORA_MMA: b holds one matrix per segment, not per adapter
     const void* bias;            // (N) in the weights' dtype, or null
     int64_t bias_s;
 };
@@ -188,7 +192,7 @@ __device__ __forceinline__ void build_runs(const Geo& g, const Lora& lo, Run* ru
         const int64_t start = load_meta(lo.start, b), len = load_meta(lo.len, b), a = load_meta(lo.idx, b);
         const int64_t end = len > g.dense_rows - start ? (int64_t)g.dense_rows : start + len;
         const bool ok = a >= 0 && a < lo.adapters && start >= 0 && start < g.dense_rows && len > 0;
-        segs[b] = ok ? Run{(int32_t)a, (int32_t)start, (int32_t)end} : Run{-1, 0, 0};
+        segs[b] = ok ? Run{lo.by_seg ? b : (int32_t)a, (int32_t)start, (int32_t)end} : Run{-1, 0, 0};
     }
     bar_sync(2, THREADS);
     for (int pass = 0; pass < 2; ++pass) {
@@ -508,9 +512,18 @@ __device__ __forceinline__ void load_t(TRows& x, int64_t row0, int i0, int begin
     for (int i = 0; i < 2; ++i) {
         const int k0 = i0 + lane + 32 * i;
         const bool in = k0 >= begin && k0 < end;
-        const float4* src = reinterpret_cast<const float4*>(lo.t + (row0 + k0) * lo.R + r);   // R, r: multiples of 8
+        const float* src = lo.t + (row0 + k0) * lo.R + r;
+        if (lo.R % 4 == 0) {   // r: a multiple of 16
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x.q[i][k] = in && 4 * k < ranks ? src[k] : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < 8; ++k)
+                x.q[i][k] = in && 4 * k < ranks ? reinterpret_cast<const float4*>(src)[k] : make_float4(0.f, 0.f, 0.f, 0.f);
+        } else {
+            const int n = in ? ranks : 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x.q[i][k] = make_float4(4 * k < n ? src[4 * k] : 0.f, 4 * k + 1 < n ? src[4 * k + 1] : 0.f,
+                                        4 * k + 2 < n ? src[4 * k + 2] : 0.f, 4 * k + 3 < n ? src[4 * k + 3] : 0.f);
+        }
     }
 }
 
@@ -1395,13 +1408,49 @@ inline bool cluster_capacity(int device, int sm_count, int (&out)[MAX_SPLITS]) {
     return true;
 }
 
-// Plans of recent calls, keyed by every field of the problem, the wishes and the device.
+// The driver's call that points a tensor map at another address; sizes, strides
+// and boxes stay.
+typedef CUresult (*ReplaceAddressFn)(CUtensorMap*, void*);
+inline ReplaceAddressFn replace_address_fn() {
+    static ReplaceAddressFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapReplaceAddress", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<ReplaceAddressFn>(ptr);
+    });
+    return fn;
+}
+
+// The problem as a plan's key: sizes, strides, types and alignments; of the
+// addresses only what is left over 16 bytes.
+inline void keyed_problem(const Problem& p, Problem* key) {
+    const auto rest = [](const void* a) { return reinterpret_cast<void*>(reinterpret_cast<uintptr_t>(a) & 15); };
+    std::memcpy(key, &p, sizeof(Problem));
+    key->x = rest(p.x);
+    key->w = rest(p.w);
+    key->out = rest(p.out);
+    key->start.ptr = key->len.ptr = key->idx.ptr = nullptr;
+}
+
+// Points a plan's maps at this call's x and weights.
+inline bool point(CUtensorMap* x, int n, CUtensorMap* w, const Problem& p) {
+    const ReplaceAddressFn put = replace_address_fn();
+    if (!put) return false;
+    for (int i = 0; i < n; ++i)
+        if (put(&x[i], const_cast<void*>(p.x)) != CUDA_SUCCESS) return false;
+    return put(w, const_cast<void*>(p.w)) == CUDA_SUCCESS;
+}
+
+// Plans of recent calls, keyed by the problem but for its addresses, the wishes and the device.
 inline bool cached_plan(const Problem& p, bool dense, bool early, int lora, int R, bool ring, int segs, int sm_count, int forced_cg,
                         EncodeTiledFn enc, Plan* out) {
     static PlanCache<PlanKey, Plan> cache;
     PlanKey key;
     std::memset(&key, 0, sizeof(key));
-    std::memcpy(&key.p, &p, sizeof(Problem));
+    keyed_problem(p, &key.p);
     key.w.dense = dense;
     key.w.early = early;
     key.w.lora = lora;
@@ -1411,7 +1460,8 @@ inline bool cached_plan(const Problem& p, bool dense, bool early, int lora, int 
     key.w.sm_count = sm_count;
     key.w.forced_cg = forced_cg;
     if (cudaGetDevice(&key.device) != cudaSuccess || !cluster_capacity(key.device, sm_count, key.w.clusters)) return false;
-    return cache.get(key, out, [&](Plan* pl) { return make_plan(p, key.w, enc, pl); });
+    return cache.get(key, out, [&](Plan* pl) { return make_plan(p, key.w, enc, pl); }) &&
+           point(out->xm.m, NUM_XMAPS, &out->wm, p);
 }
 
 template <int CG, int LORA>
@@ -1447,7 +1497,7 @@ inline bool ring_ok(const Lora& lo) { return lo.b_vec && lo.R % 8 == 0 && lo.R <
 
 // Tensor map of lora_b (adapters, N, R) for LORA_MMA; false where TMA cannot read it.
 inline bool encode_b(const Lora& lo, int64_t N, int64_t adapters, EncodeTiledFn enc, CUtensorMap* out) {
-    if (!enc || !lo.b_vec || lo.R % 8 || lo.b_ns < lo.R || adapters >= (int64_t(1) << 31)) return false;
+    if (!enc || !lo.b_vec || lo.b_ns < lo.R || adapters >= (int64_t(1) << 31)) return false;
     if (lo.b_ns >= (int64_t(1) << 38) || lo.b_as >= (int64_t(1) << 38)) return false;
     if (adapters > 1 && lo.b_as < (N - 1) * lo.b_ns + lo.R) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)lo.R, (cuuint64_t)N, (cuuint64_t)adapters};

@@ -129,6 +129,27 @@ inline bool row_shrink_vec(const Problem& p) {
            (reinterpret_cast<uintptr_t>(p.x) & 15) == 0 && (reinterpret_cast<uintptr_t>(p.w) & 15) == 0;
 }
 
+// B of every segment's adapter with its ranks contiguous, rows padded to whole
+// 16-byte pieces: out[b][n][j], j < pitch.  A thread takes a row of B, eight
+// ranks at a time; neighbouring threads take neighbouring rows, which is how a
+// transposed view lies in memory.  Segments without rows or adapter are left out.
+constexpr int PACK_THREADS = 256;
+__global__ void __launch_bounds__(PACK_THREADS) pack_b_kernel(Problem p, grp::Lora lo, uint16_t* out, int64_t N, int32_t pitch) {
+    tc::grid_dependency_wait();
+    tc::grid_dependents_launch();
+    const Segment s = load_segment(p, blockIdx.y);
+    const int64_t n = (int64_t)blockIdx.x * PACK_THREADS + threadIdx.x;
+    if (s.rows <= 0 || n >= N) return;
+    const uint16_t* b = static_cast<const uint16_t*>(lo.b) + (int64_t)s.adapter * lo.b_as + n * lo.b_ns;
+    uint16_t* o = out + ((int64_t)blockIdx.y * N + n) * pitch;
+    for (int32_t j0 = 0; j0 < pitch; j0 += 8) {
+        uint32_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j0 + j < lo.R ? b[(j0 + j) * lo.b_ks] : 0u;
+        *reinterpret_cast<uint4*>(o + j0) = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
+}
+
 // Generic form of the whole projection on the CUDA cores: any strides, rank,
 // alignment and dtypes.  Tiling as in the generic expand: a CTA of 256 threads
 // owns 128 columns and 32 rows at a time, x and W staged as fp32 in chunks of
@@ -211,6 +232,12 @@ inline int launch_row_shrink(const Problem& p, float* t, int32_t* row_adapter, i
     return row_shrink_vec(p)
                ? launch_dependent(row_shrink_kernel<true>, grid, SHRINK_THREADS, stream, p, t, row_adapter, rows)
                : launch_dependent(row_shrink_kernel<false>, grid, SHRINK_THREADS, stream, p, t, row_adapter, rows);
+}
+
+inline int launch_pack_b(const Problem& p, const grp::Lora& lo, void* out, int64_t N, int32_t pitch, cudaStream_t stream) {
+    const int64_t gx = (N + PACK_THREADS - 1) / PACK_THREADS;
+    return launch_dependent(pack_b_kernel, dim3((unsigned)gx, (unsigned)p.batches), PACK_THREADS, stream, p, lo,
+                            static_cast<uint16_t*>(out), N, pitch);
 }
 
 inline int launch_lora_simt(const Problem& p, const grp::Lora& lo, int64_t rows, cudaStream_t stream) {

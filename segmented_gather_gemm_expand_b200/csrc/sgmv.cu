@@ -687,6 +687,8 @@ struct LoraPlan {
     grp::Plan base;
     int lora;                                        // grp::LoraMode of the tensor-core form
     bool mma;                                        // that is LORA_MMA
+    grp::Lora given;                                 // pack: lora_b as the caller has it
+    bool pack;                                       // lay lora_b out anew in the workspace, per segment
     CUtensorMap bm;
     enum { NONE, BY_ROW, BLOCKS, PRODUCT } shrink;   // how t is computed
     int splits;                                      // BLOCKS: parts of K
@@ -703,8 +705,23 @@ int choose_lora(LoraCall* c, const DeviceInfo& dev, int forced, char* ws, size_t
     const bool tc = forced != SGMV_VARIANT_SIMT && dev.cc_major == 10;
     // K steps pay from a few rows per segment on: a run costs an MMA over its whole token tile
     const bool long_runs = c->rows >= mma_run_rows(c->rows) * c->shrink.batches;
-    const bool mma = tc && c->low_rank && long_runs && c->shrink.batches <= grp::SEG_CAP &&
-                     grp::encode_b(c->lo, c->base.N, c->shrink.lora_num, tc::encode_fn(), &pl->bm);
+    bool mma = tc && c->low_rank && long_runs && c->shrink.batches <= grp::SEG_CAP;
+    grp::Lora packed = c->lo;
+    int64_t pack_bytes = 0;
+    if (mma && !grp::encode_b(c->lo, c->base.N, c->shrink.lora_num, tc::encode_fn(), &pl->bm)) {
+        // A copy per segment costs less than FMAs for every row.  4096 -> 4096, a transposed B of rank 16:
+        // 8192 rows of 16 segments 1493 -> 202 us, 1024 rows of 256 segments 325 -> 138; rank 4, 8192 rows
+        // 483 -> 206, but 1024 rows of 256 segments 119 -> 128.
+        packed.by_seg = 1;
+        packed.b = ws + c->off_part;
+        packed.b_ks = 1;
+        packed.b_ns = (c->lo.R + 7) / 8 * 8;
+        packed.b_as = c->base.N * packed.b_ns;
+        packed.b_vec = 1;
+        pack_bytes = align256(c->shrink.batches * packed.b_as * 2);
+        mma = packed.b_as < (int64_t(1) << 31) && ws_bytes >= (size_t)(c->off_part + pack_bytes) &&
+              grp::encode_b(packed, c->base.N, c->shrink.batches, tc::encode_fn(), &pl->bm);
+    }
     pl->lora = !c->low_rank ? grp::LORA_NONE : mma ? grp::LORA_MMA : grp::LORA_FMA;
     const bool tc_ok = tc && grp::cached_plan(c->base, true, c->low_rank, pl->lora, c->lo.R, grp::ring_ok(c->lo),
                                               (int)c->shrink.batches, dev.sm_count,
@@ -712,6 +729,12 @@ int choose_lora(LoraCall* c, const DeviceInfo& dev, int forced, char* ws, size_t
     pl->variant = large_variant(tc_ok, forced);
     if (pl->variant < 0) return pl->variant;
     pl->mma = mma && tc_ok;
+    pl->pack = pl->mma && pack_bytes > 0;
+    pl->given = c->lo;
+    if (pl->pack) {
+        c->lo = packed;
+        c->off_part += pack_bytes;
+    }
     if (pl->mma) {
         c->lo.start = c->shrink.start;
         c->lo.len = c->shrink.len;
@@ -742,6 +765,9 @@ int run_lora(const LoraCall& c, const DeviceInfo& dev, const LoraPlan& pl, char*
     int32_t* rows = reinterpret_cast<int32_t*>(ws);
     float* t = reinterpret_cast<float*>(ws + c.off_t);
     const Call shrink{c.shrink, 0, false};
+    // first: a projection that starts early waits for the shrink alone
+    if (pl.pack && (rc = lora::launch_pack_b(c.shrink, pl.given, const_cast<void*>(c.lo.b), c.base.N, (int32_t)c.lo.b_ns, st)))
+        return rc;
     // row_shrink_kernel finds the rows' adapters by itself, the projection's K steps read the segments
     if (!pl.mma && (pl.shrink == LoraPlan::BLOCKS || pl.shrink == LoraPlan::PRODUCT))
         if ((rc = lora::launch_row_adapter(c.shrink, rows, c.rows, st))) return rc;
@@ -878,12 +904,13 @@ int sgmv_lora_linear_plan(const sgmv_tensor* inputs, const sgmv_tensor* weight, 
     DeviceInfo dev;
     if ((rc = device_info(&dev))) return rc;
     LoraPlan pl;
+    const size_t least = (size_t)c.off_part;   // choose_lora may move it
     // an aligned stand-in for the workspace's address: only sizes matter here
     if ((rc = choose_lora(&c, dev, g_forced_variant.load(), reinterpret_cast<char*>(uintptr_t(256)), ~size_t(0), &pl)))
         return rc;
     *variant = pl.variant;
     if (c.low_rank) {
-        *workspace_bytes = (size_t)c.off_part;
+        *workspace_bytes = least;
         *preferred_workspace_bytes =
             (size_t)(c.off_part + (pl.shrink == LoraPlan::BLOCKS ? shr::workspace_bytes_for(c.shrink, pl.splits) : 0));
     }

@@ -442,13 +442,14 @@ inline bool cached_plan(const Problem& p, int64_t y_cs, int64_t out_gs, int64_t 
     static PlanCache<PlanKey, Plan> cache;
     PlanKey key;
     std::memset(&key, 0, sizeof(key));
-    std::memcpy(&key.p, &p, sizeof(Problem));
+    grp::keyed_problem(p, &key.p);
     key.y_cs = y_cs;
     key.out_gs = out_gs;
     key.out_cs = out_cs;
     key.sm_count = sm_count;
     if (cudaGetDevice(&key.device) != cudaSuccess) return false;
-    return cache.get(key, out, [&](Plan* pl) { return make_plan(p, y_cs, out_gs, out_cs, sm_count, enc, pl); });
+    return cache.get(key, out, [&](Plan* pl) { return make_plan(p, y_cs, out_gs, out_cs, sm_count, enc, pl); }) &&
+           grp::point(&out->xm, 1, &out->ym, p);
 }
 
 inline int launch(const Plan& pl, const Problem& p, cudaStream_t stream) {

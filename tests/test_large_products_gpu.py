@@ -626,3 +626,52 @@ def test_values_that_are_no_numbers_in_shared_inputs():
     cols = torch.arange(264) != 7
     assert torch.isnan(out[::3]).all() and not torch.isfinite(out[:, 7]).any()
     assert torch.equal(out[rows][:, cols], ref[rows][:, cols])
+
+
+# ---------------------------------------------------------------- backward pass of a projection with adapters
+
+@pytest.mark.parametrize("lens", [[90, 40, 0, 33, 130], [1] * 7])
+@pytest.mark.parametrize("R,K,N", [(16, 264, 136), (4, 136, 200), (13, 128, 96)])
+def test_lora_backward_from_views(lens, R, K, N):
+    """dX from transposed views, dA and dB from the weight gradient, against the formulas."""
+    g = gen(31 + R)
+    A, n = 3, len(lens)
+    m, T = meta(lens, [(2 * i) % (A + 1) - 1 for i in range(n)])
+    x, w, dy = ints(g, (T, K), "bf16", 1), ints(g, (N, K), "bf16", 1), ints(g, (T, N), "bf16", 1)
+    a, b = ints(g, (A, R, K), "bf16", 1), ints(g, (A, N, R), "bf16", 1)
+    wt, at, bt = w.t(), a.transpose(1, 2), b.transpose(1, 2)
+    for dt in ("bf16", "f32"):
+        for spare in (True, False):
+            dx = torch.full((T, K), float("nan"), device="cuda", dtype=DT[dt])
+            run_lora(dy, wt, bt, at, dx, m, n, max(lens), spare=spare)
+            assert torch.equal(dx, rounded(lora_ref(dy, wt, bt, at, m, None, T), dt))
+    da, db = torch.zeros(A, R, K, device="cuda"), torch.zeros(A, N, R, device="cuda")
+    t, s = torch.zeros(T, R, device="cuda"), torch.zeros(T, R, device="cuda")   # x A^T, dY B
+    sg.sgmv_shrink(x, a, t, *m, n, max(lens))
+    sg.sgmv_shrink(dy, bt, s, *m, n, max(lens))
+    sg.sgmv_grouped_wgrad(s, x, da, *m, n, max(lens))
+    sg.sgmv_grouped_wgrad(dy, t, db, *m, n, max(lens))
+    ra, rb = torch.zeros(A, R, K, device="cuda", dtype=torch.float64), torch.zeros(A, N, R, device="cuda", dtype=torch.float64)
+    for lo, hi, i in rows_of(m, T, A):
+        xd, yd = x[lo:hi].double(), dy[lo:hi].double()
+        ra[i] += (yd @ b[i].double()).T @ xd
+        rb[i] += yd.T @ (xd @ a[i].double().T)
+    assert torch.equal(da, ra.float()) and torch.equal(db, rb.float())
+
+
+def test_plans_follow_the_tensors():
+    """Calls of the same shapes on other tensors, at other alignments too."""
+    g = gen(41)
+    m, T = meta([70, 1, 60], [0, 1, 0])
+    K, N = 128, 256
+    for shift in (0, 0, 8, 1, 0):
+        x, w, dw, out = ints(g, (T * K + 8,), "bf16", 1)[shift:shift + T * K].view(T, K), ints(g, (2, N, K), "bf16", 1), torch.zeros(
+            2, N, K, device="cuda"), torch.zeros(T, N, device="cuda", dtype=torch.bfloat16)
+        sg.sgmv_grouped_gemm(x, w, out, *m, 3, 70)
+        assert torch.equal(out, rounded(grouped_ref(x, w, torch.zeros_like(out), m, False), "bf16"))
+        dy = ints(g, (T, N), "bf16", 1)
+        sg.sgmv_grouped_wgrad(dy, x, dw, *m, 3, 70)
+        ref = torch.zeros(2, N, K, device="cuda", dtype=torch.float64)
+        for lo, hi, e in rows_of(m, T, 2):
+            ref[e] += dy[lo:hi].double().T @ x[lo:hi].double()
+        assert torch.equal(dw, ref.float())
