@@ -11,20 +11,31 @@ namespace sgmv {
 namespace lora {
 
 // Adapter of `row` (-1: none), found by the whole block; segments do not overlap.
-__device__ __forceinline__ int32_t block_adapter(const Problem& p, int64_t row, int32_t* s_adapter) {
+__device__ __forceinline__ int32_t block_adapter(const Problem& p, int64_t row, int64_t rows, int32_t* s_adapter) {
     // a decode batch has one token per segment, in order: look there first
     if (row < p.batches) {
         const Segment s = load_segment(p, row);
         if (s.rows > 0 && row >= s.row0 && row < s.row0 + s.rows) return (int32_t)s.adapter;
     }
+    // else around the place that segments of one length would give it, then everywhere
     if (threadIdx.x == 0) *s_adapter = -1;
     __syncthreads();
-    for (int64_t b = threadIdx.x; b < p.batches; b += blockDim.x) {
-        const Segment s = load_segment(p, b);
-        if (s.rows > 0 && row >= s.row0 && row < s.row0 + s.rows) *s_adapter = (int32_t)s.adapter;
+    int64_t b = threadIdx.x;
+    if (p.batches > blockDim.x) b += row * p.batches / rows - (int64_t)(blockDim.x / 2);
+    if (b < 0) b += p.batches;
+    for (int64_t left = p.batches; left > 0; left -= blockDim.x, b += blockDim.x) {
+        if (b >= p.batches) b -= p.batches;
+        bool found = false;
+        if (threadIdx.x < left) {
+            const Segment s = load_segment(p, b);
+            found = s.rows > 0 && row >= s.row0 && row < s.row0 + s.rows;
+            if (found) *s_adapter = (int32_t)s.adapter;
+        }
+        if (__syncthreads_or(found)) break;
     }
-    __syncthreads();
-    return *s_adapter;
+    const int32_t a = *s_adapter;
+    __syncthreads();   // read by all before the next row's search
+    return a;
 }
 
 // The adapter of every row: one thread per row scans the segments, which the
@@ -67,7 +78,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS) row_shrink_kernel(Problem p, f
     const int64_t j0 = (int64_t)blockIdx.x * SHRINK_RANKS;
     const bool bf16 = p.w_dt == SGMV_BF16;
     for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
-        const int32_t a = block_adapter(p, row, &s_adapter);
+        const int32_t a = block_adapter(p, row, rows, &s_adapter);
         if (blockIdx.x == 0 && tid == 0) row_adapter[row] = a;
         if (a >= 0) {
             float acc[SHRINK_RANKS] = {0.f, 0.f, 0.f, 0.f};

@@ -453,14 +453,18 @@ float* static_scratch(int* rc) {
 
 namespace {
 
-// Rows up to which a shared projection's low-rank input is computed row by row
-// (an adapter per row) instead of in 128-row blocks of one adapter.
-constexpr int64_t kRowShrinkRows = 256;
+// Whether a shared projection's low-rank input is computed row by row, every row
+// reading its adapter's A, or in blocks of up to 128 rows of a segment: the one
+// costs by rows and ranks, the other by segments.  Measured (us, 4096 columns,
+// row by row against blocks): rank 16, 512 single rows 21, 98; 4096 single rows
+// 90, 635; 512 in pairs 23, 57; 2048 in fours 74, 90; 2048 in eights 62, 52;
+// rank 64, 512 single rows 51, 102; 512 in fours 60, 37; 300 in 16s 33, 21.
+bool row_shrink_pays(int64_t rows, int64_t segs, int64_t ranks) { return rows * ranks <= 4096 + 100 * segs; }
 // Rows per segment from which the low-rank part runs on the tensor cores: a step
 // per run against a copy of B per token.  Measured (us, on the CUDA cores
 // against the tensor cores): 240 rows in 24 segments 29.8, 32.5; 946 in 232
 // 43.7, 30.9; 512 in 256 85, 103.
-constexpr int64_t mma_run_rows(int64_t rows) { return rows > kRowShrinkRows ? 4 : 16; }
+constexpr int64_t mma_run_rows(int64_t rows) { return rows > 256 ? 4 : 16; }
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
@@ -745,7 +749,7 @@ int choose_lora(LoraCall* c, const DeviceInfo& dev, int forced, char* ws, size_t
     }
     pl->shrink = c->low_rank ? LoraPlan::BY_ROW : LoraPlan::NONE;
     pl->splits = 1;
-    if (c->low_rank && tc && c->rows > kRowShrinkRows) {
+    if (c->low_rank && tc && !row_shrink_pays(c->rows, c->shrink.batches, c->lo.R)) {
         if (shr::supports(c->shrink) && c->shrink.batches <= shr::SEG_CAP) {
             pl->shrink = LoraPlan::BLOCKS;
             int sp = shr::preferred_splits(c->shrink, dev.sm_count);

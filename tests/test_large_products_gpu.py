@@ -675,3 +675,17 @@ def test_plans_follow_the_tensors():
         for lo, hi, e in rows_of(m, T, 2):
             ref[e] += dy[lo:hi].double().T @ x[lo:hi].double()
         assert torch.equal(dw, ref.float())
+
+
+@pytest.mark.parametrize("T,seg,R", [(600, 1, 16), (4096, 1, 8), (515, 2, 16), (1000, 3, 16), (250, 50, 64), (4097, 2, 8)])
+def test_lora_many_short_segments_in_any_order(T, seg, R):
+    """Segments against the rows' order, and the same adapter in neighbouring ones: a row's segment has to be searched for."""
+    g = gen(51)
+    n, A, K, N = T // seg, 6, 96, 72
+    ids = torch.randint(-1, A + 1, (n,), generator=g).int().cuda()
+    m = [(torch.arange(n - 1, -1, -1) * seg).int().cuda(), torch.full((n,), seg, dtype=torch.int32).cuda(), ids]
+    x, w = ints(g, (T, K), "bf16", 1), ints(g, (N, K), "bf16", 1)
+    a, b = ints(g, (A, R, K), "bf16", 1), ints(g, (A, N, R), "bf16", 1)
+    out = torch.zeros(T, N, device="cuda")
+    run_lora(x, w, a, b, out, m, n, seg)
+    assert torch.equal(out, lora_ref(x, w, a, b, m, None, T).float())
