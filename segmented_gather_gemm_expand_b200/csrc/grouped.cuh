@@ -527,6 +527,30 @@ __device__ __forceinline__ void load_t(TRows& x, int64_t row0, int i0, int begin
     }
 }
 
+// Two runs at a time (ranks of 16 at most): a row's ranks enter columns 0 .. 15 if
+// it belongs to run a, columns 16 .. 31 if to run b.
+__device__ __forceinline__ void load_t2(TRows& x, int64_t row0, int i0, int base, const Run& a, const Run& b, const Lora& lo,
+                                        int lane) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int k0 = i0 + lane + 32 * i, at = base + k0;
+        const bool in_a = at >= a.begin && at < a.end, in_b = at >= b.begin && at < b.end;
+        const float* src = lo.t + (row0 + k0) * lo.R;
+        const int n = in_a || in_b ? lo.R : 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float4 v;
+            if (lo.R % 4 == 0)
+                v = 4 * k < n ? reinterpret_cast<const float4*>(src)[k] : make_float4(0.f, 0.f, 0.f, 0.f);
+            else
+                v = make_float4(4 * k < n ? src[4 * k] : 0.f, 4 * k + 1 < n ? src[4 * k + 1] : 0.f,
+                                4 * k + 2 < n ? src[4 * k + 2] : 0.f, 4 * k + 3 < n ? src[4 * k + 3] : 0.f);
+            x.q[i][k] = in_a ? v : make_float4(0.f, 0.f, 0.f, 0.f);
+            x.q[i][k + 4] = in_a ? make_float4(0.f, 0.f, 0.f, 0.f) : v;
+        }
+    }
+}
+
 __device__ __forceinline__ void store_t(uint8_t* dst, TRows& x, int i0, int rows, int ranks, int parts, int lane, bool bf16) {
     const int C = parts == 2 ? 32 : 16;
 #pragma unroll
@@ -554,6 +578,15 @@ template <int CG>
 __device__ __forceinline__ void run_columns(const Run& run, int32_t ts, int32_t& off, int32_t& cols) {
     off = CG == 2 ? 0 : run.begin & ~15;
     cols = CG == 2 ? ts : min(ts, (run.end + 15) & ~15) - off;
+}
+
+// Runs that share a buffer of t: in a CTA pair two where their ranks fit into 32
+// columns, since writing a buffer takes longer than its MMAs (2048 rows of 64
+// segments, 4096 -> 4096, rank 16: 98 us with one, 87 with two).  A single CTA's
+// buffers are its run's rows alone, and twice as many: 81 us against 86.
+template <int CG>
+__device__ __forceinline__ int runs_per_step(const Lora& lo) {
+    return CG == 2 && lo.parts == 2 && lo.R <= 16 ? 2 : 1;
 }
 
 // The next box of x (16 << level rows) for `rows` more rows, a positive multiple of
@@ -811,30 +844,36 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
         const uint32_t buf = (uint32_t)(warp - LORA_WARP);
         uint8_t* dst = smem + g.off_t + buf * g.t_bytes;
         uint32_t m = 0, mine = 0;
+        const int per_step = runs_per_step<CG>(lo);
         bool ok = true;
         for (int32_t id = cid; ok && lora_here && id < total; id += ncl) {
             decode_tile(segs, nseg, g, id, WT, t);
             const int32_t last = first_run[t.tok + 1];
-            for (int32_t r = first_run[t.tok]; ok && r < last; ++r) {
-                const Run run = runs[r];
+            for (int32_t r = first_run[t.tok]; ok && r < last; r += per_step) {
+                const int n = CG == 2 ? min(per_step, last - r) : 1;
+                const Run run = runs[r], next = n == 2 ? runs[r + 1] : Run{0, 0, 0};
                 int32_t off, cols;
                 run_columns<CG>(run, t.ts, off, cols);
                 // the rows of t that this CTA's columns are: all of a single CTA's, a half of a pair's
                 const int32_t base = CG == 2 ? (int32_t)crank * (t.ts / 2) : off, rows = CG == 2 ? t.ts / 2 : cols;
                 for (int32_t r0 = 0; ok && r0 < lo.R; r0 += t_ranks, ++m) {
                     if (m % LORA_WARPS != buf) continue;
-                    const int ranks = min(t_ranks, lo.R - r0);
+                    const int ranks = n == 2 ? 32 : min(t_ranks, lo.R - r0);
                     TRows v;
-                    load_t(v, (int64_t)t.row0 + base, 0, run.begin - base, run.end - base, r0, ranks, lo, lane);
+                    const auto load = [&](int i0) {
+                        if (CG == 2 && per_step == 2) load_t2(v, (int64_t)t.row0 + base, i0, base, run, next, lo, lane);
+                        else load_t(v, (int64_t)t.row0 + base, i0, run.begin - base, run.end - base, r0, ranks, lo, lane);
+                    };
+                    load(0);
                     ok = warp_wait(smem_u32(&t_empty[buf]), (mine & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_CONVERT);
                     if (!ok) break;
                     ++mine;
                     store_t(dst, v, 0, rows, ranks, lo.parts, lane, bf16);
                     if (rows > 64) {
-                        load_t(v, (int64_t)t.row0 + base, 64, run.begin - base, run.end - base, r0, ranks, lo, lane);
+                        load(64);
                         store_t(dst, v, 64, rows, ranks, lo.parts, lane, bf16);
                     }
-                    asm volatile("fence.proxy.async;" ::: "memory");
+                    fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
                         if (CG == 2 && crank != 0) mbar_arrive_cluster(map_to_rank(smem_u32(&t_full[buf]), 0));
@@ -935,42 +974,43 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                     ok = mbar_wait(smem_u32(runs_ready), 0, abort_flag, DEVERR_TIMEOUT_MMA);
                     const uint64_t bk0 = smem_desc(smem_u32(smem), 16, 1024, 2);   // B's rows are K-major
                     const int32_t last = ok ? first_run[t.tok + 1] : 0;
-                    for (int32_t r = ok ? first_run[t.tok] : 0; ok && r < last; ++r) {
+                    const int per_step = runs_per_step<CG>(lo);
+                    for (int32_t r = ok ? first_run[t.tok] : 0; ok && r < last; r += per_step) {
+                        const int n_runs = CG == 2 ? min(per_step, last - r) : 1;
                         int32_t off, cols;
-                        run_columns<CG>(runs[r], t.ts, off, cols);
+                        run_columns<CG>(runs[r], t.ts, off, cols);   // a pair's: the whole tile for every run
                         const uint32_t idesc_t = instr_desc_mn(bf16, WT, cols), dt = d + (uint32_t)off;
-                        for (int32_t r0 = 0; r0 < lo.R; r0 += t_ranks) {
-                            if (!mbar_wait(smem_u32(&full[s]), phase, abort_flag, DEVERR_TIMEOUT_MMA)) {
-                                ok = false;
-                                break;
-                            }
+                        for (int32_t r0 = 0; ok && r0 < lo.R; r0 += t_ranks, ++m) {
                             const uint32_t buf = m % LORA_WARPS;
                             if (!mbar_wait(smem_u32(&t_full[buf]), (m / LORA_WARPS) & 1, abort_flag, DEVERR_TIMEOUT_MMA)) {
                                 ok = false;
                                 break;
                             }
-                            ++m;
-                            tc_fence_after();
-                            const uint64_t ad = bk0 + s * stage_step;
                             const uint64_t bd = smem_desc(smem_u32(smem + g.off_t + buf * g.t_bytes), 16, 1024, 2);
                             const int steps = (min(t_ranks, lo.R - r0) + 15) / 16;
-                            for (int part = 0; part < lo.parts; ++part)
-                                for (int kk = 0; kk < steps; ++kk) {
-                                    const uint64_t td = bd + (uint64_t)((part * t_ranks) / 8 + kk * 2);
-                                    if (CG == 2) tc_mma_pair(dt, ad + kk * 2, td, idesc_t, 1u);
-                                    else tc_mma(dt, ad + kk * 2, td, idesc_t, 1u);
+                            for (int i = 0; i < n_runs; ++i) {
+                                if (!mbar_wait(smem_u32(&full[s]), phase, abort_flag, DEVERR_TIMEOUT_MMA)) {
+                                    ok = false;
+                                    break;
                                 }
-                            if (CG == 2) {
-                                tc_commit_pair(smem_u32(&empty[s]));
-                                tc_commit_pair(smem_u32(&t_empty[buf]));
-                            } else {
-                                tc_commit(smem_u32(&empty[s]));
-                                tc_commit(smem_u32(&t_empty[buf]));
+                                tc_fence_after();
+                                const uint64_t ad = bk0 + s * stage_step;
+                                for (int part = 0; part < lo.parts; ++part)
+                                    for (int kk = 0; kk < steps; ++kk) {
+                                        const uint64_t td = bd + (uint64_t)((part * t_ranks) / 8 + (kk + i) * 2);
+                                        if (CG == 2) tc_mma_pair(dt, ad + kk * 2, td, idesc_t, 1u);
+                                        else tc_mma(dt, ad + kk * 2, td, idesc_t, 1u);
+                                    }
+                                if (CG == 2) tc_commit_pair(smem_u32(&empty[s]));
+                                else tc_commit(smem_u32(&empty[s]));
+                                if (++s == S) {
+                                    s = 0;
+                                    phase ^= 1;
+                                }
                             }
-                            if (++s == S) {
-                                s = 0;
-                                phase ^= 1;
-                            }
+                            if (!ok) break;
+                            if (CG == 2) tc_commit_pair(smem_u32(&t_empty[buf]));
+                            else tc_commit(smem_u32(&t_empty[buf]));
                         }
                     }
                 }

@@ -689,3 +689,21 @@ def test_lora_many_short_segments_in_any_order(T, seg, R):
     out = torch.zeros(T, N, device="cuda")
     run_lora(x, w, a, b, out, m, n, seg)
     assert torch.equal(out, lora_ref(x, w, a, b, m, None, T).float())
+
+
+@pytest.mark.parametrize("R", [4, 8, 13, 16, 17, 40])
+@pytest.mark.parametrize("lens", [[60, 70, 55], [20] * 30, [17, 200, 33, 40, 64, 31]])
+def test_lora_runs_that_share_steps(R, lens):
+    """Odd and even numbers of runs in a token tile of a CTA pair, some without an adapter, gaps between them."""
+    g = gen(61 + R)
+    n, A, K, N = len(lens), 5, 128, 300
+    m, T = meta(lens, [(3 * i) % (A + 1) - 1 for i in range(n)], gaps=[(5 * i) % 7 for i in range(n)])
+    T += 9
+    x, w = ints(g, (T, K), "f16", 1), ints(g, (N, K), "f16", 1)
+    a, b = ints(g, (A, R, K), "f16", 1), ints(g, (A, N, R), "f16", 1)
+    for variant in (sg.VARIANT_AUTO, sg.VARIANT_TC_WIDE):
+        sg.set_variant(variant)
+        for dt in ("f16", "f32"):
+            out = torch.full((T, N), float("nan"), device="cuda", dtype=DT[dt])
+            run_lora(x, w, a, b, out, m, n, max(lens))
+            assert torch.equal(out, rounded(lora_ref(x, w, a, b, m, None, T), dt))
