@@ -21,10 +21,12 @@
 //
 // Measured: 16384 ragged rows of 8 experts, 4096 x 11008, bf16: 1200-1250 us
 // back to back (1200 TFLOP/s, the power limit).  8192 rows of 16 experts, 2048 x
-// 2816: 117-135 us by box, where the flops alone would take 57: 89 us with no
+// 2816: 104-120 us by box, where the flops alone would take 57: 89 us with no
 // epilogue at all (8 K steps per tile on average; the longest cluster has 20 %
-// more than the mean), 28 more for the stores, which share the shared memory's
-// bandwidth with the MMAs' operands and TMA's writes.
+// more than the mean), 15 more for the stores, which share the shared memory's
+// bandwidth with the MMAs' operands and TMA's writes.  18 indexes of 888 x 1528 of
+// which one has rows: 22 us, of which the zeros are most (36 by way of the
+// epilogue's 64-byte pieces).
 #pragma once
 
 #include "grouped.cuh"
@@ -319,10 +321,20 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
                 grp::drain(taddr, half, g.ts, row0, valid, col, 0.f, p, stage, g.out_vec, drained, [](float (&)[8], int) {});
             } else {
                 drained();
+                if (g.out_vec && !p.add) {
+                    // zeros: 16 lanes write a row's 128 columns, a warp two rows at a time
+                    const int64_t k = k0 + (int32_t)crank * 128 + lane % 16 * 8;
+                    uint16_t* o = static_cast<uint16_t*>(p.out) + row0 * p.H + k;
+                    if (k < p.N)
+#pragma unroll 4
+                        for (int c = (warp - 2) * 2 + lane / 16; c < valid; c += 2 * EPI_WARPS)
+                            *reinterpret_cast<uint4*>(o + c * p.H) = make_uint4(0, 0, 0, 0);
+                } else {
 #pragma unroll 1
-                for (int c = half * 8; c < valid && !p.add; c += 16) {
-                    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    grp::put8(v, row0 + c, min(8, valid - c), col, p, stage, g.out_vec);
+                    for (int c = half * 8; c < valid && !p.add; c += 16) {
+                        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                        grp::put8(v, row0 + c, min(8, valid - c), col, p, stage, g.out_vec);
+                    }
                 }
             }
         }

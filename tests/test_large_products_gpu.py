@@ -707,3 +707,20 @@ def test_lora_runs_that_share_steps(R, lens):
             out = torch.full((T, N), float("nan"), device="cuda", dtype=DT[dt])
             run_lora(x, w, a, b, out, m, n, max(lens))
             assert torch.equal(out, rounded(lora_ref(x, w, a, b, m, None, T), dt))
+
+
+@pytest.mark.parametrize("cols,rows_dy", [(264, 40), (136, 300), (520, 776), (300, 48)])
+@pytest.mark.parametrize("out_dt", ["bf16", "f32"])
+def test_wgrad_zeros_stay_inside_their_index(cols, rows_dy, out_dt):
+    """Indexes without rows between those with some, in a dW whose rows and indexes have gaps: the gaps keep their bits."""
+    g = gen(71)
+    m, T = meta([3, 70, 1], [4, 1, 1])
+    dy, x = ints(g, (T, rows_dy), "bf16", 1), ints(g, (T, cols + 4 if cols % 8 else cols), "bf16", 1)[:, :cols]
+    full = torch.full((6, rows_dy + 1, cols + 8), 7.0, device="cuda", dtype=DT[out_dt])
+    dw = full[:, :rows_dy, :cols]
+    sg.sgmv_grouped_wgrad(dy, x, dw, *m, 3, 70)
+    ref = torch.full_like(full, 7.0, dtype=torch.float64)
+    ref[:, :rows_dy, :cols] = 0
+    for lo, hi, e in rows_of(m, T, 6):
+        ref[e, :rows_dy, :cols] += dy[lo:hi].double().T @ x[lo:hi].double()
+    assert torch.equal(full, ref.to(DT[out_dt]))
