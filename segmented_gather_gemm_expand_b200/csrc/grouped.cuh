@@ -432,10 +432,12 @@ __device__ __forceinline__ void repair_outputs(float (&v)[NT], int tok, int vali
 // are stored (one piece at a time: 113 us instead of 104 for the weight gradient
 // of 16 experts, whose tiles are short; the conversions and copies of a piece
 // wait for one another).  Short loops on purpose: straight-line code for 32 tokens
-// at a time spent its time fetching instructions.  `drained` runs once
+// at a time spent its time fetching instructions.  TWO false (single CTAs with
+// LORA_MMA, which have fewer registers a thread and shorter tiles): one piece at a
+// time, 37 mixed segments 39.2 us against 39.6.  `drained` runs once
 // the last values are in registers; repair(v, token) is for values that are no
 // finite numbers.
-template <class Drained, class Repair>
+template <bool TWO = true, class Drained, class Repair>
 __device__ __forceinline__ void drain(uint32_t taddr, int half, int ts, int64_t row0, int rows, int64_t n, float bias,
                                       const Problem& p, uint32_t* turn, bool vec, Drained&& drained, Repair&& repair) {
     const int lane = threadIdx.x % 32, r = lane / 4, c8 = (lane % 4) * 8;
@@ -452,7 +454,7 @@ __device__ __forceinline__ void drain(uint32_t taddr, int half, int ts, int64_t 
         drained();
         return;
     }
-    if (fast && rows >= 32) {
+    if (TWO && fast && rows >= 32) {
         tmem_ld8(taddr + (uint32_t)c, next);
         if (c + 16 < rows) tmem_ld8(taddr + (uint32_t)c + 16, next2);
 #pragma unroll 1
@@ -1142,7 +1144,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                 __syncwarp();
                 if (lane == 0 && id + 2 * ncl < total) mbar_arrive(smem_u32(&acc_empty[acc]));
             } else if (CG == 2 || csize == 1) {
-                drain(taddr, half, t.ts, t.row0, t.rows, col, bias, p, stage, g.out_vec, [&] {
+                drain<CG == 2 || LORA != LORA_MMA>(taddr, half, t.ts, t.row0, t.rows, col, bias, p, stage, g.out_vec, [&] {
                           tc_fence_before();
                           __syncwarp();
                           if (lane == 0 && id + 2 * ncl < total) {   // somebody waits for it

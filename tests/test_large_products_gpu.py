@@ -724,3 +724,18 @@ def test_wgrad_zeros_stay_inside_their_index(cols, rows_dy, out_dt):
     for lo, hi, e in rows_of(m, T, 6):
         ref[e, :rows_dy, :cols] += dy[lo:hi].double().T @ x[lo:hi].double()
     assert torch.equal(full, ref.to(DT[out_dt]))
+
+
+def test_lora_lengths_beyond_any_number_of_rows():
+    """64-bit metadata at its limits: every part of a call takes the same rows for a segment."""
+    g = gen(81)
+    m = [torch.tensor([0, 100, -5, 2 ** 62, 260], dtype=torch.int64).cuda(), torch.tensor([100, 60, 50, 5, 2 ** 62], dtype=torch.int64).cuda(),
+         torch.tensor([0, 1, 2, 1, 0], dtype=torch.int64).cuda()]
+    T, K, N, A = 300, 128, 200, 3
+    x, w = ints(g, (T, K), "bf16", 1), ints(g, (N, K), "bf16", 1)
+    a, b, out = ints(g, (A, 16, K), "bf16", 1), ints(g, (A, N, 16), "bf16", 1), torch.zeros(T, N, device="cuda")
+    run_lora(x, w, a, b, out, m, 5, 300)
+    ref = x.double() @ w.double().T
+    for lo, hi, i in ((0, 100, 0), (100, 160, 1), (260, 300, 0)):
+        ref[lo:hi] += (x[lo:hi].double() @ a[i].double().T) @ b[i].double().T
+    assert torch.equal(out, ref.float())
