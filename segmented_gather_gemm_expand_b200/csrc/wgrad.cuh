@@ -288,7 +288,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
                 for (int i = 0; i < (hs > 64 ? 4 : 3); ++i)
                     for (int32_t o = lane * 16; o < bytes; o += 512)
                         *reinterpret_cast<uint4*>(smem + s * STAGE + i * HALF + rem * 128 + o) = make_uint4(0, 0, 0, 0);
-                asm volatile("fence.proxy.async;" ::: "memory");
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     if (crank == 0) mbar_arrive(smem_u32(&full[s]));
