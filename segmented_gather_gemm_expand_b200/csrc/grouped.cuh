@@ -593,16 +593,31 @@ __device__ __forceinline__ void load_t2(TRows& x, int64_t row0, int i0, int base
     }
 }
 
-__device__ __forceinline__ void store_t(uint8_t* dst, TRows& x, int i0, int rows, int ranks, int parts, int lane, bool bf16) {
+// Rows of a buffer of t that are not zero: those of the runs (one or two) that
+// its step holds.
+struct TSpan {
+    int b[2], e[2];
+    __device__ __forceinline__ bool has(int row) const {
+        return (row >= b[0] && row < e[0]) || (row >= b[1] && row < e[1]);
+    }
+    __device__ __forceinline__ bool meets(int from, int to) const {
+        return max(b[0], from) < min(e[0], to) || max(b[1], from) < min(e[1], to);
+    }
+};
+
+// Writes the rows of `now` and zeroes those of `before`; all others are zero already
+// (2048 rows of 64 segments, rank 32: 96 us; 110 with every row written every time).
+__device__ __forceinline__ void store_t(uint8_t* dst, TRows& x, int i0, const TSpan& now, const TSpan& before, int parts,
+                                        int lane, bool bf16) {
     const int C = parts == 2 ? 32 : 16;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int row = i0 + lane + 32 * i;
-        if (row >= rows) continue;
+        if (!now.has(row) && !before.has(row)) continue;
         for (int part = 0; part < parts; ++part) {
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-                if (h >= 2 && ranks <= 16) continue;   // whole K steps of 16
+                if (h >= C / 8) continue;
                 float4 &a = x.q[i][2 * h], &b = x.q[i][2 * h + 1];
                 const uint32_t w0 = next_part(a.x, a.y, bf16), w1 = next_part(a.z, a.w, bf16);
                 const uint32_t w2 = next_part(b.x, b.y, bf16), w3 = next_part(b.z, b.w, bf16);
@@ -887,6 +902,9 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
         uint8_t* dst = smem + g.off_t + buf * g.t_bytes;
         uint32_t m = 0, mine = 0;
         const int per_step = runs_per_step<CG>(lo);
+        for (int o = lane * 16; o < g.t_bytes; o += 512) *reinterpret_cast<uint4*>(dst + o) = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+        TSpan before{{0, 0}, {0, 0}};
         bool ok = true;
         for (int32_t id = cid; ok && lora_here && id < total; id += ncl) {
             decode_tile(segs, nseg, g, id, WT, t);
@@ -906,15 +924,20 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                         if (CG == 2 && per_step == 2) load_t2(v, (int64_t)t.row0 + base, i0, base, run, next, lo, lane);
                         else load_t(v, (int64_t)t.row0 + base, i0, run.begin - base, run.end - base, r0, ranks, lo, lane);
                     };
-                    load(0);
+                    const TSpan now{{max(run.begin - base, 0), max(next.begin - base, 0)},
+                                    {min(run.end - base, rows), min(next.end - base, rows)}};
+                    const bool low = now.meets(0, 64) || before.meets(0, 64), high = now.meets(64, 128) || before.meets(64, 128);
+                    const int i0 = low ? 0 : 64;
+                    if (low || high) load(i0);
                     ok = warp_wait(smem_u32(&t_empty[buf]), (mine & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_CONVERT);
                     if (!ok) break;
                     ++mine;
-                    store_t(dst, v, 0, rows, ranks, lo.parts, lane, bf16);
-                    if (rows > 64) {
+                    if (low || high) store_t(dst, v, i0, now, before, lo.parts, lane, bf16);
+                    if (low && high) {
                         load(64);
-                        store_t(dst, v, 64, rows, ranks, lo.parts, lane, bf16);
+                        store_t(dst, v, 64, now, before, lo.parts, lane, bf16);
                     }
+                    before = now;
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
