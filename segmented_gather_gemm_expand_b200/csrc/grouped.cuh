@@ -539,11 +539,11 @@ __device__ __forceinline__ uint32_t next_part(float& a, float& b, bool bf16) {
     return bits;
 }
 
-// A low-rank step's t: `rows` (at most 128) rows of t from row0 on, ranks [r, r +
-// ranks), as a K-major tile with 128-byte swizzle: `parts` groups of C columns
-// (C = 32 for two parts, 16 for three), zero outside rows [begin, end) of the
-// tile and past the last rank.  One warp; a lane takes two rows at a time (i0 +
-// lane, i0 + lane + 32), all their ranks requested at once.
+// A low-rank step's t: up to 128 rows of t from row0 on, ranks [r, r + ranks), as
+// a K-major tile with 128-byte swizzle: `parts` groups of C columns (C = 32 for
+// two parts, 16 for three), zero outside the step's runs and past the last rank.
+// One warp; a lane takes two rows at a time (i0 + lane, i0 + lane + 32), all
+// their ranks requested at once.
 struct TRows {
     float4 q[2][8];
 };
