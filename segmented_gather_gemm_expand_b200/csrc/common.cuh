@@ -56,17 +56,22 @@ struct Segment {
     int64_t adapter;
 };
 
+// Rows of the `len` from `start` on that lie below lim: none for a negative start
+// or length.  start + len need not have a 64-bit value, so it is never formed.
+__host__ __device__ __forceinline__ int64_t clip_rows(int64_t start, int64_t len, int64_t lim) {
+    if (start < 0 || start >= lim || len <= 0) return 0;
+    return len < lim - start ? len : lim - start;
+}
+
+// The guards, for every kernel that reads segments.
+__host__ __device__ __forceinline__ Segment guard_segment(int64_t start, int64_t len, int64_t adapter, int64_t lim,
+                                                          int64_t adapters) {
+    return Segment{start, adapter >= 0 && adapter < adapters ? clip_rows(start, len, lim) : 0, adapter};
+}
+
 __device__ __forceinline__ Segment load_segment(const Problem& p, int64_t b) {
-    Segment s;
-    s.row0 = load_meta(p.start, b);
-    int64_t L = load_meta(p.len, b);
-    s.adapter = load_meta(p.idx, b);
-    const int64_t lim = p.out_rows < p.x_rows ? p.out_rows : p.x_rows;
-    int64_t end = s.row0 + L;
-    if (end > lim) end = lim;
-    bool ok = s.adapter >= 0 && s.adapter < p.lora_num && s.row0 >= 0 && L > 0 && end > s.row0;
-    s.rows = ok ? end - s.row0 : 0;
-    return s;
+    return guard_segment(load_meta(p.start, b), load_meta(p.len, b), load_meta(p.idx, b),
+                         p.out_rows < p.x_rows ? p.out_rows : p.x_rows, p.lora_num);
 }
 
 __device__ __forceinline__ float load_elem(const void* p, int dt, int64_t i) {

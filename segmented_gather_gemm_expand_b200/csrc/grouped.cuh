@@ -189,10 +189,10 @@ __device__ __forceinline__ void build_runs(const Geo& g, const Lora& lo, Run* ru
                                            int lane) {
     constexpr int THREADS = WARPS * 32;
     for (int32_t b = warp * 32 + lane; b < lo.batches; b += THREADS) {
-        const int64_t start = load_meta(lo.start, b), len = load_meta(lo.len, b), a = load_meta(lo.idx, b);
-        const int64_t end = len > g.dense_rows - start ? (int64_t)g.dense_rows : start + len;
-        const bool ok = a >= 0 && a < lo.adapters && start >= 0 && start < g.dense_rows && len > 0;
-        segs[b] = ok ? Run{lo.by_seg ? b : (int32_t)a, (int32_t)start, (int32_t)end} : Run{-1, 0, 0};
+        const Segment s =
+            guard_segment(load_meta(lo.start, b), load_meta(lo.len, b), load_meta(lo.idx, b), g.dense_rows, lo.adapters);
+        segs[b] = s.rows > 0 ? Run{lo.by_seg ? b : (int32_t)s.adapter, (int32_t)s.row0, (int32_t)(s.row0 + s.rows)}
+                             : Run{-1, 0, 0};
     }
     bar_sync(2, THREADS);
     for (int pass = 0; pass < 2; ++pass) {

@@ -171,16 +171,8 @@ __device__ __forceinline__ int64_t load_meta_l2(const MetaVec& m, int64_t i) {
 }
 
 __device__ __forceinline__ Segment load_segment_l2(const Problem& p, int64_t b) {
-    Segment s;
-    s.row0 = load_meta_l2(p.start, b);
-    const int64_t L = load_meta_l2(p.len, b);
-    s.adapter = load_meta_l2(p.idx, b);
-    const int64_t lim = p.out_rows < p.x_rows ? p.out_rows : p.x_rows;
-    int64_t end = s.row0 + L;
-    if (end > lim) end = lim;
-    const bool ok = s.adapter >= 0 && s.adapter < p.lora_num && s.row0 >= 0 && L > 0 && end > s.row0;
-    s.rows = ok ? end - s.row0 : 0;
-    return s;
+    return guard_segment(load_meta_l2(p.start, b), load_meta_l2(p.len, b), load_meta_l2(p.idx, b),
+                         p.out_rows < p.x_rows ? p.out_rows : p.x_rows, p.lora_num);
 }
 
 // log2 of the lanes between repeats of a block's rows in the staged x operand:

@@ -24,14 +24,14 @@ __global__ void validate_metadata_kernel(MetaVec start, MetaVec len, MetaVec idx
         if (a < -1 || a >= lora_num) bits |= 1;
         if (s < 0 || L < 0) bits |= 2;
         const bool valid = a >= 0 && a < lora_num && L > 0 && s >= 0;
-        if (valid && s + L > total_rows) bits |= 4;
+        if (valid && L > total_rows - s) bits |= 4;   // s + L may have no 64-bit value
         if (valid) {
             // next valid segment after b
             for (int64_t c = b + 1; c < batches; ++c) {
                 const int64_t a2 = load_meta(idx, c), s2 = load_meta(start, c), L2 = load_meta(len, c);
                 if (!(a2 >= 0 && a2 < lora_num && L2 > 0 && s2 >= 0)) continue;
                 if (s2 < s) unordered = true;
-                else if (s2 < s + L) bits |= 8;
+                else if (s2 - s < L) bits |= 8;
                 break;
             }
         }
@@ -55,7 +55,7 @@ __global__ void validate_overlap_pairwise_kernel(MetaVec start, MetaVec len, Met
         const int64_t a2 = load_meta(idx, c), s2 = load_meta(start, c), L2 = load_meta(len, c);
         const bool v1 = a1 >= 0 && a1 < lora_num && L1 > 0 && s1 >= 0;
         const bool v2 = a2 >= 0 && a2 < lora_num && L2 > 0 && s2 >= 0;
-        if (v1 && v2 && s1 < s2 + L2 && s2 < s1 + L1) atomicOr(status, 8);
+        if (v1 && v2 && s1 - s2 < L2 && s2 - s1 < L1) atomicOr(status, 8);
     }
 }
 
