@@ -41,9 +41,16 @@
 //          one adapter in a token tile and every 32 ranks, one stage holds B[a]'s
 //          rows (TMA) and a buffer of t's rows, zero outside the run, which
 //          warps of their own write some steps ahead of the MMAs.  t is fp32 and
-//          enters as the sum of two half-precision parts (hi, and what is left
-//          of it, rounded), three where out is fp32: relative errors of 2^-16
-//          (2^-24) against out's own rounding of 2^-9 (2^-24).  8764 rows of 16
+//          enters as the sum of two bf16 parts (hi, and what is left of it, rounded),
+//          three where out is fp32: two hold t to 2^-17 of itself (8 bits, and 8 of
+//          the 16 left, which have a sign), against out's own rounding of 2^-8 (fp16:
+//          2^-11); three hold fp32's 24 bits whole.  bf16 has fp32's range; fp16 parts
+//          would lose what lies above 65504 or below 2^-24, which t does even where out
+//          does not.  An fp16 B enters as two bf16 parts too, which hold its 11 bits
+//          exactly: the warps that write t split its tiles in shared memory (37 mixed
+//          segments of rank 24, fp16, 42.7 -> 44.7 us; 4520 rows of 118, 3680 -> 11867,
+//          rank 64, 595 -> 617).
+//          8764 rows of 16
 //          prompts, 4096 -> 12288, rank 16: 1483 us with FMAs in the epilogue, 710
 //          with these steps (the kernel alone 589, the tensor pipe 90 % busy; power).
 //          A B that TMA cannot read (a transposed view: the input gradient; ranks
@@ -88,6 +95,11 @@ constexpr int threads_of(int cg, int lora) {
 }
 constexpr int B_RING = 32 * 1024;          // LORA_FMA: buffered rows of B for each half of the epilogue's warps
 constexpr int B_SLOTS = 8;                 // at most
+constexpr int MAX_STAGES = 12;
+// LORA_MMA with an fp16 B: barriers on which the tiles of B to be split arrive, one per step in turn.  A step's barrier
+// is used again B_STEPS steps later, after the ring of stages has gone round, so its warp has seen the phase before.
+constexpr int B_STEPS = 2 * B_SLOTS;
+static_assert(B_STEPS >= MAX_STAGES && B_STEPS % 4 == 0, "a barrier belongs to one warp and never runs ahead of it");
 constexpr int RING_MAX_RANK = 64;
 constexpr int T_ROW = RING_MAX_RANK * 4;   // a slot's row of t, fp32
 constexpr int NUM_XMAPS = 4;            // x boxes of 16, 32, 64, 128 rows
@@ -139,7 +151,7 @@ struct Lora {
     const void* b;               // (adapters, N, R), the weights' dtype
     int64_t b_as, b_ns, b_ks;
     int32_t R;
-    int32_t parts;               // LORA_MMA: half-precision parts of t (2 or 3)
+    int32_t parts;               // LORA_MMA: bf16 parts of t (2 or 3)
     int32_t b_vec;               // rows of B can be read as 16-byte pieces
     int32_t by_seg;              // LORA_MMA: b holds one matrix per segment, not per adapter
     const void* bias;            // (N) in the weights' dtype, or null
@@ -386,7 +398,8 @@ __device__ __forceinline__ void put8(float (&v)[8], int64_t row, int valid, int6
 // would reach other requests' rows.  Where a run of the tile has such a value in
 // B's row n, the outputs of column n that are no finite numbers (of tokens tok ..
 // tok + valid - 1 of the tile, whose first row is row0) are computed again by the
-// formula, in fp32, each by the whole warp; `runs` first .. last are the tile's.
+// formula, in fp32, each by the whole warp, and with a split B all such outputs of
+// rows with an adapter; `runs` first .. last are the tile's.
 template <int NT>
 __device__ __forceinline__ void repair_outputs(float (&v)[NT], int tok, int valid, int64_t row0, int64_t n, const Run* runs,
                                                int first, int last, const Problem& p, const Lora& lo) {
@@ -400,9 +413,13 @@ __device__ __forceinline__ void repair_outputs(float (&v)[NT], int tok, int vali
         for (int r = first; r < last; ++r)
             for (int k = 0; k < lo.R; ++k)
                 b = fmaf(load_elem(lo.b, p.w_dt, (int64_t)runs[r].adapter * lo.b_as + n * lo.b_ns + k * lo.b_ks), 0.f, b);
-        if (b != 0.f)
+        unsigned redo = b != 0.f ? ~0u : 0u;
+        if (p.w_dt == SGMV_F16)   // an infinite t meets the zeros that are left of a split B
+            for (int r = first; r < last; ++r)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) bad |= (j < valid && fmaf(v[j], 0.f, 0.f) != 0.f ? 1u : 0u) << j;
+                for (int j = 0; j < NT; ++j) redo |= (tok + j >= runs[r].begin && tok + j < runs[r].end ? 1u : 0u) << j;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) bad |= (j < valid && (redo >> j & 1) && fmaf(v[j], 0.f, 0.f) != 0.f ? 1u : 0u) << j;
     }
     const int lane = threadIdx.x % 32;
     while (const unsigned who = __ballot_sync(0xffffffffu, bad != 0)) {
@@ -522,21 +539,47 @@ __device__ __forceinline__ void drain(uint32_t taddr, int half, int ts, int64_t 
     }
 }
 
-// The part of (a, b) that the parts before have not covered, rounded to the half
-// type: hi = rounded(v), then rounded(v - hi), ...  fp16 saturates (what is left
-// goes to the next part); an infinity or NaN stays in the first part alone.
-__device__ __forceinline__ uint32_t next_part(float& a, float& b, bool bf16) {
-    constexpr float MAX32 = 3.402823466e38f;
-    float x = a, y = b;
-    if (!bf16) {
-        if (fabsf(x) <= MAX32) x = fminf(fmaxf(x, -65504.f), 65504.f);
-        if (fabsf(y) <= MAX32) y = fminf(fmaxf(y, -65504.f), 65504.f);
+// The bf16 part of (a, b): hi = rounded(v), and v - hi left for the next part.  A
+// number above bf16's largest, or an infinity, leaves the largest, and the rest of it
+// (an infinity) to the last part, which is rounded as it is.
+__device__ __forceinline__ uint32_t next_part(float& a, float& b, bool last) {
+    uint32_t bits;
+    if (last) {
+        bits = pack2(a, b, true);
+    } else {
+        asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(bits) : "f"(b), "f"(a));
+        const float2 back = unpack2(bits, true);
+        a -= back.x;
+        b -= back.y;
     }
-    const uint32_t bits = pack2(x, y, bf16);
-    const float2 back = unpack2(bits, bf16);
-    a = fabsf(back.x) <= MAX32 ? a - back.x : 0.f;
-    b = fabsf(back.y) <= MAX32 ? b - back.y : 0.f;
     return bits;
+}
+
+// An fp16 tile of B (128 rows of `cols` ranks, K-major, 128-byte swizzle) as two bf16
+// tiles beside each other: the leading 8 of its 11 bits in place, the other three C
+// columns on, both exact.  (An infinity leaves NaN beside it: repair_outputs sees to
+// the outputs.)  One warp.
+__device__ __forceinline__ void split_b(uint8_t* tile, int C, int cols, int lane) {
+#pragma unroll 1
+    for (int h = 0; h < cols / 8; ++h) {
+#pragma unroll
+        for (int i = 0; i < WROWS / 32; ++i) {
+            const int row = lane + 32 * i;
+            uint4* src = reinterpret_cast<uint4*>(tile + row * 128 + ((h ^ (row & 7)) << 4));
+            const uint4 u = *src;
+            const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 v = unpack2(in[k], false);
+                const uint32_t a = __float_as_uint(v.x) & 0xffff0000u, b = __float_as_uint(v.y) & 0xffff0000u;
+                hi[k] = __byte_perm(a, b, 0x7632);
+                lo[k] = __byte_perm(__float_as_uint(v.x - __uint_as_float(a)), __float_as_uint(v.y - __uint_as_float(b)), 0x7632);
+            }
+            *src = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(tile + row * 128 + (((h + C / 8) ^ (row & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
 }
 
 // A low-rank step's t: up to 128 rows of t from row0 on, ranks [r, r + ranks), as
@@ -608,19 +651,20 @@ struct TSpan {
 // Writes the rows of `now` and zeroes those of `before`; all others are zero already
 // (2048 rows of 64 segments, rank 32: 96 us; 110 with every row written every time).
 __device__ __forceinline__ void store_t(uint8_t* dst, TRows& x, int i0, const TSpan& now, const TSpan& before, int parts,
-                                        int lane, bool bf16) {
+                                        int lane) {
     const int C = parts == 2 ? 32 : 16;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int row = i0 + lane + 32 * i;
         if (!now.has(row) && !before.has(row)) continue;
         for (int part = 0; part < parts; ++part) {
+            const bool last = part + 1 == parts;
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
                 if (h >= C / 8) continue;
                 float4 &a = x.q[i][2 * h], &b = x.q[i][2 * h + 1];
-                const uint32_t w0 = next_part(a.x, a.y, bf16), w1 = next_part(a.z, a.w, bf16);
-                const uint32_t w2 = next_part(b.x, b.y, bf16), w3 = next_part(b.z, b.w, bf16);
+                const uint32_t w0 = next_part(a.x, a.y, last), w1 = next_part(a.z, a.w, last);
+                const uint32_t w2 = next_part(b.x, b.y, last), w3 = next_part(b.z, b.w, last);
                 const int chunk = part * C / 8 + h;
                 *reinterpret_cast<uint4*>(dst + row * 128 + ((chunk ^ (row & 7)) << 4)) = make_uint4(w0, w1, w2, w3);
             }
@@ -683,7 +727,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
     uint64_t* red_free = red_full + 1;
     uint64_t* t_full = red_free + 1;   // LORA_MMA: buffers of t besides the stages
     uint64_t* t_empty = t_full + MAX_T_BUFS;
-    uint64_t* b_full = t_empty + MAX_T_BUFS;    // LORA_FMA: [half][slot]
+    uint64_t* b_full = t_empty + MAX_T_BUFS;    // LORA_FMA: [half][slot]; LORA_MMA: [step % B_STEPS]
     uint64_t* b_empty = b_full + 2 * B_SLOTS;
 
     // The table of runs (LORA_MMA) and its barrier.
@@ -707,7 +751,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                 mbar_init(smem_u32(&t_full[i]), CG);
                 mbar_init(smem_u32(&t_empty[i]), 1);
             }
-            for (int i = 0; LORA == LORA_FMA && i < 2 * B_SLOTS; ++i) {
+            for (int i = 0; LORA != LORA_NONE && i < 2 * B_SLOTS; ++i) {
                 mbar_init(smem_u32(&b_full[i]), 1);
                 mbar_init(smem_u32(&b_empty[i]), EPI_WARPS / 2);
             }
@@ -788,6 +832,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
     const int32_t kb1 = CG == 2 ? g.kblocks : (int32_t)((int64_t)g.kblocks * (crank + 1) / csize);
     const bool lora_here = CG == 2 || crank == 0;   // of CTAs that share a tile, the first adds the low-rank part
     const int32_t t_ranks = lo.parts == 2 ? 32 : 16;
+    const bool split = LORA == LORA_MMA && !bf16;   // B's tiles are split before the MMAs see them
     Tile t;
     if (LORA == LORA_MMA && warp >= 2) {
         constexpr int WARPS = EPI_WARPS + LORA_WARPS;
@@ -800,7 +845,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
         if (elect_one()) {
             const uint64_t pol_x = policy_evict_normal();
             const uint64_t pol_w = g.keep_w ? policy_evict_normal() : policy_evict_first();
-            uint32_t s = 0, phase = 1;
+            uint32_t s = 0, phase = 1, m = 0;
             bool ok = true;
             for (int32_t id = cid; ok && id < total; id += ncl) {
                 decode_tile(segs, nseg, g, id, WT, t);
@@ -861,24 +906,36 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                 if (LORA == LORA_MMA && ok && lora_here) {
                     ok = mbar_wait(smem_u32(runs_ready), 0, abort_flag, DEVERR_TIMEOUT_PRODUCER);
                     const int32_t last = ok ? first_run[t.tok + 1] : 0;
-                    for (int32_t r = ok ? first_run[t.tok] : 0; ok && r < last; ++r) {
-                        const int32_t a = runs[r].adapter;
-                        for (int32_t r0 = 0; r0 < lo.R; r0 += t_ranks) {
-                            if (!mbar_wait(smem_u32(&empty[s]), phase, abort_flag, DEVERR_TIMEOUT_PRODUCER)) {
-                                ok = false;
-                                break;
-                            }
-                            const uint32_t ws = smem_u32(smem + s * g.stage_bytes);
-                            if (CG == 2) {
-                                if (crank == 0) mbar_expect_tx(smem_u32(&full[s]), 2 * W_TILE);
-                                tma_load_3d_pair(ws, &bmap, r0, n0, a, map_to_rank(smem_u32(&full[s]), 0), pol_x);
-                            } else {
-                                mbar_expect_tx(smem_u32(&full[s]), W_TILE);
-                                tma_load_3d(ws, &bmap, r0, n0, a, smem_u32(&full[s]), pol_x);
-                            }
-                            if (++s == S) {
-                                s = 0;
-                                phase ^= 1;
+                    const int per_step = runs_per_step<CG>(lo);
+                    for (int32_t r = ok ? first_run[t.tok] : 0; ok && r < last; r += per_step) {
+                        const int n_runs = CG == 2 ? min(per_step, last - r) : 1;
+                        for (int32_t r0 = 0; ok && r0 < lo.R; r0 += t_ranks, ++m) {
+                            for (int i = 0; i < n_runs; ++i) {
+                                if (!mbar_wait(smem_u32(&empty[s]), phase, abort_flag, DEVERR_TIMEOUT_PRODUCER)) {
+                                    ok = false;
+                                    break;
+                                }
+                                const int32_t a = runs[r + i].adapter;
+                                const uint32_t ws = smem_u32(smem + s * g.stage_bytes);
+                                uint32_t bar = smem_u32(&full[s]);
+                                if (split) {
+                                    // the bytes arrive at this CTA's own barrier of the step; the stage's phase
+                                    // passes, and what the MMAs wait for is t's barrier, after the split
+                                    if (CG == 1 || crank == 0) mbar_arrive(bar);
+                                    bar = smem_u32(&b_full[m % B_STEPS]);
+                                    if (i == 0) mbar_expect_tx(bar, (uint32_t)n_runs * W_TILE);
+                                } else if (CG == 2) {
+                                    if (crank == 0) mbar_expect_tx(bar, 2 * W_TILE);
+                                    bar = map_to_rank(bar, 0);
+                                } else {
+                                    mbar_expect_tx(bar, W_TILE);
+                                }
+                                if (CG == 2) tma_load_3d_pair(ws, &bmap, r0, n0, a, bar, pol_x);
+                                else tma_load_3d(ws, &bmap, r0, n0, a, bar, pol_x);
+                                if (++s == S) {
+                                    s = 0;
+                                    phase ^= 1;
+                                }
                             }
                         }
                     }
@@ -900,7 +957,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
         if (g.early) grid_dependency_wait();
         const uint32_t buf = (uint32_t)(warp - LORA_WARP);
         uint8_t* dst = smem + g.off_t + buf * g.t_bytes;
-        uint32_t m = 0, mine = 0;
+        uint32_t m = 0, mine = 0, st = 0;   // st: the step's first stage, followed where B is split
         const int per_step = runs_per_step<CG>(lo);
         for (int o = lane * 16; o < g.t_bytes; o += 512) *reinterpret_cast<uint4*>(dst + o) = make_uint4(0, 0, 0, 0);
         __syncwarp();
@@ -909,6 +966,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
         for (int32_t id = cid; ok && lora_here && id < total; id += ncl) {
             decode_tile(segs, nseg, g, id, WT, t);
             const int32_t last = first_run[t.tok + 1];
+            if (split) st = (st + (uint32_t)(kb1 - kb0)) % S;
             for (int32_t r = first_run[t.tok]; ok && r < last; r += per_step) {
                 const int n = CG == 2 ? min(per_step, last - r) : 1;
                 const Run run = runs[r], next = n == 2 ? runs[r + 1] : Run{0, 0, 0};
@@ -917,6 +975,8 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                 // the rows of t that this CTA's columns are: all of a single CTA's, a half of a pair's
                 const int32_t base = CG == 2 ? (int32_t)crank * (t.ts / 2) : off, rows = CG == 2 ? t.ts / 2 : cols;
                 for (int32_t r0 = 0; ok && r0 < lo.R; r0 += t_ranks, ++m) {
+                    const uint32_t at = st;
+                    if (split) st = st + n >= S ? st + n - S : st + n;
                     if (m % LORA_WARPS != buf) continue;
                     const int ranks = n == 2 ? 32 : min(t_ranks, lo.R - r0);
                     TRows v;
@@ -929,15 +989,27 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                     const bool low = now.meets(0, 64) || before.meets(0, 64), high = now.meets(64, 128) || before.meets(64, 128);
                     const int i0 = low ? 0 : 64;
                     if (low || high) load(i0);
+                    // A pair's warps fall behind its MMAs, so they split B while t is on its way (642 us against
+                    // 658 on 4520 rows of 118 segments); a single CTA's have t ready long before B arrives (37 mixed
+                    // segments 45.8 against 48.3).
+                    const auto split_step = [&] {
+                        ok = warp_wait(smem_u32(&b_full[m % B_STEPS]), (m / B_STEPS) & 1, abort_flag, DEVERR_TIMEOUT_CONVERT);
+                        const int width = (min(t_ranks, lo.R - r0) + 15) & ~15;
+                        for (int i = 0; ok && i < n; ++i)
+                            split_b(smem + (at + i >= S ? at + i - S : at + i) * g.stage_bytes, t_ranks, width, lane);
+                        return ok;
+                    };
+                    if (CG == 2 && split && !split_step()) break;
                     ok = warp_wait(smem_u32(&t_empty[buf]), (mine & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_CONVERT);
                     if (!ok) break;
                     ++mine;
-                    if (low || high) store_t(dst, v, i0, now, before, lo.parts, lane, bf16);
+                    if (low || high) store_t(dst, v, i0, now, before, lo.parts, lane);
                     if (low && high) {
                         load(64);
-                        store_t(dst, v, 64, now, before, lo.parts, lane, bf16);
+                        store_t(dst, v, 64, now, before, lo.parts, lane);
                     }
                     before = now;
+                    if (CG == 1 && split && !split_step()) break;
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -1044,7 +1116,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                         const int n_runs = CG == 2 ? min(per_step, last - r) : 1;
                         int32_t off, cols;
                         run_columns<CG>(runs[r], t.ts, off, cols);   // a pair's: the whole tile for every run
-                        const uint32_t idesc_t = instr_desc_mn(bf16, WT, cols), dt = d + (uint32_t)off;
+                        const uint32_t idesc_t = instr_desc_mn(true, WT, cols), dt = d + (uint32_t)off;   // t and B in bf16
                         for (int32_t r0 = 0; ok && r0 < lo.R; r0 += t_ranks, ++m) {
                             const uint32_t buf = m % LORA_WARPS;
                             if (!mbar_wait(smem_u32(&t_full[buf]), (m / LORA_WARPS) & 1, abort_flag, DEVERR_TIMEOUT_MMA)) {
@@ -1060,12 +1132,14 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                                 }
                                 tc_fence_after();
                                 const uint64_t ad = bk0 + s * stage_step;
-                                for (int part = 0; part < lo.parts; ++part)
-                                    for (int kk = 0; kk < steps; ++kk) {
-                                        const uint64_t td = bd + (uint64_t)((part * t_ranks) / 8 + (kk + i) * 2);
-                                        if (CG == 2) tc_mma_pair(dt, ad + kk * 2, td, idesc_t, 1u);
-                                        else tc_mma(dt, ad + kk * 2, td, idesc_t, 1u);
-                                    }
+                                for (int q = 0; q < (split ? 2 : 1); ++q)
+                                    for (int part = 0; part < lo.parts; ++part)
+                                        for (int kk = 0; kk < steps; ++kk) {
+                                            const uint64_t bq = ad + (uint64_t)((q * t_ranks) / 8 + kk * 2);
+                                            const uint64_t td = bd + (uint64_t)((part * t_ranks) / 8 + (kk + i) * 2);
+                                            if (CG == 2) tc_mma_pair(dt, bq, td, idesc_t, 1u);
+                                            else tc_mma(dt, bq, td, idesc_t, 1u);
+                                        }
                                 if (CG == 2) tc_commit_pair(smem_u32(&empty[s]));
                                 else tc_commit(smem_u32(&empty[s]));
                                 if (++s == S) {
@@ -1429,7 +1503,7 @@ inline bool make_plan(const Problem& p, const Want& w, EncodeTiledFn enc, Plan* 
     g.dense_tiles = dense ? (int)((rows + g.dense_ts - 1) / g.dense_ts) : 0;
     g.max_runs = w.lora == LORA_MMA ? w.segs + g.dense_tiles : 0;   // segments that do not overlap fit
     const int table = w.lora == LORA_MMA ? (g.max_runs + w.segs) * (int)sizeof(Run) + (g.dense_tiles + 1) * 4 : 0;
-    for (g.stages = 12; g.stages >= 2; --g.stages) {
+    for (g.stages = MAX_STAGES; g.stages >= 2; --g.stages) {
         g.off_t = g.stages * g.stage_bytes;                       // t or B (1024-byte aligned: swizzled)
         g.off_tr = g.off_t + e.t_bufs * e.t + 2 * e.b_slots * g.b_bytes;
         g.off_out = g.off_tr + 2 * e.b_slots * T_ROW;

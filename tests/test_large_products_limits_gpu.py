@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import segmented_gather_gemm_expand_b200 as sg
-from test_large_products_gpu import _clean, gen, ints, run_lora  # noqa: F401
+from test_large_products_gpu import DT, _clean, gen, ints, lora_ref, meta, run_lora  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +57,85 @@ def test_metadata_check_at_the_end_of_64_bits():
     assert sg.validate_metadata(*m, 2, 1, 100) == 4 | 8 | 16
     m[1] = torch.tensor([INT64_MAX, 49]).cuda()
     assert sg.validate_metadata(*m, 2, 1, INT64_MAX) == 4 | 16
+
+# ---------------------------------------------------------------- the low-rank input t
+
+def one_entry_rows(T, K, scale, dt, g):
+    """Rows of x with one entry, a power of two: t = x A^T is then that entry times a column of A, without any rounding."""
+    k = torch.randint(0, K, (T,), generator=g)
+    x = torch.zeros(T, K, dtype=DT[dt])
+    x[torch.arange(T), k] = torch.as_tensor(scale, dtype=torch.float64).expand(T).to(DT[dt])
+    return x.cuda()
+
+
+# power of two in x, size of A, size of B: t about 1e6, 2e5, 1e-3, 1e-5, 1e-6 and 1e-8
+T_RANGE = {"1e6": (2.0 ** 10, 1000.0, 2.0 ** -10), "2e5": (2.0 ** 8, 800.0, 2.0 ** -7), "1e-3": (2.0 ** -4, 0.016, 4.0),
+           "1e-5": (2.0 ** -8, 0.0026, 500.0), "1e-6": (2.0 ** -12, 0.004, 5000.0), "1e-8": (2.0 ** -14, 0.00016, 30000.0)}
+
+
+@pytest.mark.parametrize("variant", [sg.VARIANT_AUTO, sg.VARIANT_TC_WIDE])
+@pytest.mark.parametrize("size", [*T_RANGE, "mixed"])
+@pytest.mark.parametrize("R", [8, 16, 24, 40])
+@pytest.mark.parametrize("dt,out_dt", [("f16", "f16"), ("f16", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+def test_lora_t_over_its_range(variant, size, R, dt, out_dt):
+    """The low-rank part alone (the shared weight is zero) for t of any size, on the tensor cores and beside single tokens.
+
+    t is exact here, so what is left is the split of t (none for fp32 out: three bf16 parts hold 24 bits; for two parts, t in
+    [1, 2): the first leaves at most 2^-8, whose own bf16 steps are 2^-16 at most below 2^-8, half of that is 2^-17), at most
+    6 R + K / 16 additions of the accumulator with 2^-23 of the sum of |products| each, and the rounding of out: half a step
+    of its type, at least half of its smallest one."""
+    g = gen(101 + R)
+    lens = [90, 1, 70, 33, 1, 60]
+    m, T = meta(lens, [0, 1, 2, 1, 0, 2])
+    K, N, A = 64, 136, 3
+    if size == "mixed":
+        scale, sa, sb = 2.0 ** torch.randint(-14, 11, (T,), generator=g).double(), 30.0, 2.0 ** -6
+    else:
+        scale, sa, sb = T_RANGE[size]
+    x = one_entry_rows(T, K, scale, dt, g)
+    a = (torch.rand(A, R, K, generator=g) * 2 * sa - sa).to(DT[dt]).cuda()
+    b = (torch.rand(A, N, R, generator=g) * 2 * sb - sb).to(DT[dt]).cuda()
+    w, out = torch.zeros(N, K, dtype=DT[dt], device="cuda"), torch.full((T, N), float("nan"), dtype=DT[out_dt], device="cuda")
+    sg.set_variant(variant)
+    assert sg.lora_linear_plan(x, w, a, b, out, *m, len(lens), max(lens))[0] == sg.VARIANT_TC
+    run_lora(x, w, a, b, out, m, len(lens), max(lens))
+    ref, sums = lora_ref(x, w, a, b, m, None, T), lora_ref(x.abs(), w, a.abs(), b.abs(), m, None, T)
+    f = torch.finfo(DT[out_dt])
+    bound = ((0 if out_dt == "f32" else 2 ** -17) + (6 * R + K // 16) * 2 ** -23) * sums
+    bound = bound + torch.clamp(ref.abs() + bound, min=f.tiny) * (f.eps / 2)
+    bad = (out.double() - ref).abs() > bound
+    assert not bad.any(), ((out.double() - ref).abs() / sums.clamp(min=1e-30))[bad].max()
+    assert (ref.abs() < f.max).all() and (sums > 0).any()
+
+
+@pytest.mark.parametrize("variant", [sg.VARIANT_AUTO, sg.VARIANT_TC_WIDE])
+@pytest.mark.parametrize("dt,out_dt", [("f16", "f16"), ("f16", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+def test_lora_infinite_t(variant, dt, out_dt):
+    """One infinity in an adapter's A makes t infinite in one rank: outputs are the infinities that the formula has, signs too."""
+    g = gen(111)
+    lens = [90, 1, 70, 33, 1, 60]
+    m, T = meta(lens, [0, 1, 2, 1, 0, 2])
+    x, w = torch.ones(T, 64, dtype=DT[dt], device="cuda"), ints(g, (136, 64), dt, 1)
+    a, b = ints(g, (3, 16, 64), dt, 1), ints(g, (3, 136, 16), dt, 1)
+    a[1, 5, 7] = float("inf")
+    b[1, :, 5] = torch.where(torch.arange(136) % 2 == 0, 1.0, -2.0).to(DT[dt]).cuda()
+    out = torch.zeros(T, 136, dtype=DT[out_dt], device="cuda")
+    sg.set_variant(variant)
+    run_lora(x, w, a, b, out, m, len(lens), max(lens))
+    assert torch.equal(out, lora_ref(x, w, a, b, m, None, T).to(DT[out_dt]))
+    assert torch.isinf(out[90:91]).all() and torch.isinf(out[161:194]).all() and torch.isfinite(out[:90]).all()
+
+
+@pytest.mark.parametrize("out_dt", ["bf16", "f32"])
+def test_lora_t_above_bf16s_largest_number(out_dt):
+    """fp32 goes a little further than bf16: such a t is finite, and so is its product with a small B."""
+    m, T = meta([60, 40], [0, 1])
+    x, a = torch.zeros(T, 64, device="cuda").bfloat16(), torch.zeros(2, 16, 64, device="cuda").bfloat16()
+    x[:, 0], x[:, 1] = 255 / 128 * 2.0 ** 64, 1.5 * 2.0 ** 60
+    a[:, :, 0], a[:, :, 1] = 255 / 128 * 2.0 ** 62, 2.0 ** 60
+    w, b = torch.zeros(136, 64, device="cuda").bfloat16(), torch.full((2, 136, 16), 2.0 ** -100, device="cuda").bfloat16()
+    t = x[0].double() @ a[0, 0].double()
+    assert torch.finfo(torch.bfloat16).max < t < torch.finfo(torch.float32).max
+    out = torch.zeros(T, 136, dtype=DT[out_dt], device="cuda")
+    run_lora(x, w, a, b, out, m, 2, 60)
+    assert torch.equal(out, lora_ref(x, w, a, b, m, None, T).float().to(DT[out_dt]))
