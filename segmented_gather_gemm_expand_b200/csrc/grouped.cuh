@@ -1409,6 +1409,23 @@ inline Extra extra_of(const Shape& sh, const Want& w) {
 
 inline int stage_bytes(const Shape& sh) { return W_TILE + sh.tn / sh.cg * 128; }
 
+// Token tiles of a dense call, and their height.
+struct DenseTiles {
+    int32_t ts, count;
+    DenseTiles(int64_t rows, const Shape& sh) {
+        const int64_t step = 16 * sh.cg, nt = (rows + sh.tn - 1) / sh.tn;
+        ts = (int32_t)(nt > 0 ? ((rows + nt - 1) / nt + step - 1) / step * step : step);
+        count = (int32_t)((rows + ts - 1) / ts);
+    }
+};
+
+// Bytes of the segment table, and of the table of runs (LORA_MMA: segments that do not overlap leave at most segs +
+// tiles runs, beside which stand each tile's first run and the call's segments).
+inline int64_t seg_table(const Problem& p, const Want& w) { return w.dense ? 0 : p.batches * (int64_t)sizeof(Seg); }
+inline int64_t run_table(int64_t tiles, const Want& w) {
+    return w.lora == LORA_MMA ? (2 * (int64_t)w.segs + tiles) * (int64_t)sizeof(Run) + (tiles + 1) * 4 : 0;
+}
+
 // The form with the least estimated time, in SM cycles.  A tile takes the
 // longest of: its loads at 64 bytes a cycle (weights, x, and B for LORA_FMA),
 // its MMAs (2 cycles per token column for 128 weight rows and 64 of K),
@@ -1438,7 +1455,9 @@ inline Shape choose_shape(const Problem& p, const Want& w) {
                 if (sp > 1 && kblocks < 4 * sp) break;
                 const Shape sh{cg, tn, sp};
                 const Extra e = extra_of(sh, w);
-                const int stages = (SMEM_LIMIT - 4096 - e.total()) / stage_bytes(sh);
+                // tables, barriers and alignment
+                const int64_t tables = seg_table(p, w) + run_table(w.dense ? DenseTiles(rows, sh).count : 0, w) + 1664;
+                const int stages = (int)((SMEM_LIMIT - (tables > 4096 ? tables : 4096) - e.total()) / stage_bytes(sh));
                 if (stages < 2) continue;
                 const int64_t workers = w.clusters[cg == 2 ? 1 : sp - 1];
                 if (workers < 1) continue;
@@ -1498,18 +1517,19 @@ inline bool make_plan(const Problem& p, const Want& w, EncodeTiledFn enc, Plan* 
     g.t_bytes = e.t;
     g.b_slots = e.b_slots;
     g.b_bytes = e.b_bytes;
-    const int step = 16 * sh.cg, nt = dense ? (int)((rows + sh.tn - 1) / sh.tn) : 0;
-    g.dense_ts = nt > 0 ? (int)(((rows + nt - 1) / nt + step - 1) / step * step) : step;
-    g.dense_tiles = dense ? (int)((rows + g.dense_ts - 1) / g.dense_ts) : 0;
-    g.max_runs = w.lora == LORA_MMA ? w.segs + g.dense_tiles : 0;   // segments that do not overlap fit
-    const int table = w.lora == LORA_MMA ? (g.max_runs + w.segs) * (int)sizeof(Run) + (g.dense_tiles + 1) * 4 : 0;
+    const DenseTiles tiles_of(dense ? rows : 0, sh);
+    g.dense_ts = tiles_of.ts;
+    g.dense_tiles = tiles_of.count;
+    g.max_runs = w.lora == LORA_MMA ? w.segs + g.dense_tiles : 0;
+    if (seg_table(p, w) + run_table(g.dense_tiles, w) > SMEM_LIMIT) return false;
+    const int table = (int)run_table(g.dense_tiles, w);
     for (g.stages = MAX_STAGES; g.stages >= 2; --g.stages) {
         g.off_t = g.stages * g.stage_bytes;                       // t or B (1024-byte aligned: swizzled)
         g.off_tr = g.off_t + e.t_bufs * e.t + 2 * e.b_slots * g.b_bytes;
         g.off_out = g.off_tr + 2 * e.b_slots * T_ROW;
         g.off_red = g.off_out + e.out;
         g.off_seg = g.off_red + e.red;
-        g.off_runs = (g.off_seg + (dense ? 0 : (int)segs * (int)sizeof(Seg)) + 15) & ~15;
+        g.off_runs = (g.off_seg + (int)seg_table(p, w) + 15) & ~15;
         g.off_bar = (g.off_runs + table + 15) & ~15;
         out->smem_bytes = g.off_bar + 8 * (2 * g.stages + 7 + 2 * MAX_T_BUFS + 4 * B_SLOTS) + 1024;
         if (out->smem_bytes <= SMEM_LIMIT) break;

@@ -727,9 +727,16 @@ int choose_lora(LoraCall* c, const DeviceInfo& dev, int forced, char* ws, size_t
               grp::encode_b(packed, c->base.N, c->shrink.batches, tc::encode_fn(), &pl->bm);
     }
     pl->lora = !c->low_rank ? grp::LORA_NONE : mma ? grp::LORA_MMA : grp::LORA_FMA;
-    const bool tc_ok = tc && grp::cached_plan(c->base, true, c->low_rank, pl->lora, c->lo.R, grp::ring_ok(c->lo),
-                                              (int)c->shrink.batches, dev.sm_count,
-                                              forced_cg(forced), tc::encode_fn(), &pl->base);
+    const auto plan = [&] {
+        return tc && grp::cached_plan(c->base, true, c->low_rank, pl->lora, c->lo.R, grp::ring_ok(c->lo),
+                                      (int)c->shrink.batches, dev.sm_count, forced_cg(forced), tc::encode_fn(), &pl->base);
+    };
+    bool tc_ok = plan();
+    if (!tc_ok && mma) {   // millions of rows: the table of runs leaves no room for two stages
+        mma = false;
+        pl->lora = grp::LORA_FMA;
+        tc_ok = plan();
+    }
     pl->variant = large_variant(tc_ok, forced);
     if (pl->variant < 0) return pl->variant;
     pl->mma = mma && tc_ok;

@@ -139,3 +139,25 @@ def test_lora_t_above_bf16s_largest_number(out_dt):
     out = torch.zeros(T, 136, dtype=DT[out_dt], device="cuda")
     run_lora(x, w, a, b, out, m, 2, 60)
     assert torch.equal(out, lora_ref(x, w, a, b, m, None, T).float().to(DT[out_dt]))
+
+
+# ---------------------------------------------------------------- many segments, many rows
+
+@pytest.mark.parametrize("rows,segs,K,N,R,dt", [(16384, 4096, 128, 512, 16, "bf16"), (16000, 4000, 256, 136, 8, "f16"),
+                                                (32768, 4096, 64, 264, 32, "bf16"), (2200000, 5, 64, 72, 16, "bf16")])
+def test_lora_counts_at_the_tables_limits(rows, segs, K, N, R, dt):
+    """As many segments as the tensor-core forms take, four rows each, and more rows than a table of runs holds."""
+    g = gen(121)
+    x, w = ints(g, (rows, K), dt, 1), ints(g, (N, K), dt, 1)
+    a, b = ints(g, (7, R, K), dt, 1), ints(g, (7, N, R), dt, 1)
+    n = rows // segs
+    m = [(torch.arange(segs) * n).int().cuda(), torch.full((segs,), n).int().cuda(), (torch.arange(segs) % 8 - 1).int().cuda()]
+    out = torch.zeros(rows, N, device="cuda")
+    assert sg.lora_linear_plan(x, w, a, b, out, *m, segs, n)[0] == sg.VARIANT_TC
+    run_lora(x, w, a, b, out, m, segs, n)
+    ids = (torch.arange(rows, device="cuda") // n).clamp(max=segs - 1) % 8 - 1
+    ref = x.float() @ w.float().T          # whole numbers below 2^24: exact
+    for i in range(7):
+        at = (ids == i).nonzero()[:, 0]
+        ref[at] += (x[at].float() @ a[i].float().T) @ b[i].float().T
+    assert torch.equal(out, ref)
