@@ -55,7 +55,7 @@
 //          with these steps (the kernel alone 589, the tensor pipe 90 % busy; power).
 //          A B that TMA cannot read (a transposed view: the input gradient; ranks
 //          that leave rows off the 16-byte boundaries) is laid out anew, per
-//          segment, where the workspace has room.
+//          segment or per adapter, where the workspace has room.
 //   LORA_FMA   on the CUDA cores in fp32, by the epilogue's warps while the K loop
 //          runs (they keep it in TMEM until the sums are there): single tokens
 //          with an adapter each, or a B that TMA cannot read (without room).  Warp 10 copies
@@ -153,7 +153,7 @@ struct Lora {
     int32_t R;
     int32_t parts;               // LORA_MMA: bf16 parts of t (2 or 3)
     int32_t b_vec;               // rows of B can be read as 16-byte pieces
-    int32_t by_seg;              // LORA_MMA: b holds one matrix per segment, not per adapter
+    int32_t by_seg;              // LORA_MMA: b is laid out anew with one matrix per segment, not per adapter
     const void* bias;            // (N) in the weights' dtype, or null
     int64_t bias_s;
 };

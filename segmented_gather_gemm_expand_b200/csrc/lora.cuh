@@ -140,18 +140,32 @@ inline bool row_shrink_vec(const Problem& p) {
            (reinterpret_cast<uintptr_t>(p.x) & 15) == 0 && (reinterpret_cast<uintptr_t>(p.w) & 15) == 0;
 }
 
-// B of every segment's adapter with its ranks contiguous, rows padded to whole
-// 16-byte pieces: out[b][n][j], j < pitch.  A thread takes a row of B, eight
-// ranks at a time; neighbouring threads take neighbouring rows, which is how a
-// transposed view lies in memory.  Segments without rows or adapter are left out.
+// B with its ranks contiguous, rows padded to whole 16-byte pieces: out[i][n][j],
+// j < pitch.  i: a segment, whose adapter's B it is (by_seg), or an adapter,
+// whichever are fewer.  A thread takes a row of B, eight ranks at a time;
+// neighbouring threads take neighbouring rows, which is how a transposed view
+// lies in memory.  Segments without rows and adapters without segments are left out.
 constexpr int PACK_THREADS = 256;
-__global__ void __launch_bounds__(PACK_THREADS) pack_b_kernel(Problem p, grp::Lora lo, uint16_t* out, int64_t N, int32_t pitch) {
+__global__ void __launch_bounds__(PACK_THREADS) pack_b_kernel(Problem p, grp::Lora lo, uint16_t* out, int64_t N, int32_t pitch,
+                                                              bool by_seg) {
     tc::grid_dependency_wait();
     tc::grid_dependents_launch();
-    const Segment s = load_segment(p, blockIdx.y);
+    int64_t adapter = blockIdx.y;
+    bool used = false;
+    if (by_seg) {
+        const Segment s = load_segment(p, blockIdx.y);
+        used = s.rows > 0;
+        adapter = s.adapter;
+    } else {
+        for (int64_t b = threadIdx.x; b < p.batches && !used; b += PACK_THREADS) {
+            const Segment s = load_segment(p, b);
+            used = s.rows > 0 && s.adapter == adapter;
+        }
+        used = __syncthreads_or(used);
+    }
     const int64_t n = (int64_t)blockIdx.x * PACK_THREADS + threadIdx.x;
-    if (s.rows <= 0 || n >= N) return;
-    const uint16_t* b = static_cast<const uint16_t*>(lo.b) + (int64_t)s.adapter * lo.b_as + n * lo.b_ns;
+    if (!used || n >= N) return;
+    const uint16_t* b = static_cast<const uint16_t*>(lo.b) + adapter * lo.b_as + n * lo.b_ns;
     uint16_t* o = out + ((int64_t)blockIdx.y * N + n) * pitch;
     for (int32_t j0 = 0; j0 < pitch; j0 += 8) {
         uint32_t v[8];
@@ -245,10 +259,12 @@ inline int launch_row_shrink(const Problem& p, float* t, int32_t* row_adapter, i
                : launch_dependent(row_shrink_kernel<false>, grid, SHRINK_THREADS, stream, p, t, row_adapter, rows);
 }
 
-inline int launch_pack_b(const Problem& p, const grp::Lora& lo, void* out, int64_t N, int32_t pitch, cudaStream_t stream) {
+// The caller's lora_b (`given`) into the place and layout of `packed`.
+inline int launch_pack_b(const Problem& p, const grp::Lora& given, const grp::Lora& packed, int64_t N, cudaStream_t stream) {
     const int64_t gx = (N + PACK_THREADS - 1) / PACK_THREADS;
-    return launch_dependent(pack_b_kernel, dim3((unsigned)gx, (unsigned)p.batches), PACK_THREADS, stream, p, lo,
-                            static_cast<uint16_t*>(out), N, pitch);
+    return launch_dependent(pack_b_kernel, dim3((unsigned)gx, (unsigned)(packed.by_seg ? p.batches : p.lora_num)), PACK_THREADS,
+                            stream, p, given, const_cast<uint16_t*>(static_cast<const uint16_t*>(packed.b)), N,
+                            (int32_t)packed.b_ns, packed.by_seg != 0);
 }
 
 inline int launch_lora_simt(const Problem& p, const grp::Lora& lo, int64_t rows, cudaStream_t stream) {

@@ -692,7 +692,7 @@ struct LoraPlan {
     int lora;                                        // grp::LoraMode of the tensor-core form
     bool mma;                                        // that is LORA_MMA
     grp::Lora given;                                 // pack: lora_b as the caller has it
-    bool pack;                                       // lay lora_b out anew in the workspace, per segment
+    bool pack;                                       // lay lora_b out anew in the workspace, per segment or adapter
     CUtensorMap bm;
     enum { NONE, BY_ROW, BLOCKS, PRODUCT } shrink;   // how t is computed
     int splits;                                      // BLOCKS: parts of K
@@ -713,18 +713,19 @@ int choose_lora(LoraCall* c, const DeviceInfo& dev, int forced, char* ws, size_t
     grp::Lora packed = c->lo;
     int64_t pack_bytes = 0;
     if (mma && !grp::encode_b(c->lo, c->base.N, c->shrink.lora_num, tc::encode_fn(), &pl->bm)) {
-        // A copy per segment costs less than FMAs for every row.  4096 -> 4096, a transposed B of rank 16:
-        // 8192 rows of 16 segments 1493 -> 202 us, 1024 rows of 256 segments 325 -> 138; rank 4, 8192 rows
-        // 483 -> 206, but 1024 rows of 256 segments 119 -> 128.
-        packed.by_seg = 1;
+        // A copy costs less than FMAs for every row: per segment, or per adapter where those are fewer.  4096 -> 4096,
+        // 32 adapters, a transposed B of rank 16: 8192 rows of 16 segments 1489 -> 210 us, 1024 rows of 256 segments
+        // 284 -> 103 (120 with a copy per segment); rank 4, 8192 rows 483 -> 212, but 1024 rows of 256 segments 75 -> 90.
+        packed.by_seg = c->shrink.batches <= c->shrink.lora_num;
         packed.b = ws + c->off_part;
         packed.b_ks = 1;
         packed.b_ns = (c->lo.R + 7) / 8 * 8;
         packed.b_as = c->base.N * packed.b_ns;
         packed.b_vec = 1;
-        pack_bytes = align256(c->shrink.batches * packed.b_as * 2);
+        const int64_t copies = packed.by_seg ? c->shrink.batches : c->shrink.lora_num;
+        pack_bytes = align256(copies * packed.b_as * 2);
         mma = packed.b_as < (int64_t(1) << 31) && ws_bytes >= (size_t)(c->off_part + pack_bytes) &&
-              grp::encode_b(packed, c->base.N, c->shrink.batches, tc::encode_fn(), &pl->bm);
+              grp::encode_b(packed, c->base.N, copies, tc::encode_fn(), &pl->bm);
     }
     pl->lora = !c->low_rank ? grp::LORA_NONE : mma ? grp::LORA_MMA : grp::LORA_FMA;
     const auto plan = [&] {
@@ -777,8 +778,7 @@ int run_lora(const LoraCall& c, const DeviceInfo& dev, const LoraPlan& pl, char*
     float* t = reinterpret_cast<float*>(ws + c.off_t);
     const Call shrink{c.shrink, 0, false};
     // first: a projection that starts early waits for the shrink alone
-    if (pl.pack && (rc = lora::launch_pack_b(c.shrink, pl.given, const_cast<void*>(c.lo.b), c.base.N, (int32_t)c.lo.b_ns, st)))
-        return rc;
+    if (pl.pack && (rc = lora::launch_pack_b(c.shrink, pl.given, c.lo, c.base.N, st))) return rc;
     // row_shrink_kernel finds the rows' adapters by itself, the projection's K steps read the segments
     if (!pl.mma && (pl.shrink == LoraPlan::BLOCKS || pl.shrink == LoraPlan::PRODUCT))
         if ((rc = lora::launch_row_adapter(c.shrink, rows, c.rows, st))) return rc;

@@ -161,3 +161,22 @@ def test_lora_counts_at_the_tables_limits(rows, segs, K, N, R, dt):
         at = (ids == i).nonzero()[:, 0]
         ref[at] += (x[at].float() @ a[i].float().T) @ b[i].float().T
     assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("adapters", [3, 40, 90])
+@pytest.mark.parametrize("R", [4, 16])
+def test_lora_turned_b_of_fewer_adapters_than_segments(adapters, R):
+    """A B that has to be laid out anew takes the space of the adapters or of the segments' copies, whichever is less."""
+    g = gen(131)
+    K, N, segs = 64, 264, 60
+    m, T = meta([5 + i % 4 for i in range(segs)], [(7 * i) % (min(adapters, 30) + 2) - 1 for i in range(segs)], gaps=[i % 2 for i in range(segs)])
+    x, w, a = ints(g, (T, K), "bf16", 1), ints(g, (N, K), "bf16", 1), ints(g, (adapters, R, K), "bf16", 1)
+    b, out = ints(g, (adapters, R, N), "bf16", 1).transpose(1, 2), torch.zeros(T, N, device="cuda")
+    _, need, pref = sg.lora_linear_plan(x, w, a, b, out, *m, segs, 8)
+    # what the sums of t take beside it: nothing at ranks that are no multiple of 16
+    straight = sg.lora_linear_plan(x, w, a, b.contiguous(), out, *m, segs, 8)[2] if R == 16 else need
+    assert need < pref <= straight + min(adapters, segs) * N * ((R + 7) // 8 * 8) * 2 + 256
+    for spare in (True, False):
+        out.fill_(float("nan"))
+        run_lora(x, w, a, b, out, m, segs, 8, spare=spare)
+        assert torch.equal(out, lora_ref(x, w, a, b, m, None, T).float())
