@@ -393,53 +393,107 @@ __device__ __forceinline__ void put8(float (&v)[8], int64_t row, int valid, int6
         if (j < valid) o[j * p.H] = (uint16_t)float_to_half_bits(v[j], ob);
 }
 
-// LORA_MMA, where an accumulator is an infinity or NaN: rows outside a run take
+// NaN where a value is no finite number, else z.
+__device__ __forceinline__ float no_numbers(const float (&v)[8], float z) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z = fmaf(v[j], 0.f, z);
+    return z;
+}
+
+// LORA_MMA, where an accumulator was an infinity or NaN: rows outside a run take
 // part in the run's MMA with t = 0, and 0 times an infinity in that adapter's B
-// would reach other requests' rows.  Where a run of the tile has such a value in
-// B's row n, the outputs of column n that are no finite numbers (of tokens tok ..
-// tok + valid - 1 of the tile, whose first row is row0) are computed again by the
-// formula, in fp32, each by the whole warp, and with a split B all such outputs of
-// rows with an adapter; `runs` first .. last are the tile's.
-template <int NT>
-__device__ __forceinline__ void repair_outputs(float (&v)[NT], int tok, int valid, int64_t row0, int64_t n, const Run* runs,
-                                               int first, int last, const Problem& p, const Lora& lo) {
-    float z = 0.f;   // NaN if any value is no finite number
-#pragma unroll
-    for (int j = 0; j < NT; ++j) z = fmaf(v[j], 0.f, z);
-    if (!__any_sync(0xffffffffu, z != 0.f)) return;
-    unsigned bad = 0;
-    if (z != 0.f && n < p.N) {
-        float b = 0.f;
+// reaches other requests' rows.  Where a run of the tile has such a value in B's
+// row n, the outputs of column n that are no finite numbers (of the tokens first_tok
+// .. end_tok of the tile that this warp has stored, whose first row is row0) are
+// computed again by the formula, in fp32; with a split B all such outputs of rows
+// with an adapter, since an infinite t met the zeros that are left of B.  `runs`
+// first .. last are the tile's.  The warp computes its 32 columns of eight tokens at
+// once, after it has handed its accumulator back: with a warp per output and the
+// accumulator held, a tile took up to 350 ms at K = 4096, which for K above 24000
+// was more than the two seconds that the MMAs wait.  8192 rows of 16 segments, 4096 ->
+// 4096, one adapter full of NaN: 352 ms then, 8 ms now (200 us without the NaN).
+__device__ __forceinline__ void repair_outputs(int first_tok, int end_tok, int64_t row0, int64_t n, float bias, const Run* runs,
+                                            int first, int last, const Problem& p, const Lora& lo) {
+    const bool bf16 = p.w_dt == SGMV_BF16;
+    const int64_t col = n < p.N ? n : p.N - 1;
+    const uint16_t* b = static_cast<const uint16_t*>(lo.b) + col * lo.b_ns;
+    float z = 0.f;   // NaN if a run's B is no finite number in this row
+#pragma unroll 1
+    for (int r = first; r < last; ++r)
+#pragma unroll 4
+        for (int k = 0; k < lo.R; ++k)
+            z = fmaf(half_bits_to_float(__ldg(b + runs[r].adapter * lo.b_as + k * lo.b_ks), bf16), 0.f, z);
+    // rows of x start on 16-byte boundaries, the weights' too where K is their contiguous axis
+    const uint16_t* w = static_cast<const uint16_t*>(p.w) + col * p.w_ns;
+    const bool w_vec = p.w_ks == 1 && (p.w_ns * 2) % 16 == 0;
+    __syncwarp();   // the outputs were stored by other lanes
+#pragma unroll 1
+    for (int tok = first_tok; tok < end_tok; tok += 16) {
+        const int64_t row = row0 + tok;
+        unsigned bad = 0, in_run = 0;
+        for (int j = 0; j < 8; ++j)
+            if (tok + j < end_tok && n < p.N && fmaf(load_elem(p.out, p.out_dt, (row + j) * p.H + n), 0.f, 0.f) != 0.f)
+                bad |= 1u << j;
         for (int r = first; r < last; ++r)
-            for (int k = 0; k < lo.R; ++k)
-                b = fmaf(load_elem(lo.b, p.w_dt, (int64_t)runs[r].adapter * lo.b_as + n * lo.b_ns + k * lo.b_ks), 0.f, b);
-        unsigned redo = b != 0.f ? ~0u : 0u;
-        if (p.w_dt == SGMV_F16)   // an infinite t meets the zeros that are left of a split B
+            for (int j = 0; j < 8; ++j) in_run |= (tok + j >= runs[r].begin && tok + j < runs[r].end ? 1u : 0u) << j;
+        if (z == 0.f) bad &= bf16 ? 0u : in_run;
+        const unsigned want = __reduce_or_sync(0xffffffffu, bad);
+        if (!want) continue;
+        const uint16_t* x[8];
+        float s[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {   // rows that nobody asks for may not exist
+            x[j] = static_cast<const uint16_t*>(p.x) + (row + (want >> j & 1 ? j : __ffs(want) - 1)) * p.x_rs;
+            s[j] = 0.f;
+        }
+        int64_t k = 0;
+#pragma unroll 1
+        for (; k + 8 <= p.K; k += 8) {
+            uint4 u[8];
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = __ldg(reinterpret_cast<const uint4*>(x[j] + k));
+            if (w_vec) {
+                const uint4 q = __ldg(reinterpret_cast<const uint4*>(w + k));
+                const uint32_t q4[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 c = unpack2(q4[i], bf16);
+                    f[2 * i] = c.x;
+                    f[2 * i + 1] = c.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = half_bits_to_float(__ldg(w + (k + i) * p.w_ks), bf16);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t q4[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 c = unpack2(q4[i], bf16);
+                    s[j] = fmaf(c.x, f[2 * i], s[j]);
+                    s[j] = fmaf(c.y, f[2 * i + 1], s[j]);
+                }
+            }
+        }
+#pragma unroll 1
+        for (; k < p.K; ++k) {
+            const float f = half_bits_to_float(__ldg(w + k * p.w_ks), bf16);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] = fmaf(half_bits_to_float(__ldg(x[j] + k), bf16), f, s[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (!(want >> j & 1)) continue;
+#pragma unroll 1
             for (int r = first; r < last; ++r)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) redo |= (tok + j >= runs[r].begin && tok + j < runs[r].end ? 1u : 0u) << j;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) bad |= (j < valid && (redo >> j & 1) && fmaf(v[j], 0.f, 0.f) != 0.f ? 1u : 0u) << j;
-    }
-    const int lane = threadIdx.x % 32;
-    while (const unsigned who = __ballot_sync(0xffffffffu, bad != 0)) {
-        const int src = __ffs(who) - 1, at = __shfl_sync(0xffffffffu, __ffs(bad) - 1, src);
-        const int64_t row = row0 + tok + at, col = n - lane + src;
-        float sum = 0.f;
-        for (int64_t k = lane; k < p.K; k += 32)
-            sum = fmaf(load_elem(p.x, p.x_dt, row * p.x_rs + k * p.x_cs), load_elem(p.w, p.w_dt, col * p.w_ns + k * p.w_ks), sum);
-        for (int r = first; r < last; ++r)
-            if (tok + at >= runs[r].begin && tok + at < runs[r].end)
-                for (int k = lane; k < lo.R; k += 32)
-                    sum = fmaf(lo.t[row * lo.R + k],
-                               load_elem(lo.b, p.w_dt, (int64_t)runs[r].adapter * lo.b_as + col * lo.b_ns + k * lo.b_ks), sum);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == src) {
-            bad &= bad - 1;
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                if (j == at) v[j] = sum;
+                if (tok + j >= runs[r].begin && tok + j < runs[r].end)
+#pragma unroll 4
+                    for (int i = 0; i < lo.R; ++i)
+                        s[j] = fmaf(lo.t[(row + j) * lo.R + i],
+                                    half_bits_to_float(__ldg(b + runs[r].adapter * lo.b_as + i * lo.b_ks), bf16), s[j]);
+            if (bad >> j & 1) store_elem(p.out, p.out_dt, (row + j) * p.H + n, s[j] + bias);
         }
     }
 }
@@ -452,11 +506,11 @@ __device__ __forceinline__ void repair_outputs(float (&v)[NT], int tok, int vali
 // at a time spent its time fetching instructions.  TWO false (single CTAs with
 // LORA_MMA, which have fewer registers a thread and shorter tiles): one piece at a
 // time, 37 mixed segments 39.2 us against 39.6.  `drained` runs once
-// the last values are in registers; repair(v, token) is for values that are no
-// finite numbers.
-template <bool TWO = true, class Drained, class Repair>
-__device__ __forceinline__ void drain(uint32_t taddr, int half, int ts, int64_t row0, int rows, int64_t n, float bias,
-                                      const Problem& p, uint32_t* turn, bool vec, Drained&& drained, Repair&& repair) {
+// the last values are in registers.  With CHECK the result is NaN where a value was
+// no finite number.
+template <bool TWO, bool CHECK, class Drained>
+__device__ __forceinline__ float drain(uint32_t taddr, int half, int ts, int64_t row0, int rows, int64_t n, float bias,
+                                      const Problem& p, uint32_t* turn, bool vec, Drained&& drained) {
     const int lane = threadIdx.x % 32, r = lane / 4, c8 = (lane % 4) * 8;
     const bool ob = p.out_dt == SGMV_BF16;
     const bool fast = vec && !p.add;
@@ -466,10 +520,11 @@ __device__ __forceinline__ void drain(uint32_t taddr, int half, int ts, int64_t 
     const int64_t step = 16 * p.H;
     uint32_t next[8], next2[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
     float v[8], u[8];
+    float z = 0.f;
     int c = half * 8;
     if (c >= rows) {
         drained();
-        return;
+        return z;
     }
     if (TWO && fast && rows >= 32) {
         tmem_ld8(taddr + (uint32_t)c, next);
@@ -488,8 +543,7 @@ __device__ __forceinline__ void drain(uint32_t taddr, int half, int ts, int64_t 
                 tmem_ld8(taddr + (uint32_t)c + 32, next);
                 if (c + 48 < rows) tmem_ld8(taddr + (uint32_t)c + 48, next2);
             } else drained();
-            repair(v, c);
-            repair(u, c + 16);
+            if (CHECK) z = no_numbers(u, no_numbers(v, z));
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -507,7 +561,7 @@ __device__ __forceinline__ void drain(uint32_t taddr, int half, int ts, int64_t 
             }
             if (!more) break;
         }
-        return;
+        return z;
     }
     tmem_ld8(taddr + (uint32_t)c, next);
 #pragma unroll 1
@@ -518,7 +572,7 @@ __device__ __forceinline__ void drain(uint32_t taddr, int half, int ts, int64_t 
         const bool more = c + 16 < rows;
         if (more) tmem_ld8(taddr + (uint32_t)c + 16, next);
         else drained();
-        repair(v, c);
+        if (CHECK) z = no_numbers(v, z);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += bias;
         if (fast) {
@@ -537,6 +591,7 @@ __device__ __forceinline__ void drain(uint32_t taddr, int half, int ts, int64_t 
         }
         if (!more) break;
     }
+    return z;
 }
 
 // The bf16 part of (a, b): hi = rounded(v), and v - hi left for the next part.  A
@@ -705,7 +760,8 @@ __device__ __forceinline__ int x_box(int rows, int room) {
 template <int CG, int LORA>
 __global__ void __launch_bounds__(LORA == LORA_FMA ? 512 : threads_of(CG, LORA), 1)
 gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtensorMap wmap,
-            const __grid_constant__ CUtensorMap bmap, const Problem p, const Geo g, const Lora lo) {
+            const __grid_constant__ CUtensorMap bmap, const __grid_constant__ Problem p, const Geo g,
+            const __grid_constant__ Lora lo) {
     constexpr int THREADS = threads_of(CG, LORA), LORA_WARPS = lora_warps(CG);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1241,17 +1297,17 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                 __syncwarp();
                 if (lane == 0 && id + 2 * ncl < total) mbar_arrive(smem_u32(&acc_empty[acc]));
             } else if (CG == 2 || csize == 1) {
-                drain<CG == 2 || LORA != LORA_MMA>(taddr, half, t.ts, t.row0, t.rows, col, bias, p, stage, g.out_vec, [&] {
-                          tc_fence_before();
-                          __syncwarp();
-                          if (lane == 0 && id + 2 * ncl < total) {   // somebody waits for it
-                              if (CG == 2) mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[acc]), 0));
-                              else mbar_arrive(smem_u32(&acc_empty[acc]));
-                          }
-                      }, [&](float (&v)[8], int c) {
-                          if (LORA != LORA_MMA) return;
-                          repair_outputs<8>(v, c, t.rows - c, t.row0, col, runs, first_run[t.tok], first_run[t.tok + 1], p, lo);
-                      });
+                const float z = drain<CG == 2 || LORA != LORA_MMA, LORA == LORA_MMA>(
+                    taddr, half, t.ts, t.row0, t.rows, col, bias, p, stage, g.out_vec, [&] {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0 && id + 2 * ncl < total) {   // somebody waits for it
+                            if (CG == 2) mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[acc]), 0));
+                            else mbar_arrive(smem_u32(&acc_empty[acc]));
+                        }
+                    });
+                if (LORA == LORA_MMA && __any_sync(0xffffffffu, z != 0.f))
+                    repair_outputs(half * 8, t.rows, t.row0, col, bias, runs, first_run[t.tok], first_run[t.tok + 1], p, lo);
             } else {
                 // Partial sums go to the CTA that owns the token, four tokens of a weight row
                 // (16 bytes) at a time: red[source][token / 4][weight row][token % 4].  The
@@ -1282,6 +1338,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                     if (!warp_wait_cluster(smem_u32(red_full), reds & 1, abort_flag, DEVERR_TIMEOUT_EPILOGUE)) break;
                     ++reds;
                     const float4* rp = reinterpret_cast<const float4*>(smem + g.off_red) + nl;
+                    float z = 0.f;
                     for (int j0 = half * 8; j0 < cnt; j0 += 16) {
                         float v[8];
 #pragma unroll
@@ -1303,13 +1360,14 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                                     v[j + 2] += f.z;
                                     v[j + 3] += f.w;
                                 }
-                        if (LORA == LORA_MMA)
-                            repair_outputs<8>(v, t0 + j0, cnt - j0, t.row0, col, runs, first_run[t.tok], first_run[t.tok + 1], p,
-                                              lo);
+                        if (LORA == LORA_MMA) z = no_numbers(v, z);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) v[j] += bias;
                         put8(v, (int64_t)t.row0 + t0 + j0, min(8, cnt - j0), col, p, stage, g.out_vec);
                     }
+                    if (LORA == LORA_MMA && __any_sync(0xffffffffu, z != 0.f))
+                        repair_outputs(t0 + half * 8, t0 + cnt, t.row0, col, bias, runs, first_run[t.tok], first_run[t.tok + 1],
+                                       p, lo);
                 }
                 __syncwarp();
                 if (lane < (int)csize && id + ncl < total) mbar_arrive_remote(map_to_rank(smem_u32(red_free), (uint32_t)lane));

@@ -180,3 +180,32 @@ def test_lora_turned_b_of_fewer_adapters_than_segments(adapters, R):
         out.fill_(float("nan"))
         run_lora(x, w, a, b, out, m, segs, 8, spare=spare)
         assert torch.equal(out, lora_ref(x, w, a, b, m, None, T).float())
+
+
+# ---------------------------------------------------------------- values that are no numbers
+
+@pytest.mark.parametrize("variant", [sg.VARIANT_AUTO, sg.VARIANT_TC_WIDE])
+@pytest.mark.parametrize("T,K,N,turned", [(700, 28672, 136, False), (700, 28672, 136, True), (60, 4100 * 2, 40, False), (2100, 1004, 777, False)])
+@pytest.mark.parametrize("dt,out_dt", [("f16", "f16"), ("bf16", "f32")])
+def test_lora_one_adapter_full_of_nan(variant, T, K, N, turned, dt, out_dt):
+    """A long prompt whose adapter's B is NaN from end to end, beside others in the same token tiles: the others come out
+    right, bias included, however long K is, and soon (the kernels' waits are limited to two seconds)."""
+    g = gen(141)
+    lens = [T // 7, T // 5, 1, T // 9, T // 3]
+    m, rows = meta(lens, [0, 1, 2, 1, 0], gaps=[1, 0, 3, 0, 2])
+    x = torch.zeros(rows + 5, (K + 7) // 8 * 8, dtype=DT[dt], device="cuda")[:, :K]
+    x.copy_(ints(g, (rows + 5, K), dt, 1))
+    w = ints(g, (K, (N + 7) // 8 * 8), dt, 1).t()[:N] if turned else torch.zeros(N, (K + 7) // 8 * 8, dtype=DT[dt], device="cuda")[:, :K]
+    if not turned:
+        w.copy_(ints(g, (N, K), dt, 1))
+    a, b, bias = ints(g, (3, 16, K), dt, 1) * (torch.rand(3, 16, K, generator=g) < 0.02).cuda(), ints(g, (3, N, 16), dt, 1), ints(g, (N,), dt, 9)
+    ref = lora_ref(x, w, a, b, m, bias, rows + 5).to(DT[out_dt])
+    b[1] = float("nan")
+    out = torch.zeros(rows + 5, N, dtype=DT[out_dt], device="cuda")
+    sg.set_variant(variant)
+    assert sg.lora_linear_plan(x, w, a, b, out, *m, 5, max(lens), bias=bias)[0] == sg.VARIANT_TC
+    run_lora(x, w, a, b, out, m, 5, max(lens), bias)
+    own = torch.zeros(rows + 5, dtype=torch.bool, device="cuda")
+    for s, n, e in zip(*[v.tolist() for v in m]):
+        own[s:s + n] |= e == 1
+    assert torch.equal(out[~own], ref[~own]) and torch.isnan(out[own]).all()
