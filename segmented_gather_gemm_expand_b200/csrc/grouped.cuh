@@ -1175,10 +1175,11 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                         const uint32_t idesc_t = instr_desc_mn(true, WT, cols), dt = d + (uint32_t)off;   // t and B in bf16
                         for (int32_t r0 = 0; ok && r0 < lo.R; r0 += t_ranks, ++m) {
                             const uint32_t buf = m % LORA_WARPS;
-                            if (!mbar_wait(smem_u32(&t_full[buf]), (m / LORA_WARPS) & 1, abort_flag, DEVERR_TIMEOUT_MMA)) {
-                                ok = false;
-                                break;
-                            }
+                            // a pair's second CTA writes its half of t (and splits its rows of B) itself
+                            const uint32_t tb = smem_u32(&t_full[buf]), tp = (m / LORA_WARPS) & 1;
+                            ok = CG == 2 ? mbar_wait_cluster(tb, tp, abort_flag, DEVERR_TIMEOUT_MMA)
+                                         : mbar_wait(tb, tp, abort_flag, DEVERR_TIMEOUT_MMA);
+                            if (!ok) break;
                             const uint64_t bd = smem_desc(smem_u32(smem + g.off_t + buf * g.t_bytes), 16, 1024, 2);
                             const int steps = (min(t_ranks, lo.R - r0) + 15) / 16;
                             for (int i = 0; i < n_runs; ++i) {

@@ -61,7 +61,30 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
-// The same wait executed by all 32 lanes; the outcome is made warp-uniform so
+// The same wait for an arrival with release semantics of another CTA of the
+// cluster: it acquires what that CTA wrote.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t err) {
+    const unsigned long long t0 = clock64();
+    while (true) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if (*abort_flag) return false;
+        if (clock64() - t0 > WAIT_LIMIT_CYCLES) {
+            *abort_flag = 1;
+            raise_device_error(err);
+            return false;
+        }
+    }
+}
+
+// mbar_wait executed by all 32 lanes; the outcome is made warp-uniform so
 // that no lane leaves a loop its neighbours stay in.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t err) {
     const bool ok = mbar_wait(bar, parity, abort_flag, err);
@@ -369,29 +392,10 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Bounded wait of a whole warp that also acquires what other CTAs of the
-// cluster released with their arrivals.
+// The cluster's form of the wait by a whole warp.
 __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                                   int32_t err) {
-    bool ok = false;
-    const unsigned long long t0 = clock64();
-    while (true) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        ok = done != 0;
-        if (ok || *abort_flag) break;
-        if (clock64() - t0 > WAIT_LIMIT_CYCLES) {
-            *abort_flag = 1;
-            raise_device_error(err);
-            break;
-        }
-    }
+    const bool ok = mbar_wait_cluster(bar, parity, abort_flag, err);
     return __all_sync(0xffffffffu, ok);
 }
 

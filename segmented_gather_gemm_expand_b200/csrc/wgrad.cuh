@@ -241,10 +241,11 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
                 for (int32_t b = exps[e].first; ok && b >= 0; b = segs[b].next) {
                     const int32_t rows = segs[b].rows;
                     for (int32_t r = 0; r < rows; r += BT) {
-                        if (!mbar_wait(smem_u32(&full[s]), phase, abort_flag, DEVERR_TIMEOUT_MMA)) {
-                            ok = false;
-                            break;
-                        }
+                        // a segment's end: the other CTA's warps have zeroed rows of this stage
+                        const bool zeroed = rows - r < BT && (rows - r) % 16 != 0;
+                        ok = zeroed ? mbar_wait_cluster(smem_u32(&full[s]), phase, abort_flag, DEVERR_TIMEOUT_MMA)
+                                    : mbar_wait(smem_u32(&full[s]), phase, abort_flag, DEVERR_TIMEOUT_MMA);
+                        if (!ok) break;
                         tc_fence_after();
                         const uint64_t ad = ad0 + s * (uint64_t)(STAGE >> 4), bd = bd0 + s * (uint64_t)(STAGE >> 4);
                         const int steps = (rows - r + 15) / 16;   // K steps that hold rows

@@ -209,3 +209,23 @@ def test_lora_one_adapter_full_of_nan(variant, T, K, N, turned, dt, out_dt):
     for s, n, e in zip(*[v.tolist() for v in m]):
         own[s:s + n] |= e == 1
     assert torch.equal(out[~own], ref[~own]) and torch.isnan(out[own]).all()
+
+
+# ---------------------------------------------------------------- what the two CTAs of a pair write for each other
+
+def test_ragged_ends_and_short_runs_many_times():
+    """Rows zeroed, and t written, by the pair's second CTA for the first one's MMAs: the same bits every time."""
+    g = gen(151)
+    lens = [1 + (37 * i) % 61 for i in range(64)]
+    m, T = meta(lens, [i % 5 for i in range(64)])
+    x, dy = ints(g, (T, 520), "bf16", 1), ints(g, (T, 264), "bf16", 1)
+    w, a, b = ints(g, (264, 520), "bf16", 1), ints(g, (5, 16, 520), "bf16", 1), ints(g, (5, 264, 16), "bf16", 1)
+    ref, rw = lora_ref(x, w, a, b, m, None, T).float(), torch.zeros(5, 264, 520, dtype=torch.float64, device="cuda")
+    for s, n, e in zip(*[v.tolist() for v in m]):
+        rw[e] += dy[s:s + n].double().T @ x[s:s + n].double()
+    out, dw = torch.zeros(T, 264, device="cuda"), torch.zeros(5, 264, 520, device="cuda")
+    sg.set_variant(sg.VARIANT_TC_WIDE)
+    for _ in range(100):
+        run_lora(x, w, a, b, out, m, 64, 61)
+        sg.sgmv_grouped_wgrad(dy, x, dw, *m, 64, 61)
+        assert torch.equal(out, ref) and torch.equal(dw, rw.float())
