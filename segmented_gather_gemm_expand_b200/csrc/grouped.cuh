@@ -763,6 +763,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
             const __grid_constant__ CUtensorMap bmap, const __grid_constant__ Problem p, const Geo g,
             const __grid_constant__ Lora lo) {
     constexpr int THREADS = threads_of(CG, LORA), LORA_WARPS = lora_warps(CG);
+    constexpr bool EARLY = LORA != LORA_NONE;   // producer and MMAs may run while the shrink still does
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ int s_abort;
@@ -915,7 +916,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                 const int32_t xr = t.row0 + (CG == 2 ? (int32_t)crank * hs : 0);
                 const int32_t n0 = t.n0 + (CG == 2 ? (int32_t)crank * WROWS : 0);
                 for (int32_t kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(smem_u32(&empty[s]), phase, abort_flag, DEVERR_TIMEOUT_PRODUCER)) {
+                    if (!mbar_wait<EARLY>(smem_u32(&empty[s]), phase, abort_flag, DEVERR_TIMEOUT_PRODUCER)) {
                         ok = false;
                         break;
                     }
@@ -960,14 +961,14 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                     }
                 }
                 if (LORA == LORA_MMA && ok && lora_here) {
-                    ok = mbar_wait(smem_u32(runs_ready), 0, abort_flag, DEVERR_TIMEOUT_PRODUCER);
+                    ok = mbar_wait<EARLY>(smem_u32(runs_ready), 0, abort_flag, DEVERR_TIMEOUT_PRODUCER);
                     const int32_t last = ok ? first_run[t.tok + 1] : 0;
                     const int per_step = runs_per_step<CG>(lo);
                     for (int32_t r = ok ? first_run[t.tok] : 0; ok && r < last; r += per_step) {
                         const int n_runs = CG == 2 ? min(per_step, last - r) : 1;
                         for (int32_t r0 = 0; ok && r0 < lo.R; r0 += t_ranks, ++m) {
                             for (int i = 0; i < n_runs; ++i) {
-                                if (!mbar_wait(smem_u32(&empty[s]), phase, abort_flag, DEVERR_TIMEOUT_PRODUCER)) {
+                                if (!mbar_wait<EARLY>(smem_u32(&empty[s]), phase, abort_flag, DEVERR_TIMEOUT_PRODUCER)) {
                                     ok = false;
                                     break;
                                 }
@@ -999,7 +1000,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
             }
             // the commits of the other CTA's MMAs arrive here: none may be under way when this CTA ends
             for (uint32_t i = 0; CG == 2 && ok && i < S; ++i) {
-                ok = mbar_wait(smem_u32(&empty[s]), phase, abort_flag, DEVERR_TIMEOUT_PRODUCER);
+                ok = mbar_wait<EARLY>(smem_u32(&empty[s]), phase, abort_flag, DEVERR_TIMEOUT_PRODUCER);
                 if (++s == S) {
                     s = 0;
                     phase ^= 1;
@@ -1141,10 +1142,10 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                 const uint32_t acc = n & 1;
                 const uint32_t idesc = instr_desc_mn(bf16, WT, t.ts) | (g.w_mn ? IDESC_A_MN : 0u);
                 const uint32_t d = tmem_base + acc * (uint32_t)g.acc_stride;
-                if (!mbar_wait(smem_u32(&acc_empty[acc]), ((n >> 1) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_MMA)) break;
+                if (!mbar_wait<EARLY>(smem_u32(&acc_empty[acc]), ((n >> 1) & 1) ^ 1, abort_flag, DEVERR_TIMEOUT_MMA)) break;
                 tc_fence_after();
                 for (int32_t kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(smem_u32(&full[s]), phase, abort_flag, DEVERR_TIMEOUT_MMA)) {
+                    if (!mbar_wait<EARLY>(smem_u32(&full[s]), phase, abort_flag, DEVERR_TIMEOUT_MMA)) {
                         ok = false;
                         break;
                     }
@@ -1164,7 +1165,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                     }
                 }
                 if (LORA == LORA_MMA && ok && lora_here) {
-                    ok = mbar_wait(smem_u32(runs_ready), 0, abort_flag, DEVERR_TIMEOUT_MMA);
+                    ok = mbar_wait<EARLY>(smem_u32(runs_ready), 0, abort_flag, DEVERR_TIMEOUT_MMA);
                     const uint64_t bk0 = smem_desc(smem_u32(smem), 16, 1024, 2);   // B's rows are K-major
                     const int32_t last = ok ? first_run[t.tok + 1] : 0;
                     const int per_step = runs_per_step<CG>(lo);
@@ -1177,13 +1178,13 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                             const uint32_t buf = m % LORA_WARPS;
                             // a pair's second CTA writes its half of t (and splits its rows of B) itself
                             const uint32_t tb = smem_u32(&t_full[buf]), tp = (m / LORA_WARPS) & 1;
-                            ok = CG == 2 ? mbar_wait_cluster(tb, tp, abort_flag, DEVERR_TIMEOUT_MMA)
-                                         : mbar_wait(tb, tp, abort_flag, DEVERR_TIMEOUT_MMA);
+                            ok = CG == 2 ? mbar_wait_cluster<EARLY>(tb, tp, abort_flag, DEVERR_TIMEOUT_MMA)
+                                         : mbar_wait<EARLY>(tb, tp, abort_flag, DEVERR_TIMEOUT_MMA);
                             if (!ok) break;
                             const uint64_t bd = smem_desc(smem_u32(smem + g.off_t + buf * g.t_bytes), 16, 1024, 2);
                             const int steps = (min(t_ranks, lo.R - r0) + 15) / 16;
                             for (int i = 0; i < n_runs; ++i) {
-                                if (!mbar_wait(smem_u32(&full[s]), phase, abort_flag, DEVERR_TIMEOUT_MMA)) {
+                                if (!mbar_wait<EARLY>(smem_u32(&full[s]), phase, abort_flag, DEVERR_TIMEOUT_MMA)) {
                                     ok = false;
                                     break;
                                 }

@@ -46,14 +46,24 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 }
 
 // Bounded wait.  Returns false (after raising `err`) if the phase did not
-// complete in time or another role of the CTA already gave up.
+// complete in time or another role of the CTA already gave up.  EARLY: the role
+// may have started before the preceding kernel was done, and other roles wait for
+// that; its limit counts from then on.
+template <bool EARLY = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t err) {
     if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = clock64();
+    unsigned long long t0 = clock64();
+    bool again = EARLY;
     while (true) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (clock64() - t0 > WAIT_LIMIT_CYCLES) {
+            if (again) {
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                again = false;
+                t0 = clock64();
+                continue;
+            }
             *abort_flag = 1;
             raise_device_error(err);
             return false;
@@ -63,8 +73,10 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 
 // The same wait for an arrival with release semantics of another CTA of the
 // cluster: it acquires what that CTA wrote.
+template <bool EARLY = false>
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t err) {
-    const unsigned long long t0 = clock64();
+    unsigned long long t0 = clock64();
+    bool again = EARLY;
     while (true) {
         uint32_t done;
         asm volatile(
@@ -77,6 +89,12 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
         if (done) return true;
         if (*abort_flag) return false;
         if (clock64() - t0 > WAIT_LIMIT_CYCLES) {
+            if (again) {
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                again = false;
+                t0 = clock64();
+                continue;
+            }
             *abort_flag = 1;
             raise_device_error(err);
             return false;

@@ -229,3 +229,22 @@ def test_ragged_ends_and_short_runs_many_times():
         run_lora(x, w, a, b, out, m, 64, 61)
         sg.sgmv_grouped_wgrad(dy, x, dw, *m, 64, 61)
         assert torch.equal(out, ref) and torch.equal(dw, rw.float())
+
+
+def test_lora_when_the_shrink_takes_longer_than_the_waits_limit():
+    """Single tokens in random order, so many that finding their adapters takes seconds: the projection's roles that start
+    before that is done wait for it, and their limits of two seconds count from then on."""
+    T, g = 800_000, gen(161)
+    x, w, a, b = ints(g, (T, 64), "bf16", 1), ints(g, (64, 64), "bf16", 1), ints(g, (7, 8, 64), "bf16", 1), ints(g, (7, 64, 8), "bf16", 1)
+    start, ids = torch.randperm(T, generator=g), torch.randint(-1, 7, (T,), generator=g)
+    m = [start.int().cuda(), torch.ones(T).int().cuda(), ids.int().cuda()]
+    out = torch.zeros(T, 64, device="cuda")
+    assert sg.lora_linear_plan(x, w, a, b, out, *m, T, 1)[0] == sg.VARIANT_TC
+    run_lora(x, w, a, b, out, m, T, 1)
+    row = torch.empty_like(ids)
+    row[start] = ids
+    ref = x.float() @ w.float().T          # whole numbers below 2^24: exact
+    for i in range(7):
+        at = (row == i).nonzero()[:, 0].cuda()
+        ref[at] += (x[at].float() @ a[i].float().T) @ b[i].float().T
+    assert torch.equal(out, ref)
