@@ -1380,6 +1380,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
     if (CG == 1 && csize > 1 && warp < 2) cluster_wait();   // the meeting at the start
     tc_fence_before();
     __syncthreads();
+    outlast_copies(abort_flag);
     if (csize > 1) cluster_sync();   // no CTA leaves while another may still signal it
     tc_fence_after();
     if (warp == 1) {

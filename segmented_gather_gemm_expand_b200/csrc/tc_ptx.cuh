@@ -417,6 +417,17 @@ __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity,
     return __all_sync(0xffffffffu, ok);
 }
 
+// At a kernel's end, by every thread, after the CTA's roles have met: where one of
+// them gave up, copies and MMAs that it had started may still be on their way into
+// this CTA's shared memory or TMEM.  They take microseconds; the CTA stays a
+// millisecond longer, then it leaves in any case.
+__device__ __forceinline__ void outlast_copies(const volatile int* abort_flag) {
+    if (!*abort_flag) return;
+    const unsigned long long t0 = clock64();
+    while (clock64() - t0 < 2000000ull) __nanosleep(1000);
+    __syncwarp();
+}
+
 // Stores 16 bytes into the shared memory of a CTA of the cluster and counts
 // them at that CTA's mbarrier; nothing else orders or waits for them.
 __device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t bar, float a, float b, float c, float d) {

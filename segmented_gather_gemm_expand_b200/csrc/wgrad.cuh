@@ -343,6 +343,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
 
     tc_fence_before();
     __syncthreads();
+    outlast_copies(abort_flag);
     cluster_sync();
     tc_fence_after();
     if (warp == 1) tmem_dealloc_pair(tmem_base, (uint32_t)g.tmem_cols);
