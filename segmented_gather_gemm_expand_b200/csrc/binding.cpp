@@ -117,8 +117,11 @@ PyObject* lora_linear(PyObject*, PyObject* const* args, Py_ssize_t n) {
     }
     const c10::cuda::CUDAGuard guard(device);
     void* stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+    // a launch waits where the stream's queue is full: other Python threads run meanwhile
+    Py_BEGIN_ALLOW_THREADS
     rc = g_lora(&d[0], &d[1], bias ? &d[2] : nullptr, &d[3], &d[4], &d[5], &d[6], &d[7], &d[8], batches, max_len, ws,
                 ws_bytes, stream);
+    Py_END_ALLOW_THREADS
     return PyLong_FromLong(rc);
     END_HANDLE_TH_ERRORS
 }
@@ -142,7 +145,9 @@ PyObject* grouped(GroupedFn fn, PyObject* const* args, Py_ssize_t n) {
     if (add < 0) return nullptr;
     const c10::cuda::CUDAGuard guard(device);
     void* stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+    Py_BEGIN_ALLOW_THREADS
     rc = fn(&d[0], &d[1], &d[2], &d[3], &d[4], &d[5], batches, max_len, add, stream);
+    Py_END_ALLOW_THREADS
     return PyLong_FromLong(rc);
     END_HANDLE_TH_ERRORS
 }
