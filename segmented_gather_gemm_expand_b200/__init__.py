@@ -51,7 +51,15 @@ _DTYPES = {torch.float16: _abi.F16, torch.bfloat16: _abi.BF16, torch.float32: _a
            torch.int32: _abi.I32, torch.int64: _abi.I64}
 
 _lib = _abi.load()
-_binding = _abi.load_binding(_lib)
+_calls = None
+
+
+def _large():
+    """The extension that calls the large products, loaded at the first of their calls: the others do without it."""
+    global _calls
+    if _calls is None:
+        _calls = _abi.load_binding(_lib)
+    return _calls
 
 
 class SgmvError(RuntimeError):
@@ -256,8 +264,9 @@ def sgmv_lora_linear(inputs, weight, lora_a_weights, lora_b_weights, output_tens
     """``output_tensor[r] = inputs[r] @ weight.T + bias + (inputs[r] @ A.T) @ B.T`` with the adapter (A, B) of row r's
     sequence; rows without one get the projection alone.  Every row is written.  ``workspace``: contiguous CUDA tensor
     of scratch of at least ``lora_linear_plan``'s first size (None only without adapters)."""
-    rc = _binding.lora_linear(inputs, weight, bias, lora_a_weights, lora_b_weights, output_tensor, b_seq_start_loc,
-                              seq_len_tensor, lora_indices_tensor, batches, max_seq_length, workspace)
+    rc = (_calls or _large()).lora_linear(inputs, weight, bias, lora_a_weights, lora_b_weights, output_tensor,
+                                          b_seq_start_loc, seq_len_tensor, lora_indices_tensor, batches, max_seq_length,
+                                          workspace)
     if rc != 0:
         raise SgmvError(rc, "sgmv_lora_linear")
     return output_tensor
@@ -287,8 +296,8 @@ def sgmv_grouped_gemm(inputs, weights, output_tensor, b_seq_start_loc, seq_len_t
     """``output_tensor[r] = inputs[r] @ weights[e].T`` (added to the old values when ``add_inputs``) for the rows of
     every segment with index e; other rows keep their bits.  ``weights`` is (E, N, K) with K or N contiguous: pass
     ``w.transpose(1, 2)`` for the input gradient."""
-    rc = _binding.grouped_gemm(inputs, weights, output_tensor, b_seq_start_loc, seq_len_tensor, group_indices_tensor,
-                               batches, max_seq_length, add_inputs)
+    rc = (_calls or _large()).grouped_gemm(inputs, weights, output_tensor, b_seq_start_loc, seq_len_tensor,
+                                           group_indices_tensor, batches, max_seq_length, add_inputs)
     if rc != 0:
         raise SgmvError(rc, "sgmv_grouped_gemm")
     return output_tensor
@@ -298,8 +307,8 @@ def sgmv_grouped_wgrad(grad_output, inputs, grad_weights, b_seq_start_loc, seq_l
                        batches, max_seq_length, add_inputs=False):
     """``grad_weights[e] = grad_output[rows of e].T @ inputs[rows of e]`` (added to the old values when
     ``add_inputs``) for every index e; an index without rows gets zeros (keeps its values when ``add_inputs``)."""
-    rc = _binding.grouped_wgrad(grad_output, inputs, grad_weights, b_seq_start_loc, seq_len_tensor,
-                                group_indices_tensor, batches, max_seq_length, add_inputs)
+    rc = (_calls or _large()).grouped_wgrad(grad_output, inputs, grad_weights, b_seq_start_loc, seq_len_tensor,
+                                            group_indices_tensor, batches, max_seq_length, add_inputs)
     if rc != 0:
         raise SgmvError(rc, "sgmv_grouped_wgrad")
     return grad_weights

@@ -110,11 +110,15 @@ def load():
 
 def load_binding(lib):
     """The extension that calls the large products (built beside the library), bound to lib's functions."""
+    from .build import binding_target
     try:
         from . import _binding
     except ImportError as e:
         raise ImportError("_binding.so not found or not loadable; build it with "
                           "`python segmented_gather_gemm_expand_b200/build.py`") from e
+    if _binding.built_for != binding_target():
+        raise ImportError(f"_binding.so was built for {_binding.built_for}, this is {binding_target()}; build it again with "
+                          "`python segmented_gather_gemm_expand_b200/build.py`")
     address = [ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
                for n in ("sgmv_lora_linear", "sgmv_grouped_gemm", "sgmv_grouped_wgrad")]
     _binding.init(*address)

@@ -27,17 +27,33 @@ def sources():
                   [os.path.join(INCLUDE, "sgmv.h")])
 
 
+def binding_target() -> str:
+    """The Python and torch that the extension is compiled for; it holds this text as `built_for`."""
+    import torch
+    return f"python {sys.version_info.major}.{sys.version_info.minor}, torch {torch.__version__}"
+
+
+def binding_is_current() -> bool:
+    if not os.path.exists(BINDING):
+        return False
+    if os.path.getmtime(BINDING) < max(os.path.getmtime(s) for s in (os.path.join(CSRC, "binding.cpp"),
+                                                                     os.path.join(INCLUDE, "sgmv.h"))):
+        return False
+    with open(BINDING, "rb") as f:
+        return binding_target().encode() + b"\0" in f.read()
+
+
 def build_binding(force: bool = False) -> str:
     src = os.path.join(CSRC, "binding.cpp")
-    if not force and os.path.exists(BINDING):
-        if os.path.getmtime(BINDING) >= max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "sgmv.h"))):
-            return BINDING
+    if not force and binding_is_current():
+        return BINDING
     import sysconfig
 
     import torch
     root = os.path.dirname(torch.__file__)
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DBUILT_FOR="{binding_target()}"',
+           "-I", INCLUDE,
            "-isystem", os.path.join(root, "include"),
            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], "-isystem", "/usr/local/cuda/include",
