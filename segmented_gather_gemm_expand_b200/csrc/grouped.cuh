@@ -500,15 +500,13 @@ __device__ __forceinline__ void repair_outputs(int first_tok, int end_tok, int64
 
 // A warp's share of a tile from TMEM to memory: 8 of every 16 columns (tokens),
 // from 8 * half on, two such pieces in turn, the next ones under way while these
-// are stored (one piece at a time: 113 us instead of 104 for the weight gradient
-// of 16 experts, whose tiles are short; the conversions and copies of a piece
+// are stored (one piece at a time: 113 us instead of 104, on one GPU, for the weight
+// gradient of 16 experts, whose tiles are short; the conversions and copies of a piece
 // wait for one another).  Short loops on purpose: straight-line code for 32 tokens
-// at a time spent its time fetching instructions.  TWO false (single CTAs with
-// LORA_MMA, which have fewer registers a thread and shorter tiles): one piece at a
-// time, 37 mixed segments 39.2 us against 39.6.  `drained` runs once
-// the last values are in registers.  With CHECK the result is NaN where a value was
-// no finite number.
-template <bool TWO, bool CHECK, class Drained>
+// at a time spent its time fetching instructions.  `drained` runs once the last
+// values are in registers.  With CHECK the result is NaN where a value was no
+// finite number.
+template <bool CHECK, class Drained>
 __device__ __forceinline__ float drain(uint32_t taddr, int half, int ts, int64_t row0, int rows, int64_t n, float bias,
                                       const Problem& p, uint32_t* turn, bool vec, Drained&& drained) {
     const int lane = threadIdx.x % 32, r = lane / 4, c8 = (lane % 4) * 8;
@@ -526,7 +524,7 @@ __device__ __forceinline__ float drain(uint32_t taddr, int half, int ts, int64_t
         drained();
         return z;
     }
-    if (TWO && fast && rows >= 32) {
+    if (fast && rows >= 32) {
         tmem_ld8(taddr + (uint32_t)c, next);
         if (c + 16 < rows) tmem_ld8(taddr + (uint32_t)c + 16, next2);
 #pragma unroll 1
@@ -1299,7 +1297,7 @@ gemm_kernel(const __grid_constant__ XMaps xmaps, const __grid_constant__ CUtenso
                 __syncwarp();
                 if (lane == 0 && id + 2 * ncl < total) mbar_arrive(smem_u32(&acc_empty[acc]));
             } else if (CG == 2 || csize == 1) {
-                const float z = drain<CG == 2 || LORA != LORA_MMA, LORA == LORA_MMA>(
+                const float z = drain<LORA == LORA_MMA>(
                     taddr, half, t.ts, t.row0, t.rows, col, bias, p, stage, g.out_vec, [&] {
                         tc_fence_before();
                         __syncwarp();

@@ -319,7 +319,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
             };
             const int64_t row0 = (int64_t)e * g.rows_per_group + n0;
             if (any) {
-                grp::drain<true, false>(taddr, half, g.ts, row0, valid, col, 0.f, p, stage, g.out_vec, drained);
+                grp::drain<false>(taddr, half, g.ts, row0, valid, col, 0.f, p, stage, g.out_vec, drained);
             } else {
                 drained();
                 if (g.out_vec && !p.add) {
