@@ -461,10 +461,15 @@ namespace {
 // rank 64, 512 single rows 51, 102; 512 in fours 60, 37; 300 in 16s 33, 21.
 bool row_shrink_pays(int64_t rows, int64_t segs, int64_t ranks) { return rows * ranks <= 4096 + 100 * segs; }
 // Rows per segment from which the low-rank part runs on the tensor cores: a step
-// per run against a copy of B per token.  Measured (us, on the CUDA cores
-// against the tensor cores): 240 rows in 24 segments 29.8, 32.5; 946 in 232
-// 43.7, 30.9; 512 in 256 85, 103.
-constexpr int64_t mma_run_rows(int64_t rows) { return rows > 256 ? 4 : 16; }
+// per run against a copy of B per token; an fp16 B, which a step splits first, is
+// worth it later, unless the copies are no whole rows (`ring` false: B read lane by
+// lane).  Measured (us, 4096 -> 4096, rank 16, tensor cores against CUDA cores; bf16,
+// fp16): 240 rows in 24 segments 29.8, 33.8 against 29.2; 256 in 16 28.2, 31.0 against
+// 29.3; 512 in pairs 71, 84 against 52; in fours 51, 59 against 51; in sixes 46.6,
+// 51.7 against 50.9; in eights 43.8, 46.6 against 50.8; rank 64, in fours 81, 96 against 89.
+constexpr int64_t mma_run_rows(int64_t rows, bool f16, bool ring) {
+    return (rows > 256 ? 4 : 16) * (f16 && ring ? 3 : 2) / 2;
+}
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
@@ -708,7 +713,8 @@ int choose_lora(LoraCall* c, const DeviceInfo& dev, int forced, char* ws, size_t
     }
     const bool tc = forced != SGMV_VARIANT_SIMT && dev.cc_major == 10;
     // K steps pay from a few rows per segment on: a run costs an MMA over its whole token tile
-    const bool long_runs = c->rows >= mma_run_rows(c->rows) * c->shrink.batches;
+    const bool long_runs =
+        c->rows >= mma_run_rows(c->rows, c->base.w_dt == SGMV_F16, grp::ring_ok(c->lo)) * c->shrink.batches;
     bool mma = tc && c->low_rank && long_runs && c->shrink.batches <= grp::SEG_CAP;
     grp::Lora packed = c->lo;
     int64_t pack_bytes = 0;
