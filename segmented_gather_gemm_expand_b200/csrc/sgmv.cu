@@ -464,12 +464,11 @@ bool row_shrink_pays(int64_t rows, int64_t segs, int64_t ranks) { return rows * 
 // per run against a copy of B per token; an fp16 B, which a step splits first, is
 // worth it later, unless the copies are no whole rows (`ring` false: B read lane by
 // lane).  Measured (us, 4096 -> 4096, rank 16, tensor cores against CUDA cores; bf16,
-// fp16): 240 rows in 24 segments 29.8, 33.8 against 29.2; 256 in 16 28.2, 31.0 against
-// 29.3; 512 in pairs 71, 84 against 52; in fours 51, 59 against 51; in sixes 46.6,
-// 51.7 against 50.9; in eights 43.8, 46.6 against 50.8; rank 64, in fours 81, 96 against 89.
-constexpr int64_t mma_run_rows(int64_t rows, bool f16, bool ring) {
-    return (rows > 256 ? 4 : 16) * (f16 && ring ? 3 : 2) / 2;
-}
+// fp16): 240 rows in 24 segments 29.8, 33.8 against 29.2; 256 in 16 28.2, 30.8 against
+// 29.3 (rank 64: 35.0 in fp16 against 45.8); 512 in pairs 71, 84 against 52; in fours 51, 58
+// against 51; in fives 49, 54 against 52; in eights 43.8, 46.6 against 50.8; rank 64, in
+// fours 81, 96 against 89; in fives 74, 88 against 91.
+constexpr int64_t mma_run_rows(int64_t rows, bool f16, bool ring) { return rows > 256 ? (f16 && ring ? 5 : 4) : 16; }
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
