@@ -248,3 +248,35 @@ def test_lora_when_the_shrink_takes_longer_than_the_waits_limit():
         at = (row == i).nonzero()[:, 0].cuda()
         ref[at] += (x[at].float() @ a[i].float().T) @ b[i].float().T
     assert torch.equal(out, ref)
+
+
+# ---------------------------------------------------------------- gradients of adapters from half t
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("R,K,N", [(16, 264, 136), (64, 136, 200), (8, 128, 96)])
+@pytest.mark.parametrize("out_dt,add", [("f32", True), (None, False)])
+def test_adapters_gradients_from_half_t(dt, R, K, N, out_dt, add):
+    """dA and dB with t and dt as sgmv_shrink writes them in the weights' type: the tensor-core form, both short sides."""
+    g = gen(171 + R)
+    lens, A = [90, 40, 0, 33, 130, 1, 1, 17], 5
+    m, T = meta(lens, [1, 0, 2, 1, 3, -1, 0, 2], gaps=[i % 3 for i in range(8)])
+    sparse = lambda v: v * (torch.rand(v.shape, generator=g) < 0.2).to(v.device)   # sums below 128: whole in bf16
+    x, dy = sparse(ints(g, (T, K), dt, 1)), sparse(ints(g, (T, N), dt, 1))
+    a, b = ints(g, (A, R, K), dt, 1), ints(g, (A, N, R), dt, 1)
+    t, s = torch.zeros(T, R, device="cuda", dtype=DT[dt]), torch.zeros(T, R, device="cuda", dtype=DT[dt])   # x A^T, dY B
+    sg.sgmv_shrink(x, a, t, *m, 8, 130)
+    sg.sgmv_shrink(dy, b.transpose(1, 2), s, *m, 8, 130)
+    od = DT[out_dt or dt]
+    da, db = ints(g, (A, R, K), "f32", 9).to(od), ints(g, (A, N, R), "f32", 9).to(od)
+    ra, rb = (da.double(), db.double()) if add else (torch.zeros_like(da).double(), torch.zeros_like(db).double())
+    for lo, n, i in zip(*[v.tolist() for v in m]):
+        if i < 0:
+            continue
+        xd, yd = x[lo:lo + n].double(), dy[lo:lo + n].double()
+        ra[i] += (yd @ b[i].double()).T @ xd
+        rb[i] += yd.T @ (xd @ a[i].double().T)
+    for y, z, grad in ((s, x, da), (dy, t, db)):
+        assert sg.grouped_wgrad_plan(y, z, grad, *m, 8, 130, add) == sg.VARIANT_TC
+        sg.sgmv_grouped_wgrad(y, z, grad, *m, 8, 130, add)
+    assert t.abs().max() < 256 and s.abs().max() < 256      # whole numbers in bf16
+    assert torch.equal(da, ra.to(od)) and torch.equal(db, rb.to(od))
