@@ -317,9 +317,15 @@ SGMV_API int bgmv_plan(const sgmv_tensor* inputs, const sgmv_tensor* lora_b, con
  *
  * for EVERY row r < min(T_x, T_out); a is the adapter of the segment that holds
  * row r, and rows of no segment, or of one whose adapter is outside
- * [0, lora_num), get the projection and the bias alone.  t is kept in fp32 and
- * not rounded; all sums are in fp32, and out is rounded once.  (Shrink, a
- * library GEMM and expand in add mode give the same up to two more roundings.)
+ * [0, lora_num), get the projection and the bias alone.  t is a sum in fp32 and
+ * kept so; all sums are in fp32, and out is rounded once.  (Shrink, a library
+ * GEMM and expand in add mode give the same up to two more roundings.)  Where
+ * the low-rank part runs on the tensor cores (segments of a few rows and more),
+ * t enters it as a sum of bf16 parts: two for a half out, which hold t to 2^-17
+ * of itself (out's own rounding is 2^-8 in bf16, 2^-11 in fp16), three for an
+ * fp32 out, which hold it whole; t has fp32's range in either case.  A value of
+ * a request (its rows, its adapter) that is no finite number reaches that
+ * request's rows alone.
  * out is overwritten; rows past min(T_x, T_out) keep their bits.  Segments must
  * not overlap.
  *
@@ -338,7 +344,8 @@ SGMV_API int bgmv_plan(const sgmv_tensor* inputs, const sgmv_tensor* lora_b, con
  *             SGMV_ERR_WORKSPACE; with the preferred size the sums of t may be
  *             split over more CTAs, and a lora_b whose rows are not contiguous
  *             on 16-byte boundaries is laid out anew for segments of some
- *             length.  NULL will do for a call without adapters
+ *             length (a copy per adapter or per segment, whichever are
+ *             fewer).  NULL will do for a call without adapters
  *             (batches, lora_num or R zero).  Calls that run at the same time
  *             need separate workspaces, and so do captured graphs that may.
  *
@@ -409,7 +416,9 @@ SGMV_API int sgmv_grouped_gemm_plan(const sgmv_tensor* inputs, const sgmv_tensor
  *
  * for EVERY e < E: without add_inputs an index that no row has gets zeros; with
  * it, it keeps its bits.  Of sgmv_grouped_gemm it is the gradient by the
- * weights; with X = t it is that of lora_b, with dY = dt that of lora_a.
+ * weights; with X = t it is that of lora_b, with dY = dt that of lora_a.  (Let
+ * sgmv_shrink write t and dt in the other operand's half type: in fp32 they
+ * leave the call to the generic kernel, since the tensor-core path takes one type.)
  *
  *   grad_out      (T_y, N)     f16 | bf16 | f32, any strides
  *   inputs        (T_x, K)     f16 | bf16 | f32, any strides

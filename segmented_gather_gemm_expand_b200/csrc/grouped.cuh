@@ -25,8 +25,8 @@
 //   pair   CTA pairs (cta_group::2), 256 weight rows x up to 256 tokens.  Each
 //          CTA loads its 128 weight rows and half of the tokens, so a stage
 //          brings 64 MMA columns per KB instead of 43: compute-bound shapes.
-//          16384 ragged rows over 8 experts, 4096 -> 11008, bf16: 1023 us in a
-//          single launch (1445 TFLOP/s), the tensor pipe 95 % busy at the 1.34 GHz
+//          16384 ragged rows over 8 experts, 4096 -> 11008, bf16: 1010-1023 us in a
+//          single launch (1450 TFLOP/s), the tensor pipe 94 % busy at the 1.34-1.39 GHz
 //          that the power limit leaves; 1200 us back to back.  Bound: power.
 //   single one CTA, 128 weight rows x up to 128 tokens; with few tiles, the
 //          CTAs of a cluster share one tile by cutting K, push their partial
@@ -50,9 +50,9 @@
 //          exactly: the warps that write t split its tiles in shared memory (37 mixed
 //          segments of rank 24, fp16, 42.7 -> 44.7 us; 4520 rows of 118, 3680 -> 11867,
 //          rank 64, 595 -> 617).
-//          8764 rows of 16
-//          prompts, 4096 -> 12288, rank 16: 1483 us with FMAs in the epilogue, 710
-//          with these steps (the kernel alone 589, the tensor pipe 90 % busy; power).
+//          8764 rows of 16 prompts, 4096 -> 12288, rank 16: 1483 us with FMAs in the
+//          epilogue, 690-720 with these steps (the kernel alone 574, the tensor pipe
+//          91 % busy; power).
 //          A B that TMA cannot read (a transposed view: the input gradient; ranks
 //          that leave rows off the 16-byte boundaries) is laid out anew, per
 //          segment or per adapter, where the workspace has room.

@@ -21,10 +21,10 @@
 //
 // Measured: 16384 ragged rows of 8 experts, 4096 x 11008, bf16: 1200-1250 us
 // back to back (1200 TFLOP/s, the power limit).  8192 rows of 16 experts, 2048 x
-// 2816: 104-120 us by box, where the flops alone would take 57: 89 us with no
-// epilogue at all (8 K steps per tile on average; the longest cluster has 20 %
-// more than the mean), 15 more for the stores, which share the shared memory's
-// bandwidth with the MMAs' operands and TMA's writes.  18 indexes of 888 x 1528 of
+// 2816: 118-124 us by GPU, where the flops alone would take 57.  In an earlier build of
+// 104 us on one GPU, 89 were left with no epilogue at all (8 K steps per tile on
+// average; the longest cluster has 20 % more than the mean); the other 15 were the
+// stores, which share the shared memory's bandwidth with the MMAs' operands and TMA's writes.  18 indexes of 888 x 1528 of
 // which one has rows: 22 us, of which the zeros are most (36 by way of the
 // epilogue's 64-byte pieces).
 #pragma once
