@@ -56,17 +56,15 @@ struct Segment {
     int64_t adapter;
 };
 
-// Rows of the `len` from `start` on that lie below lim: none for a negative start
-// or length.  start + len need not have a 64-bit value, so it is never formed.
-__host__ __device__ __forceinline__ int64_t clip_rows(int64_t start, int64_t len, int64_t lim) {
-    if (start < 0 || start >= lim || len <= 0) return 0;
-    return len < lim - start ? len : lim - start;
-}
-
-// The guards, for every kernel that reads segments.
+// The guards, for every kernel that reads segments: the `len` rows from `start` on
+// that lie below lim, none for a negative start or length or an adapter out of
+// range.  start + len may be more than 63 bits hold: it is an unsigned number here.
 __host__ __device__ __forceinline__ Segment guard_segment(int64_t start, int64_t len, int64_t adapter, int64_t lim,
                                                           int64_t adapters) {
-    return Segment{start, adapter >= 0 && adapter < adapters ? clip_rows(start, len, lim) : 0, adapter};
+    const uint64_t past = (uint64_t)start + (uint64_t)len;
+    const int64_t end = past > (uint64_t)lim ? lim : (int64_t)past;
+    const bool ok = adapter >= 0 && adapter < adapters && start >= 0 && len > 0 && end > start;
+    return Segment{start, ok ? end - start : 0, adapter};
 }
 
 __device__ __forceinline__ Segment load_segment(const Problem& p, int64_t b) {
